@@ -281,6 +281,63 @@ oscar_status oscar_calibrate_layer(const void* q, const void* k, const void* v, 
                                    float* clip_K, float* clip_V, double* covariances, void* workspace,
                                    size_t ws_bytes, void* stream);
 
+/* Rotary positions (RoPE) on queries and keys, before the append and the decode.  Pair i of
+ * a row at position p turns by the angle p f_i, (a, b) -> magnitude (a cos - b sin, b cos +
+ * a sin); channels from rotary_dim on pass through.  The pairs are channels (i, i +
+ * rotary_dim / 2), or (2 i, 2 i + 1) with OSCAR_ROPE_INTERLEAVED.  With
+ * OSCAR_ROPE_TRANSPOSE the angles are negated: the transposed map, which takes the
+ * gradient of the outputs to that of the inputs.
+ *
+ * oscar_rope_steps computes the table of a configuration [host]: steps [rotary_dim / 2],
+ * entry i = f_i / (2 pi) turns a position as a 64-bit fixed-point fraction of a turn
+ * (p * steps[i] modulo 2^64 is the phase: every 64-bit position keeps its precision), and
+ * *magnitude.  f_i = base^(-2 i / rotary_dim), scaled for contexts longer than the model's
+ * original_context by
+ *   OSCAR_ROPE_LINEAR  f_i / factor;
+ *   OSCAR_ROPE_BANDS   by the turns n_i = original_context f_i / (2 pi): f_i where n_i >= high,
+ *                      f_i / factor where n_i <= low, linear in n_i between (low < high);
+ *   OSCAR_ROPE_YARN    by the pair's index (YaRN): with x(n) = rotary_dim ln(original_context /
+ *                      (2 pi n)) / (2 ln base), f_i up to floor(x(high)), f_i / factor from
+ *                      ceil(x(low)), linear in i between (both held to [0, rotary_dim - 1]);
+ *                      magnitude = 0.1 ln(factor) + 1.
+ * rotary_dim even in [2, 512], base > 1, factor > 0 (>= 1 for YARN), 0 < low < high. */
+#define OSCAR_ROPE_UNSCALED 0
+#define OSCAR_ROPE_LINEAR 1
+#define OSCAR_ROPE_BANDS 2
+#define OSCAR_ROPE_YARN 3
+typedef struct {
+  int rotary_dim;
+  int scaling; /* OSCAR_ROPE_UNSCALED, _LINEAR, _BANDS or _YARN; the fields below as it needs them */
+  double base, factor, low, high, original_context;
+} oscar_rope_config;
+oscar_status oscar_rope_steps(const oscar_rope_config* cfg, uint64_t* steps, float* magnitude);
+
+/* One tensor of a call: rows x n_heads x head_dim channels [dev], channels contiguous, the
+ * strides in elements (inputs: any >= 0; outputs: rows and heads that do not overlap).
+ * Elementwise: out may be in, with the same strides; any other overlap of a call's outputs
+ * with its inputs or outputs is not allowed. */
+typedef struct {
+  const void* in;
+  void* out;
+  int n_heads;
+  long long in_row, in_head, out_row, out_head;
+} oscar_rope_tensor;
+
+/* Turn tensors[0 .. n_tensors - 1] (1 or 2: queries and keys of the same rows and dtype) by
+ * the table `steps` [dev] uint64 [rotary_dim / 2] and `magnitude`.  positions [dev]: int32
+ * [n_rows], or int64 with OSCAR_ROPE_POSITIONS64; any values, in any order.  head_dim in
+ * [rotary_dim, 512].  Products and sums in fp32, one rounding to dtype.  n_rows = 0 launches
+ * nothing.  Everything must belong to the current device. */
+#define OSCAR_DTYPE_BF16 0
+#define OSCAR_DTYPE_F16 1
+#define OSCAR_DTYPE_F32 2
+#define OSCAR_ROPE_INTERLEAVED 0x1u
+#define OSCAR_ROPE_TRANSPOSE 0x2u
+#define OSCAR_ROPE_POSITIONS64 0x4u
+oscar_status oscar_rope(const oscar_rope_tensor* tensors, int n_tensors, const uint64_t* steps, int head_dim,
+                        int rotary_dim, float magnitude, int dtype, uint32_t flags, const void* positions,
+                        long long n_rows, void* stream);
+
 /* Bounded waits: a work item of oscar_append_decode_attention that waits for the append
  * tasks it depends on gives up after `counter_polls` polls of their counter (each poll
  * sleeps about 0.1 us; 0 restores the default of 2^22 polls, about a second), sets

@@ -2,10 +2,11 @@
 
 The compute lives in liboscar.so (hand-written CUDA behind the C ABI of include/oscar.h);
 this package is a ctypes binding (_native), a torch-facing cache handle (cache), the
-offline calibration step (calibrate) and seeded synthetic workloads (workloads).
+offline calibration step (calibrate), rotary positions (rotary) and seeded synthetic workloads (workloads).
 """
 from . import _native
 from ._native import OSCAR_FORMAT_BF16, OSCAR_FORMAT_INT2, OSCAR_FORMAT_INT2_CM, OscarError
 from .cache import KVCache
+from .rotary import RotaryEmbedding
 
-__all__ = ["KVCache", "OscarError", "OSCAR_FORMAT_INT2", "OSCAR_FORMAT_INT2_CM", "OSCAR_FORMAT_BF16", "_native"]
+__all__ = ["KVCache", "RotaryEmbedding", "OscarError", "OSCAR_FORMAT_INT2", "OSCAR_FORMAT_INT2_CM", "OSCAR_FORMAT_BF16", "_native"]

@@ -38,6 +38,16 @@ class oscar_config(ctypes.Structure):
                                             "max_pages_per_request")]
 
 
+class oscar_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "low", "high", "original_context")]
+
+
+class oscar_rope_tensor(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n_heads", ctypes.c_int)] + [
+        (n, ctypes.c_longlong) for n in ("in_row", "in_head", "out_row", "out_head")]
+
+
 class oscar_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("codes", "sz", "sink", "ring", "bf16_pages", "codes_page_bytes",
                                                "sz_page_bytes", "bf16_page_bytes", "sink_bytes_per_head",
@@ -52,6 +62,7 @@ EXPORTS = [
     "oscar_decode_workspace_max_bytes", "oscar_plan_info",
     "oscar_decode_attention", "oscar_append_decode_attention", "oscar_decode_attention_noalloc", "oscar_bf16_append",
     "oscar_bf16_decode_attention", "oscar_calibration_workspace_bytes", "oscar_calibrate_layer",
+    "oscar_rope_steps", "oscar_rope",
     "oscar_set_wait_limit", "oscar_inject_fault", "oscar_get_status",
     "oscar_last_error", "oscar_last_launch_count",
 ]
@@ -98,6 +109,10 @@ def lib() -> ctypes.CDLL:
                 "oscar_bf16_decode_attention": (I, [P, I, P, P, P, S, P, P]),
                 "oscar_calibration_workspace_bytes": (S, [I, I, I]),
                 "oscar_calibrate_layer": (I, [P, P, P, I, I, I, ctypes.c_longlong, I, P, P, P, P, P, P, S, P]),
+                "oscar_rope_steps": (I, [ctypes.POINTER(oscar_rope_config), ctypes.POINTER(ctypes.c_uint64),
+                                         ctypes.POINTER(ctypes.c_float)]),
+                "oscar_rope": (I, [ctypes.POINTER(oscar_rope_tensor), I, P, I, I, ctypes.c_float, I, ctypes.c_uint32, P,
+                                   ctypes.c_longlong, P]),
                 "oscar_set_wait_limit": (I, [P, ctypes.c_uint32]),
                 "oscar_inject_fault": (I, [P, ctypes.c_uint32]),
                 "oscar_get_status": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -310,3 +325,34 @@ def oscar_calibrate_layer(q, k, v, clip_rank: int, rotation: int, R_K, R_V, clip
                                        _ptr(R_K), _ptr(R_V), _ptr(clip_K), _ptr(clip_V), _ptr(covariances),
                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream(stream)))
+
+
+OSCAR_ROPE_UNSCALED = 0
+OSCAR_ROPE_LINEAR = 1
+OSCAR_ROPE_BANDS = 2
+OSCAR_ROPE_YARN = 3
+OSCAR_DTYPE_BF16 = 0
+OSCAR_DTYPE_F16 = 1
+OSCAR_DTYPE_F32 = 2
+OSCAR_ROPE_INTERLEAVED = 0x1
+OSCAR_ROPE_TRANSPOSE = 0x2
+OSCAR_ROPE_POSITIONS64 = 0x4
+
+
+def oscar_rope_steps(cfg: oscar_rope_config):
+    """(steps, magnitude): the phase steps of every pair (Python ints, 2^-64 turns a position)
+    and the factor on the rotated channels."""
+    steps = (ctypes.c_uint64 * max(1, cfg.rotary_dim // 2))()
+    magnitude = ctypes.c_float()
+    _check(lib().oscar_rope_steps(ctypes.byref(cfg), steps, ctypes.byref(magnitude)))
+    return list(steps), magnitude.value
+
+
+def oscar_rope(tensors, steps, head_dim: int, rotary_dim: int, magnitude: float, dtype: int, flags: int, positions,
+               stream=None) -> None:
+    """tensors: one or two (input, output) pairs of [rows, heads, head_dim] device tensors."""
+    arr = (oscar_rope_tensor * max(1, len(tensors)))()
+    for i, (x, y) in enumerate(tensors):
+        arr[i] = oscar_rope_tensor(_ptr(x), _ptr(y), x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+    _check(lib().oscar_rope(arr, len(tensors), _ptr(steps), head_dim, rotary_dim, magnitude, dtype, flags,
+                            _ptr(positions), positions.shape[0], _stream(stream)))

@@ -1014,6 +1014,105 @@ oscar_status oscar_calibrate_layer(const void* q, const void* k, const void* v, 
   return OSCAR_OK;
 }
 
+oscar_status oscar_rope_steps(const oscar_rope_config* cfg, uint64_t* steps, float* magnitude) {
+  if (!cfg || !steps || !magnitude) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+  const int R = cfg->rotary_dim;
+  if (R < 2 || R > 512 || R % 2) return fail(OSCAR_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, 512]", R);
+  if (!(cfg->base > 1.0) || !std::isfinite(cfg->base)) return fail(OSCAR_ERR_INVALID_ARG, "base must be > 1");
+  if (cfg->scaling < OSCAR_ROPE_UNSCALED || cfg->scaling > OSCAR_ROPE_YARN)
+    return fail(OSCAR_ERR_INVALID_ARG, "unknown scaling %d", cfg->scaling);
+  const bool banded = cfg->scaling == OSCAR_ROPE_BANDS || cfg->scaling == OSCAR_ROPE_YARN;
+  if (cfg->scaling != OSCAR_ROPE_UNSCALED &&
+      (!(cfg->factor > 0.0) || !std::isfinite(cfg->factor) || (cfg->scaling == OSCAR_ROPE_YARN && cfg->factor < 1.0)))
+    return fail(OSCAR_ERR_INVALID_ARG, "factor %g out of range", cfg->factor);
+  if (banded && (!(cfg->low > 0.0) || !(cfg->high > cfg->low) || !std::isfinite(cfg->high) ||
+                 !(cfg->original_context > 0.0) || !std::isfinite(cfg->original_context)))
+    return fail(OSCAR_ERR_INVALID_ARG, "scaling needs 0 < low < high and original_context > 0");
+  const double two_pi = 6.283185307179586476925;
+  double x0 = 0.0, x1 = 0.0;
+  if (cfg->scaling == OSCAR_ROPE_YARN) {
+    auto index = [&](double n) {
+      return R * std::log(cfg->original_context / (two_pi * n)) / (2.0 * std::log(cfg->base));
+    };
+    x0 = std::min(std::max(std::floor(index(cfg->high)), 0.0), R - 1.0);
+    x1 = std::min(std::max(std::ceil(index(cfg->low)), 0.0), R - 1.0);
+  }
+  for (int i = 0; i < R / 2; ++i) {
+    double f = std::pow(cfg->base, -2.0 * i / R);
+    double keep = 1.0;  // share of the unscaled frequency
+    if (cfg->scaling == OSCAR_ROPE_LINEAR) keep = 0.0;
+    if (cfg->scaling == OSCAR_ROPE_BANDS) {
+      const double n = cfg->original_context * f / two_pi;
+      keep = std::min(std::max((n - cfg->low) / (cfg->high - cfg->low), 0.0), 1.0);
+    }
+    if (cfg->scaling == OSCAR_ROPE_YARN)
+      keep = 1.0 - std::min(std::max((i - x0) / std::max(x1 - x0, 0.001), 0.0), 1.0);
+    if (cfg->scaling != OSCAR_ROPE_UNSCALED) f = f / cfg->factor * (1.0 - keep) + f * keep;
+    double turns = f / two_pi;
+    turns -= std::floor(turns);  // positions are whole numbers: whole turns a position are none
+    steps[i] = uint64_t(std::ldexp(turns, 64));
+  }
+  *magnitude = cfg->scaling == OSCAR_ROPE_YARN ? float(0.1 * std::log(cfg->factor) + 1.0) : 1.0f;
+  return OSCAR_OK;
+}
+
+oscar_status oscar_rope(const oscar_rope_tensor* tensors, int n_tensors, const uint64_t* steps, int head_dim,
+                        int rotary_dim, float magnitude, int dtype, uint32_t flags, const void* positions,
+                        long long n_rows, void* stream) {
+  g_launches = 0;
+  if (!tensors || n_tensors < 1 || n_tensors > 2) return fail(OSCAR_ERR_INVALID_ARG, "one or two tensors");
+  if (rotary_dim < 2 || rotary_dim % 2 || head_dim < rotary_dim || head_dim > 512)
+    return fail(OSCAR_ERR_INVALID_ARG, "rotary_dim %d must be even, head_dim %d in [rotary_dim, 512]", rotary_dim, head_dim);
+  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_F16 && dtype != OSCAR_DTYPE_F32)
+    return fail(OSCAR_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
+  if (flags & ~(OSCAR_ROPE_INTERLEAVED | OSCAR_ROPE_TRANSPOSE | OSCAR_ROPE_POSITIONS64))
+    return fail(OSCAR_ERR_INVALID_ARG, "unknown rope flags %#x", flags);
+  if (n_rows < 0 || n_rows > 0x7fffffffLL) return fail(OSCAR_ERR_INVALID_ARG, "n_rows %lld out of range", n_rows);
+  const size_t size = dtype == OSCAR_DTYPE_F32 ? 4 : 2;
+  const size_t pos_size = flags & OSCAR_ROPE_POSITIONS64 ? 8 : 4;
+  RopeParams p = {};
+  bool aligned = true;
+  for (int i = 0; i < n_tensors; ++i) {
+    const oscar_rope_tensor& t = tensors[i];
+    if (t.n_heads < 1 || t.n_heads > 65536) return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: %d heads", i, t.n_heads);
+    if (n_rows > 0 && (!t.in || !t.out)) return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: NULL in or out", i);
+    if (t.in_row < 0 || t.in_head < 0 || t.out_row < 0 || t.out_head < 0)
+      return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: negative stride", i);
+    // outputs: heads inside their row, or rows inside their head
+    const bool rows_out = (t.n_heads == 1 || t.out_head >= head_dim) &&
+                          (n_rows <= 1 || t.out_row >= (t.n_heads - 1) * t.out_head + head_dim);
+    const bool heads_out = (n_rows <= 1 || t.out_row >= head_dim) &&
+                           (t.n_heads == 1 || t.out_head >= (n_rows - 1) * t.out_row + head_dim);
+    if (!rows_out && !heads_out) return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: output rows or heads overlap", i);
+    if (t.in == t.out && ((n_rows > 1 && t.in_row != t.out_row) || (t.n_heads > 1 && t.in_head != t.out_head)))
+      return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: in place with other strides", i);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out);
+    if (a % size) return fail(OSCAR_ERR_INVALID_ARG, "tensor %d: not aligned to its dtype", i);
+    if (a % 16 || (t.in_row * size) % 16 || (t.in_head * size) % 16 || (t.out_row * size) % 16 || (t.out_head * size) % 16)
+      aligned = false;
+    p.x[i] = {t.in, t.out, t.n_heads, t.in_row, t.in_head, t.out_row, t.out_head};
+  }
+  if (n_rows == 0) return OSCAR_OK;
+  if (!steps || !positions) return fail(OSCAR_ERR_INVALID_ARG, "NULL steps or positions");
+  if (reinterpret_cast<uintptr_t>(steps) % 8 || reinterpret_cast<uintptr_t>(positions) % pos_size)
+    return fail(OSCAR_ERR_INVALID_ARG, "steps or positions are not aligned to their type");
+  p.steps = steps;
+  p.positions = positions;
+  p.n_rows = n_rows;
+  p.head_dim = head_dim;
+  p.rotary_dim = rotary_dim;
+  p.magnitude = magnitude;
+  p.interleaved = (flags & OSCAR_ROPE_INTERLEAVED) != 0;
+  p.transpose = (flags & OSCAR_ROPE_TRANSPOSE) != 0;
+  p.positions64 = (flags & OSCAR_ROPE_POSITIONS64) != 0;
+  int dev = 0, n_sm = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  CUDA_TRY(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
+  const int e = launch_rope(p, dtype, aligned, n_sm, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "rope launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
 oscar_status oscar_set_wait_limit(oscar_cache* c, uint32_t counter_polls) {
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
   c->counter_polls = counter_polls;

@@ -163,6 +163,27 @@ int launch_calibrate(const void* q, const void* k, const void* v, int n_tokens, 
                      long clip_rank, bool hadamard_only, float* R_K, float* R_V, float* clip_K, float* clip_V,
                      double* C_out, uint8_t* ws, void* stream, int* launches);
 
+// Rotary positions (rope.cu): the tensors of a call (x[1].n_heads = 0 without a second one).
+// head_lanes, units, turn_units and rows_per_cta are the launcher's.
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int n_heads;
+  long long in_row, in_head, out_row, out_head;  // elements
+};
+struct RopeParams {
+  RopeTensor x[2];
+  const uint64_t* steps;
+  const void* positions;
+  long long n_rows;
+  int head_dim, rotary_dim;
+  float magnitude;
+  bool interleaved, transpose, positions64;
+  int units, turn_units, head_lanes, rows_per_cta;
+};
+// `aligned`: every row and head of every tensor starts on a 16-byte boundary.
+int launch_rope(const RopeParams& p, int dtype, bool aligned, int n_sm, void* stream, int* launches);
+
 // Decode with the library's own fixed device scratch instead of a caller workspace
 // (decode.cu).  Returns a cudaError_t as int; `too_big` is set when the plan's workspace
 // exceeds static_scratch_bytes().
