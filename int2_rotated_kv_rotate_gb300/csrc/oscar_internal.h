@@ -164,7 +164,7 @@ int launch_calibrate(const void* q, const void* k, const void* v, int n_tokens, 
                      double* C_out, uint8_t* ws, void* stream, int* launches);
 
 // Rotary positions (rope.cu): the tensors of a call (x[1].n_heads = 0 without a second one).
-// head_lanes, units, turn_units and rows_per_cta are the launcher's.
+// The last line is the launcher's.
 struct RopeTensor {
   const void* in;
   void* out;
@@ -179,7 +179,7 @@ struct RopeParams {
   int head_dim, rotary_dim;
   float magnitude;
   bool interleaved, transpose, positions64;
-  int units, turn_units, head_lanes, rows_per_cta;
+  int units, turn_units, pass_from, head_lanes, rows_per_cta;
 };
 // `aligned`: every row and head of every tensor starts on a 16-byte boundary.
 int launch_rope(const RopeParams& p, int dtype, bool aligned, int n_sm, void* stream, int* launches);

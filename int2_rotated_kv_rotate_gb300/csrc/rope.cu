@@ -8,15 +8,20 @@
 // converts to fp32 with a relative error of 2^-24.
 //
 // Elementwise and HBM-bound: every channel is read once and written once.  A CTA takes the
-// rows of `rows_per_cta` positions: it computes their sines and cosines once into shared
-// memory (one per row and pair, for all heads), then thread (head, unit) turns one unit of
-// its head: 16 bytes of the first half with the 16 bytes that pair with them (half layout)
-// or 16 bytes of adjacent pairs (interleaved).  A thread keeps its unit over the row's
-// heads, so its sines and cosines stay in registers.
+// rows of `rows_per_cta` positions and some 320 threads' worth of heads.  It computes its
+// rows' sines and cosines once into shared memory (one per row and pair, for all heads),
+// then thread (head, unit) walks down the rows with one unit of its head: 16 bytes of the
+// first half with the 16 bytes that pair with them (half layout), or 16 bytes of adjacent
+// pairs (interleaved).  Two rows are loaded before the first is stored.  Walking the rows
+// with a fixed head costs one pointer step a row; walking the heads of a row, and holding
+// the sines in registers, spent more on addresses than it saved (8192 rows of 40 heads with
+// 96 turning channels: 54 against 41 us).  Measured: 5.65 TB/s on 16384 rows of 72 bf16
+// heads (107 us), 5.6 TB/s on 4099 rows of 40 fp32 heads (30 us); one row 1.7 us in a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -42,6 +47,26 @@ struct alignas(V * sizeof(T)) Vec {
   T v[V];
 };
 
+// V channels at p: one access where VEC (aligned to it), else one by one.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+  Vec<T, V> w;
+  if constexpr (VEC) w = *reinterpret_cast<const Vec<T, V>*>(p);
+  else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) w.v[i] = p[i];
+  }
+  return w;
+}
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void store(T* p, const Vec<T, V>& w) {
+  if constexpr (VEC) *reinterpret_cast<Vec<T, V>*>(p) = w;
+  else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = w.v[i];
+  }
+}
+
 // cos and sin of 2 pi (phase / 2^64).
 __device__ __forceinline__ float2 turn(uint64_t phase) {
   const uint64_t q = (phase + (uint64_t(1) << 61)) >> 62;      // nearest quarter turn, mod 4
@@ -52,81 +77,98 @@ __device__ __forceinline__ float2 turn(uint64_t phase) {
   return make_float2((q == 1 || q == 2) ? -a : a, (q & 2) ? -b : b);
 }
 
-// V: channels of a unit (16 bytes, or 1 where the layout or the rotary size does not allow
-// vectors).  A unit of the half layout is V channels of the first half and their V
-// partners; of the interleaved one, V channels (2 at V = 1).  Channels past rotary_dim are
-// copied, VP at a time, unless the call works in place.
-template <typename T, int V, int VP, bool INTERLEAVED>
-__global__ void __launch_bounds__(512) rope_kernel(RopeParams p) {
-  extern __shared__ __align__(16) float2 table[];  // [rows_per_cta][pairs]
+constexpr int kBatch = 2;  // rows that a thread loads before it stores the first
+
+// V: channels of a vector, 16 bytes of them, or 1 where strides or sizes do not allow
+// vectors.  A unit that turns is V channels of the first half and their V partners (half
+// layout) or V channels (interleaved; 2 at V = 1).  Channels past rotary_dim are copied by
+// units of their own, unless the call works in place: 16 bytes each; at V = 1 first single
+// channels up to pass_from, then 16 bytes each if pass_from < head_dim.
+template <typename T, int V, bool INTERLEAVED>
+__global__ void __launch_bounds__(512, 2) rope_kernel(RopeParams p) {
+  extern __shared__ __align__(16) float2 table[];  // [rows_per_cta][pairs], see slot()
   constexpr int kPairs = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;  // pairs of a unit
+  constexpr int kChannels = INTERLEAVED ? 2 * kPairs : V;        // channels of one of its vectors
+  constexpr bool kVec = V > 1;
+  constexpr int kWide = 16 / sizeof(T);
   const int pairs = p.rotary_dim / 2;
   const long long row0 = (long long)blockIdx.x * p.rows_per_cta;
   const int n_rows = int(min((long long)p.rows_per_cta, p.n_rows - row0));
+  const int unit = threadIdx.x % p.units, head = blockIdx.y * p.head_lanes + threadIdx.x / p.units;
+  const int z = head >= p.x[0].n_heads;
+  const RopeTensor& x = p.x[z];
+  const int h = z ? head - p.x[0].n_heads : head;
+  const bool mine = threadIdx.x / p.units < p.head_lanes && h < x.n_heads;
+  const bool turns = unit < p.turn_units;
+  const bool single = !turns && unit - p.turn_units < p.pass_from - p.rotary_dim;
+  const int c0 = turns    ? unit * kChannels
+                 : single ? p.rotary_dim + unit - p.turn_units
+                          : p.pass_from + (unit - p.turn_units - (p.pass_from - p.rotary_dim)) * kWide;
+  const T* in = static_cast<const T*>(x.in) + row0 * x.in_row + h * x.in_head + c0;
+  T* out = static_cast<T*>(x.out) + row0 * x.out_row + h * x.out_head + c0;
+  // The pairs of a unit in twos of 16 bytes, the twos of all units side by side: a warp's
+  // 16-byte reads fall in different banks.
+  auto slot = [&](int r, int u, int j) {
+    if constexpr (kPairs == 1) return r * pairs + u;
+    return r * pairs + ((j >> 1) * p.turn_units + u) * 2 + (j & 1);
+  };
+  Vec<T, kChannels> a[kBatch], b[kBatch];
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (r + k < n_rows) {
+        a[k] = load<T, kChannels, kVec>(in + k * x.in_row);
+        if constexpr (!INTERLEAVED)
+          if (turns) b[k] = load<T, kChannels, kVec>(in + k * x.in_row + pairs);
+      }
+  };
+  const bool copies = mine && !turns && static_cast<const void*>(in) != static_cast<const void*>(out);
   pdl_wait();
   pdl_trigger();
+  if (mine && (kVec || turns)) fetch(0);  // in flight while the table is made
   for (int e = threadIdx.x; e < n_rows * pairs; e += blockDim.x) {
     const int r = e / pairs, i = e - r * pairs;
     const long long pos = p.positions64 ? reinterpret_cast<const long long*>(p.positions)[row0 + r]
                                         : (long long)(reinterpret_cast<const int*>(p.positions)[row0 + r]);
-    float2 cs = turn(uint64_t(pos) * p.steps[i]);
-    table[e] = make_float2(cs.x * p.magnitude, (p.transpose ? -cs.y : cs.y) * p.magnitude);
+    const float2 cs = turn(uint64_t(pos) * p.steps[i]);
+    table[slot(r, i / kPairs, i % kPairs)] =
+        make_float2(cs.x * p.magnitude, (p.transpose ? -cs.y : cs.y) * p.magnitude);
   }
   __syncthreads();
-  const int unit = threadIdx.x % p.units, lane = threadIdx.x / p.units;
-  if (lane >= p.head_lanes) return;  // threads past the last whole head
-  const int H = p.x[0].n_heads + p.x[1].n_heads;
-  for (int r = 0; r < n_rows; ++r) {
-    float2 cs[kPairs];
-    const bool turns = unit < p.turn_units;
-    if (turns) {
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) cs[j] = table[r * pairs + unit * kPairs + j];
-    }
-    for (int h = lane; h < H; h += p.head_lanes) {
-      const int z = h >= p.x[0].n_heads;
-      const RopeTensor& x = p.x[z];
-      const int hh = z ? h - p.x[0].n_heads : h;
-      const T* in = static_cast<const T*>(x.in) + (row0 + r) * x.in_row + (long long)hh * x.in_head;
-      T* out = static_cast<T*>(x.out) + (row0 + r) * x.out_row + (long long)hh * x.out_head;
-      if (turns) {
-        if constexpr (INTERLEAVED) {
-          using W = Vec<T, 2 * kPairs>;
-          W w;
-          if constexpr (V > 1) w = *reinterpret_cast<const W*>(in + unit * 2 * kPairs);
-          else {
-            w.v[0] = in[2 * unit];
-            w.v[1] = in[2 * unit + 1];
-          }
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            const float a = to_f32(w.v[2 * j]), b = to_f32(w.v[2 * j + 1]);
-            w.v[2 * j] = from_f32<T>(a * cs[j].x - b * cs[j].y);
-            w.v[2 * j + 1] = from_f32<T>(b * cs[j].x + a * cs[j].y);
-          }
-          if constexpr (V > 1) *reinterpret_cast<W*>(out + unit * 2 * kPairs) = w;
-          else {
-            out[2 * unit] = w.v[0];
-            out[2 * unit + 1] = w.v[1];
-          }
-        } else {
-          using W = Vec<T, V>;
-          W a = *reinterpret_cast<const W*>(in + unit * V);
-          W b = *reinterpret_cast<const W*>(in + pairs + unit * V);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float u = to_f32(a.v[j]), v = to_f32(b.v[j]);
-            a.v[j] = from_f32<T>(u * cs[j].x - v * cs[j].y);
-            b.v[j] = from_f32<T>(v * cs[j].x + u * cs[j].y);
-          }
-          *reinterpret_cast<W*>(out + unit * V) = a;
-          *reinterpret_cast<W*>(out + pairs + unit * V) = b;
-        }
-      } else if (in != out) {  // channels past rotary_dim
-        const int c = p.rotary_dim + (unit - p.turn_units) * VP;
-        *reinterpret_cast<Vec<T, VP>*>(out + c) = *reinterpret_cast<const Vec<T, VP>*>(in + c);
+  if (!mine) return;
+  if constexpr (!kVec) {
+    if (!turns) {  // single channels and 16-byte vectors past rotary_dim
+      if (!copies) return;
+      for (int r = 0; r < n_rows; ++r, in += x.in_row, out += x.out_row) {
+        if (single) *out = *in;
+        else store<T, kWide, true>(out, load<T, kWide, true>(in));
       }
+      return;
     }
+  }
+  for (int r = 0; r < n_rows; r += kBatch) {
+    if (r) fetch(r);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (r + k >= n_rows) break;
+      T* o = out + k * x.out_row;
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 cs = table[slot(r + k, unit, j)];
+          T& tu = INTERLEAVED ? a[k].v[2 * j] : a[k].v[j];
+          T& tv = INTERLEAVED ? a[k].v[2 * j + 1] : b[k].v[j];
+          const float u = to_f32(tu), v = to_f32(tv);
+          tu = from_f32<T>(u * cs.x - v * cs.y);
+          tv = from_f32<T>(v * cs.x + u * cs.y);
+        }
+      }
+      if (turns || copies) store<T, kChannels, kVec>(o, a[k]);
+      if constexpr (!INTERLEAVED)
+        if (turns) store<T, kChannels, kVec>(o + pairs, b[k]);
+    }
+    in += kBatch * x.in_row;
+    out += kBatch * x.out_row;
   }
 }
 
@@ -134,29 +176,28 @@ template <typename T>
 int launch_t(RopeParams p, bool aligned, int n_sm, void* stream, int* launches) {
   constexpr int V = 16 / sizeof(T);
   const int pairs = p.rotary_dim / 2, rest = p.head_dim - p.rotary_dim;
-  const bool vec = aligned && (p.interleaved ? p.rotary_dim : pairs) % V == 0;
-  const bool vec_rest = aligned && p.rotary_dim % V == 0 && rest % V == 0;
+  const bool vec = aligned && (p.interleaved ? p.rotary_dim : pairs) % V == 0 && rest % V == 0;
   p.turn_units = vec ? (p.interleaved ? p.rotary_dim / V : pairs / V) : pairs;
-  p.units = p.turn_units + rest / (vec_rest ? V : 1);
+  const int up = (p.rotary_dim + V - 1) / V * V;  // the first channel past the turning ones on 16 bytes
+  p.pass_from = vec ? p.rotary_dim : aligned && up < p.head_dim && p.head_dim % V == 0 ? up : p.head_dim;
+  p.units = p.turn_units + (p.pass_from - p.rotary_dim) + (p.head_dim - p.pass_from) / V;
+  // CTAs of about 320 threads: whole heads, evenly over the CTAs of a row block
   const int H = p.x[0].n_heads + p.x[1].n_heads;
-  // Lanes of heads that fill a CTA of about 320 threads with no ragged last pass.
-  const int want = p.units < 320 ? 320 / p.units : 1;
-  const int passes = (H + want - 1) / want;
-  p.head_lanes = (H + passes - 1) / passes;
+  const int most = p.units < 320 ? 320 / p.units : 1;
+  const int chunks = (H + most - 1) / most;
+  p.head_lanes = (H + chunks - 1) / chunks;
   const int threads = (p.units * p.head_lanes + 31) / 32 * 32;
-  // Few rows: one a CTA, to spread them.  Many: four share the table's barrier.
-  p.rows_per_cta = p.n_rows >= 16LL * n_sm ? 4 : 1;
+  // Rows of a CTA: what one wave of CTAs (1024 threads an SM at 64 registers) needs, at most
+  // 16.  4099 rows of 40 bf16 heads: 16.9 us in one wave, 18.9 and 21.5 us with 4 and 8 rows
+  // a CTA (a ragged second wave); 16384 rows of 72 heads: 112, 107 and 109 us with 4, 8, 16.
+  const long long wave = std::max<long long>(1, (long long)n_sm * (1024 / threads) / chunks);
+  p.rows_per_cta = int(std::min<long long>(16, (p.n_rows + wave - 1) / wave));
   const size_t smem = size_t(p.rows_per_cta) * pairs * sizeof(float2);
-  const long long grid = (p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta;
-  auto go = [&](auto kernel) { return launch_ex(kernel, dim3(unsigned(grid)), dim3(threads), smem, stream, p); };
+  const dim3 grid(unsigned((p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta), chunks);
+  auto go = [&](auto kernel) { return launch_ex(kernel, grid, dim3(threads), smem, stream, p); };
   int e;
-  if (p.interleaved) {
-    if (vec) e = vec_rest ? go(rope_kernel<T, V, V, true>) : go(rope_kernel<T, V, 1, true>);
-    else e = vec_rest ? go(rope_kernel<T, 1, V, true>) : go(rope_kernel<T, 1, 1, true>);
-  } else {
-    if (vec) e = vec_rest ? go(rope_kernel<T, V, V, false>) : go(rope_kernel<T, V, 1, false>);
-    else e = vec_rest ? go(rope_kernel<T, 1, V, false>) : go(rope_kernel<T, 1, 1, false>);
-  }
+  if (p.interleaved) e = vec ? go(rope_kernel<T, V, true>) : go(rope_kernel<T, 1, true>);
+  else e = vec ? go(rope_kernel<T, V, false>) : go(rope_kernel<T, 1, false>);
   if (!e) *launches += 1;
   return e;
 }

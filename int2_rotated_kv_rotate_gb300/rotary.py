@@ -82,7 +82,11 @@ class RotaryEmbedding:
             raise ValueError("k_out without k")
         flags = ((N.OSCAR_ROPE_INTERLEAVED if self.interleaved else 0) | (N.OSCAR_ROPE_TRANSPOSE if transpose else 0)
                  | (N.OSCAR_ROPE_POSITIONS64 if positions.dtype == torch.int64 else 0))
-        with torch.cuda.device(self.device):
-            N.oscar_rope(pairs, self.steps, self.head_dim, self.rotary_dim, self.magnitude, _DTYPES[q.dtype], flags,
-                         positions, stream)
+        args = (pairs, self.steps, self.head_dim, self.rotary_dim, self.magnitude, _DTYPES[q.dtype], flags, positions,
+                stream)
+        if self.device.index == torch.cuda.current_device():
+            N.oscar_rope(*args)
+        else:
+            with torch.cuda.device(self.device):
+                N.oscar_rope(*args)
         return (pairs[0][1], pairs[1][1]) if k is not None else pairs[0][1]
