@@ -179,7 +179,7 @@ struct RopeParams {
   int head_dim, rotary_dim;
   float magnitude;
   bool interleaved, transpose, positions64;
-  int units, turn_units, pass_from, head_lanes, rows_per_cta;
+  int units, turn_units, pass_from, head_lanes, chunks, rows_per_cta;
 };
 // `aligned`: every row and head of every tensor starts on a 16-byte boundary.
 int launch_rope(const RopeParams& p, int dtype, bool aligned, int n_sm, void* stream, int* launches);

@@ -78,6 +78,10 @@ __device__ __forceinline__ float2 turn(uint64_t phase) {
 }
 
 constexpr int kBatch = 2;  // rows that a thread loads before it stores the first
+// CTAs of 512 threads whose registers an SM has to hold.  The half layout keeps two vectors
+// a row, for which 40 registers spill (138 against 107 us on 16384 rows of 72 bf16 heads);
+// the interleaved one needs no more (98 against 104 us).
+constexpr int kPerSMHalf = 2, kPerSMInterleaved = 3;
 
 // V: channels of a vector, 16 bytes of them, or 1 where strides or sizes do not allow
 // vectors.  A unit that turns is V channels of the first half and their V partners (half
@@ -85,16 +89,18 @@ constexpr int kBatch = 2;  // rows that a thread loads before it stores the firs
 // units of their own, unless the call works in place: 16 bytes each; at V = 1 first single
 // channels up to pass_from, then 16 bytes each if pass_from < head_dim.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(512, 2) rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMHalf)
+    rope_kernel(RopeParams p) {
   extern __shared__ __align__(16) float2 table[];  // [rows_per_cta][pairs], see slot()
   constexpr int kPairs = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;  // pairs of a unit
   constexpr int kChannels = INTERLEAVED ? 2 * kPairs : V;        // channels of one of its vectors
   constexpr bool kVec = V > 1;
   constexpr int kWide = 16 / sizeof(T);
   const int pairs = p.rotary_dim / 2;
-  const long long row0 = (long long)blockIdx.x * p.rows_per_cta;
+  const unsigned block = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;  // a row block's chunks run together
+  const long long row0 = (long long)block * p.rows_per_cta;
   const int n_rows = int(min((long long)p.rows_per_cta, p.n_rows - row0));
-  const int unit = threadIdx.x % p.units, head = blockIdx.y * p.head_lanes + threadIdx.x / p.units;
+  const int unit = threadIdx.x % p.units, head = chunk * p.head_lanes + threadIdx.x / p.units;
   const int z = head >= p.x[0].n_heads;
   const RopeTensor& x = p.x[z];
   const int h = z ? head - p.x[0].n_heads : head;
@@ -184,17 +190,18 @@ int launch_t(RopeParams p, bool aligned, int n_sm, void* stream, int* launches) 
   // CTAs of about 320 threads: whole heads, evenly over the CTAs of a row block
   const int H = p.x[0].n_heads + p.x[1].n_heads;
   const int most = p.units < 320 ? 320 / p.units : 1;
-  const int chunks = (H + most - 1) / most;
-  p.head_lanes = (H + chunks - 1) / chunks;
+  p.chunks = (H + most - 1) / most;
+  p.head_lanes = (H + p.chunks - 1) / p.chunks;
   const int threads = (p.units * p.head_lanes + 31) / 32 * 32;
-  // Rows of a CTA: what one wave of CTAs (1024 threads an SM at 64 registers) needs, at most
-  // 16.  4099 rows of 40 bf16 heads: 16.9 us in one wave, 18.9 and 21.5 us with 4 and 8 rows
+  // Rows of a CTA: what one wave of CTAs needs, at most 16.  4099 rows of 40 bf16 heads: 16.9 us in one wave, 18.9 and 21.5 us with 4 and 8 rows
   // a CTA (a ragged second wave); 16384 rows of 72 heads: 112, 107 and 109 us with 4, 8, 16.
-  const long long wave = std::max<long long>(1, (long long)n_sm * (1024 / threads) / chunks);
+  const int per_sm = p.interleaved ? kPerSMInterleaved : kPerSMHalf;
+  const long long wave = std::max<long long>(1, (long long)n_sm * (512 * per_sm / threads) / p.chunks);
   p.rows_per_cta = int(std::min<long long>(16, (p.n_rows + wave - 1) / wave));
   const size_t smem = size_t(p.rows_per_cta) * pairs * sizeof(float2);
-  const dim3 grid(unsigned((p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta), chunks);
-  auto go = [&](auto kernel) { return launch_ex(kernel, grid, dim3(threads), smem, stream, p); };
+  const long long grid = (p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta * p.chunks;
+  if (grid > 0x7fffffffLL) return int(cudaErrorInvalidConfiguration);
+  auto go = [&](auto kernel) { return launch_ex(kernel, dim3(unsigned(grid)), dim3(threads), smem, stream, p); };
   int e;
   if (p.interleaved) e = vec ? go(rope_kernel<T, V, true>) : go(rope_kernel<T, 1, true>);
   else e = vec ? go(rope_kernel<T, V, false>) : go(rope_kernel<T, 1, false>);
