@@ -234,6 +234,55 @@ oscar_status oscar_bf16_append(oscar_cache* cache, int layer, const void* k_new,
 oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const void* q, void* out, void* workspace,
                                          size_t ws_bytes, float* out_f32, void* stream);
 
+/* Accumulated attention weights (format OSCAR_FORMAT_BF16).  A row of weights is
+ * oscar_weights_stride tokens, 64 * min(max_pages_per_request, max_pages); a buffer of one
+ * layer is fp32 [max_requests][H_kv][stride] [dev], indexed by request slot and position and
+ * owned by the caller, who zeroes a slot's rows when a request starts in it.
+ *
+ * oscar_bf16_decode_weights is oscar_bf16_decode_attention (same plan, q, out and out_f32)
+ * that also writes weights_out[slot][kv-head][t] = weights_in[slot][kv-head][t] + sum over
+ * the kv-head's query heads of softmax(q K^T / sqrt(d))[t] for every token t < L of the
+ * planned requests; weights_in NULL counts as zeros and may be weights_out (it must not
+ * overlap it otherwise).  Other entries of weights_out stay as they are.  The workspace
+ * (oscar_decode_weights_workspace_bytes for the current plan, _max_bytes for every plan)
+ * also holds the scores, 4 bytes a query head and token of a row.  Two launches. */
+int oscar_weights_stride(const oscar_cache* cache);
+size_t oscar_decode_weights_workspace_bytes(const oscar_cache* cache);
+size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* cache);
+oscar_status oscar_bf16_decode_weights(oscar_cache* cache, int layer, const void* q, void* out, const float* weights_in,
+                                       float* weights_out, void* workspace, size_t ws_bytes, float* out_f32,
+                                       void* stream);
+
+/* Eviction by accumulated attention weight (format OSCAR_FORMAT_BF16): of a request's L
+ * tokens `keep` stay, per layer and kv-head: the first n_sink, the last n_recent, and of the
+ * others those with the greatest weight (equal weights: the lowest positions; -0 equals 0;
+ * NaN comes last).  They move, in the order of their positions, into new pages (pages shared
+ * with other requests are never rewritten), and the request's length becomes keep.  A
+ * request with L <= keep keeps everything where it is.
+ *
+ * Step 1 (host): oscar_evict_begin takes the new pages for `keep[i]` tokens of request
+ * `slots[i]` [host arrays of n_req distinct slots] and uploads the plan on `stream`, which
+ * serves every layer until the commit.  keep[i] >= n_sink + n_recent where tokens go.  On
+ * OSCAR_ERR_OUT_OF_PAGES nothing is taken.  Until the commit (or cancel), reserving, freeing
+ * requests and sharing prefixes is refused; decodes still see the old pages.
+ * Step 2 (device, per layer): oscar_evict copies the layer's kept rows.  weights as above,
+ * 16-byte aligned; weights_out, same shape: the rows of the listed slots become the kept
+ * tokens' weights, then zeros to the end of the row; kept int32, same shape: the positions
+ * (before the eviction) of the kept tokens, entries from keep on stay as they are.  The
+ * three must not overlap.
+ * Step 3 (host): oscar_evict_commit makes the new pages the requests' (uploads their
+ * page-table rows on `stream`) and frees the old ones; plan again before decoding.
+ * oscar_evict_cancel gives the new pages back instead.
+ * oscar_evict_pages: between begin and commit, host copy of up to n of the pages that slot
+ * will have, their number in *n_pages (nullable). */
+oscar_status oscar_evict_begin(oscar_cache* cache, const int* slots, const int* keep, int n_req, int n_sink,
+                               int n_recent, void* stream);
+oscar_status oscar_evict(oscar_cache* cache, int layer, const float* weights, float* weights_out, int* kept,
+                         void* stream);
+oscar_status oscar_evict_pages(const oscar_cache* cache, int slot, int* pages, int n, int* n_pages);
+oscar_status oscar_evict_commit(oscar_cache* cache, void* stream);
+oscar_status oscar_evict_cancel(oscar_cache* cache);
+
 /* oscar_decode_attention without a caller workspace.  The paper has no counterpart:
  * this exists for callers that cannot allocate device memory themselves, for example a
  * plugin whose host framework owns every device allocation and gives it none, or a

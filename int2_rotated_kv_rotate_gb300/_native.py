@@ -62,7 +62,9 @@ EXPORTS = [
     "oscar_decode_workspace_max_bytes", "oscar_plan_info",
     "oscar_decode_attention", "oscar_append_decode_attention", "oscar_decode_attention_noalloc", "oscar_bf16_append",
     "oscar_bf16_decode_attention", "oscar_calibration_workspace_bytes", "oscar_calibrate_layer",
-    "oscar_rope_steps", "oscar_rope",
+    "oscar_rope_steps", "oscar_rope", "oscar_weights_stride", "oscar_decode_weights_workspace_bytes",
+    "oscar_decode_weights_workspace_max_bytes", "oscar_bf16_decode_weights", "oscar_evict_begin", "oscar_evict",
+    "oscar_evict_pages", "oscar_evict_commit", "oscar_evict_cancel",
     "oscar_set_wait_limit", "oscar_inject_fault", "oscar_get_status",
     "oscar_last_error", "oscar_last_launch_count",
 ]
@@ -109,6 +111,15 @@ def lib() -> ctypes.CDLL:
                 "oscar_bf16_decode_attention": (I, [P, I, P, P, P, S, P, P]),
                 "oscar_calibration_workspace_bytes": (S, [I, I, I]),
                 "oscar_calibrate_layer": (I, [P, P, P, I, I, I, ctypes.c_longlong, I, P, P, P, P, P, P, S, P]),
+                "oscar_weights_stride": (I, [P]),
+                "oscar_decode_weights_workspace_bytes": (S, [P]),
+                "oscar_decode_weights_workspace_max_bytes": (S, [P]),
+                "oscar_bf16_decode_weights": (I, [P, I, P, P, P, P, P, S, P, P]),
+                "oscar_evict_begin": (I, [P, IP, IP, I, I, I, P]),
+                "oscar_evict": (I, [P, I, P, P, P, P]),
+                "oscar_evict_pages": (I, [P, I, IP, I, IP]),
+                "oscar_evict_commit": (I, [P, P]),
+                "oscar_evict_cancel": (I, [P]),
                 "oscar_rope_steps": (I, [ctypes.POINTER(oscar_rope_config), ctypes.POINTER(ctypes.c_uint64),
                                          ctypes.POINTER(ctypes.c_float)]),
                 "oscar_rope": (I, [ctypes.POINTER(oscar_rope_tensor), I, P, I, I, ctypes.c_float, I, ctypes.c_uint32, P,
@@ -286,6 +297,53 @@ def oscar_bf16_decode_attention(handle: int, layer: int, q, out, workspace, out_
     _check(lib().oscar_bf16_decode_attention(handle, layer, _ptr(q), _ptr(out), _ptr(workspace),
                                              workspace.numel() * workspace.element_size(), _ptr(out_f32),
                                              _stream(stream)))
+
+
+def oscar_weights_stride(handle: int) -> int:
+    """Tokens of a row of accumulated weights (0 for the INT2 formats)."""
+    return int(lib().oscar_weights_stride(handle))
+
+
+def oscar_decode_weights_workspace_bytes(handle: int) -> int:
+    return int(lib().oscar_decode_weights_workspace_bytes(handle))
+
+
+def oscar_decode_weights_workspace_max_bytes(handle: int) -> int:
+    return int(lib().oscar_decode_weights_workspace_max_bytes(handle))
+
+
+def oscar_bf16_decode_weights(handle: int, layer: int, q, out, weights_in, weights_out, workspace, out_f32=None,
+                              stream=None) -> None:
+    _check(lib().oscar_bf16_decode_weights(handle, layer, _ptr(q), _ptr(out), _ptr(weights_in), _ptr(weights_out),
+                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                           _ptr(out_f32), _stream(stream)))
+
+
+def oscar_evict_begin(handle: int, slots, keep, n_sink: int = 0, n_recent: int = 0, stream=None) -> None:
+    s, n = _ints(slots)
+    k, n2 = _ints(keep)
+    assert n == n2
+    _check(lib().oscar_evict_begin(handle, s, k, n, int(n_sink), int(n_recent), _stream(stream)))
+
+
+def oscar_evict(handle: int, layer: int, weights, weights_out, kept, stream=None) -> None:
+    _check(lib().oscar_evict(handle, layer, _ptr(weights), _ptr(weights_out), _ptr(kept), _stream(stream)))
+
+
+def oscar_evict_pages(handle: int, slot: int):
+    n = ctypes.c_int()
+    _check(lib().oscar_evict_pages(handle, slot, None, 0, ctypes.byref(n)))
+    buf = (ctypes.c_int * max(1, n.value))()
+    _check(lib().oscar_evict_pages(handle, slot, buf, n.value, None))
+    return list(buf)[:n.value]
+
+
+def oscar_evict_commit(handle: int, stream=None) -> None:
+    _check(lib().oscar_evict_commit(handle, _stream(stream)))
+
+
+def oscar_evict_cancel(handle: int) -> None:
+    _check(lib().oscar_evict_cancel(handle))
 
 
 def oscar_get_status(handle: int, stream=None):

@@ -25,6 +25,8 @@ class KVCache:
         self.handle = N.oscar_cache_create(self.cfg, self.mem, self.nbytes)
         self.layout = N.oscar_cache_layout(self.handle)
         self.workspace = None
+        self.weights_workspace = None
+        self.weights_stride = N.oscar_weights_stride(self.handle)  # 0: no weights in this format
         self.fmt = fmt
         self.is_int2 = fmt in (N.OSCAR_FORMAT_INT2, N.OSCAR_FORMAT_INT2_CM)
         self._rows = None  # rows of k_new / v_new the pending reservation expects
@@ -133,6 +135,68 @@ class KVCache:
             N.oscar_bf16_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
         return out
 
+    # ------------------------------------------------------------------ accumulated weights (BF16 format)
+    def new_weights(self) -> torch.Tensor:
+        """A layer's accumulated attention weights, zeros: fp32 [request slots, H_kv, weights_stride]."""
+        return torch.zeros(self._weights_shape(), device=self.device)
+
+    def _weights_shape(self):
+        if not self.weights_stride:
+            raise ValueError("accumulated weights need the BF16 format")
+        return (self.cfg.max_requests, self.cfg.n_kv_heads, self.weights_stride)
+
+    def _check_weights(self, name, t, dtype=torch.float32):
+        shape = self._weights_shape()
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.mem.device:
+            raise ValueError(f"{name} must be contiguous {dtype} {shape} on {self.mem.device}")
+
+    def decode_weights(self, layer: int, q, weights, weights_out=None, out=None, out_f32=None, stream=None):
+        """decode that also adds every attended token's softmax probability, summed over its
+        kv-head's query heads, to `weights`: (out, weights_out).  In place without weights_out;
+        rows of requests outside the plan and entries past a request's length stay as they are."""
+        weights_out = weights if weights_out is None else weights_out
+        self._check_weights("weights", weights)
+        self._check_weights("weights_out", weights_out)
+        out = self._check_decode(q, out, out_f32)
+        if self.weights_workspace is None:  # sized for every plan, once: captured launches keep this pointer
+            self.weights_workspace = torch.empty(N.oscar_decode_weights_workspace_max_bytes(self.handle),
+                                                 dtype=torch.uint8, device=self.device)
+        N.oscar_bf16_decode_weights(self.handle, layer, q, out, weights, weights_out, self.weights_workspace, out_f32,
+                                    stream)
+        return out, weights_out
+
+    # ------------------------------------------------------------------ eviction (BF16 format)
+    def evict_begin(self, slots, keep, n_sink: int = 0, n_recent: int = 0, stream=None) -> None:
+        """Plan the eviction of all but keep[i] tokens of request slots[i], per layer and kv-head:
+        the first n_sink and the last n_recent stay, of the others those with the greatest weight."""
+        N.oscar_evict_begin(self.handle, slots, keep, n_sink, n_recent, stream)
+
+    def evict(self, layer: int, weights, weights_out=None, kept=None, stream=None):
+        """Copy one layer's kept tokens into their new pages: (weights_out, kept), the kept tokens'
+        weights (zeros behind them) and their positions before the eviction, int32 (-1 behind
+        them when this call makes the tensor).  Rows of other slots stay as they are (those of a
+        weights_out that this call makes: as in weights)."""
+        self._check_weights("weights", weights)
+        if weights_out is None:
+            weights_out = weights.clone()
+        if kept is None:
+            kept = torch.full(weights.shape, -1, dtype=torch.int32, device=self.device)
+        self._check_weights("weights_out", weights_out)
+        self._check_weights("kept", kept, torch.int32)
+        N.oscar_evict(self.handle, layer, weights, weights_out, kept, stream)
+        return weights_out, kept
+
+    def evict_pages(self, slot: int):
+        """Pages that slot will have after the commit of the pending eviction."""
+        return N.oscar_evict_pages(self.handle, slot)
+
+    def evict_commit(self, stream=None) -> None:
+        N.oscar_evict_commit(self.handle, stream)
+        self._n_plan = None
+
+    def evict_cancel(self) -> None:
+        N.oscar_evict_cancel(self.handle)
+
     def append_decode(self, layer: int, k_new, v_new, q, out=None, out_f32=None, stream=None):
         """quantize_append then decode of `layer` in one launch (INT2 format; plan made
         during the reservation over every reserved slot)."""
@@ -147,6 +211,14 @@ class KVCache:
     # ------------------------------------------------------------------ raw reads (tests)
     def _bytes(self, offset: int, n: int) -> torch.Tensor:
         return self.mem[offset:offset + n]
+
+    def bf16_pages(self, layer: int) -> torch.Tensor:
+        """The BF16 format's pages of one layer, a view: [pages, H_kv, K|V, 64, 128]."""
+        if self.is_int2:
+            raise ValueError("BF16 pages need the BF16 format")
+        n = self.cfg.max_pages * self.cfg.n_kv_heads * self.layout.bf16_page_bytes
+        at = self.layout.bf16_pages + layer * n
+        return self._bytes(at, n).view(torch.bfloat16).view(self.cfg.max_pages, self.cfg.n_kv_heads, 2, 64, 128)
 
     def int2_rows(self, layer: int, slot: int, kvh: int, kv: int, positions):
         """Device-stored 32-byte code rows and scale/zero words of INT2 positions (host)."""

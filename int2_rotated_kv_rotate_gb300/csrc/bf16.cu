@@ -24,10 +24,13 @@ namespace {
 template <int G, int NBUF>
 constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::kBytes;
 
-template <int G, int NBUF>
+// WEIGHTS: the scores (log2 units) go to scores, fp32 [plan request][kv-head][stride][G], and
+// each head's (maximum, 1 / denominator) to ml, for bf16_weights_kernel.
+template <int G, int NBUF, bool WEIGHTS>
 __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q,
                                                          uint8_t* __restrict__ partials, uint16_t* __restrict__ out,
-                                                         float* __restrict__ out_f32) {
+                                                         float* __restrict__ out_f32, float* __restrict__ scores,
+                                                         float2* __restrict__ ml) {
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + Bf16Rows<4, NBUF>::kSmemBytes);
   int* s_last_p = reinterpret_cast<int*>(smem + Bf16Rows<4, NBUF>::kSmemBytes + G * kQRow * 4);
@@ -87,7 +90,13 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
     }
     for (int e = threadIdx.x; e < G * kHeadDim; e += 128) qs[(e / kHeadDim) * kQRow + e % kHeadDim] = bf16_f32(q[head0 * kHeadDim + e]);
     __syncthreads();
-    bf16_rows_mma<G, 4, NBUF>(rowK, rowV, t0, t1, qs, part, smem, staged, [] {});
+    auto keep = [=](int h, int u, float s) {
+      if constexpr (WEIGHTS)
+        scores[((size_t(it.req) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride) + size_t(u)) * G + h] = s;
+    };
+    auto nothing = [] {};
+    bf16_rows_mma<G, 4, NBUF, decltype(rowK), decltype(rowV), decltype(nothing), decltype(keep), true>(
+        rowK, rowV, t0, t1, qs, part, smem, staged, nothing, keep);
 
     MergeAcc<G, 128> acc;
     if (merge_partial<G, 128>(kp, it, partials, acc, s_last_p, smem, kBf16SlabSlots<G, NBUF>, smem_u32(slab_bar), slab_phase,
@@ -98,6 +107,8 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
         const float r = acc.L[h] > 0.f ? acc.O[h] / acc.L[h] : 0.f;
         out[(head0 + h) * kHeadDim + c] = bf16_rne(r);
         if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = r;
+        if constexpr (WEIGHTS)
+          if (c == h) ml[head0 + h] = acc.L[h] > 0.f ? make_float2(acc.M[h], 1.f / acc.L[h]) : make_float2(0.f, 0.f);
       }
     }
     fence_proxy_async();  // generic use of the buffers is over before later bulk copies
@@ -109,20 +120,76 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
   wq.leave();
 }
 
+// Second pass of the decode with weights: the softmax probabilities of each (request,
+// kv-head)'s tokens, summed over its G query heads, added to their accumulated weights.
+// Memory-bound: 4 G + 8 bytes a token (the K and V rows of the first pass are 512), four
+// tokens a thread in flight.  The plan's items give the work, kPiece tokens of one at a time.
+constexpr int kWeightsThreads = 128;
+constexpr int kPiece = 4 * kWeightsThreads;
+
+template <int G>
+__global__ void __launch_bounds__(kWeightsThreads) bf16_weights_kernel(KernelParams kp, const float* __restrict__ scores,
+                                                                       const float2* __restrict__ ml,
+                                                                       const float* weights_in, float* weights_out) {
+  pdl_wait();
+  pdl_trigger();
+  const int n_items = reinterpret_cast<const int*>(kp.base + kp.lay.decode_counts)[0];
+  for (int ix = blockIdx.x; ix < n_items; ix += gridDim.x) {
+    const DecodeItem it = reinterpret_cast<const DecodeItem*>(kp.base + kp.lay.decode_items)[ix];
+    const DecodeReq dr = reinterpret_cast<const DecodeReq*>(kp.base + kp.lay.decode_reqs)[it.req];
+    if (dr.slot < 0 || dr.slot >= kp.max_requests || it.kind != 0) continue;
+    const int t0 = it.begin * kPage, t1 = min(it.end * kPage, dr.L);
+    if (t0 + int(blockIdx.y) * kPiece >= t1) continue;
+    float2 head[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) head[h] = ml[size_t(it.req) * kp.n_q_heads + size_t(it.kvh) * G + h];
+    const float* sc = scores + (size_t(it.req) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride) * G;
+    const size_t row = (size_t(dr.slot) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride);
+    for (int p = t0 + int(blockIdx.y) * kPiece; p < t1; p += int(gridDim.y) * kPiece) {
+      float4 s[4][G / 4];
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = p + i * kWeightsThreads + int(threadIdx.x);
+        if (t < t1) {
+          w[i] = weights_in ? weights_in[row + t] : 0.f;
+#pragma unroll
+          for (int j = 0; j < G / 4; ++j) s[i][j] = reinterpret_cast<const float4*>(sc + size_t(t) * G)[j];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = p + i * kWeightsThreads + int(threadIdx.x);
+        if (t < t1) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < G / 4; ++j) {
+            sum = fmaf(ex2(s[i][j].x - head[4 * j].x), head[4 * j].y, sum);
+            sum = fmaf(ex2(s[i][j].y - head[4 * j + 1].x), head[4 * j + 1].y, sum);
+            sum = fmaf(ex2(s[i][j].z - head[4 * j + 2].x), head[4 * j + 2].y, sum);
+            sum = fmaf(ex2(s[i][j].w - head[4 * j + 3].x), head[4 * j + 3].y, sum);
+          }
+          weights_out[row + t] = w[i] + sum;
+        }
+      }
+    }
+  }
+}
+
 constexpr int kBf16KernelSmem(int G, int nbuf) {
   return (nbuf == 3 ? Bf16Rows<4, 3>::kSmemBytes : Bf16Rows<4, 2>::kSmemBytes) + G * kQRow * 4 + 32;  // + flags, barrier
 }
 
-template <int G, int NBUF>
+template <int G, int NBUF, bool WEIGHTS = false>
 int resident_ctas(int n_sm) {
   static int resident = 0;
   if (resident == 0) {
-    int e = int(cudaFuncSetAttribute(bf16_split_kernel<G, NBUF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    int e = int(cudaFuncSetAttribute(bf16_split_kernel<G, NBUF, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kBf16KernelSmem(G, NBUF)));
     int per_sm = 0;
     if (!e)
-      e = int(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, bf16_split_kernel<G, NBUF>, 128,
-                                                            kBf16KernelSmem(G, NBUF)));
+      e = int(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, bf16_split_kernel<G, NBUF, WEIGHTS>,
+                                                            128, kBf16KernelSmem(G, NBUF)));
     if (e) return -e;
     resident = (per_sm > 0 ? per_sm : 1) * n_sm;
   }
@@ -136,8 +203,27 @@ int launch_t(const KernelParams& kp, int layer, const void* q, void* out, float*
   const int resident = resident_ctas<G, NBUF>(n_sm);
   if (resident < 0) return -resident;
   const int grid = resident;  // persistent-style: CTAs loop over the plan's items
-  int e = launch_ex(bf16_split_kernel<G, NBUF>, dim3(grid), dim3(128), size_t(kBf16KernelSmem(G, NBUF)), stream, kp,
-                    layer, static_cast<const uint16_t*>(q), partials, static_cast<uint16_t*>(out), out_f32);
+  int e = launch_ex(bf16_split_kernel<G, NBUF, false>, dim3(grid), dim3(128), size_t(kBf16KernelSmem(G, NBUF)), stream,
+                    kp, layer, static_cast<const uint16_t*>(q), partials, static_cast<uint16_t*>(out), out_f32,
+                    static_cast<float*>(nullptr), static_cast<float2*>(nullptr));
+  if (!e) *launches += 1;
+  return e;
+}
+
+template <int G, int NBUF>
+int launch_weights_t(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, const float* w_in,
+                     float* w_out, uint8_t* ws, const WeightsWorkspace& wl, int n_sm, void* stream, int* launches) {
+  const int resident = resident_ctas<G, NBUF, true>(n_sm);
+  if (resident < 0) return -resident;
+  float* scores = reinterpret_cast<float*>(ws + wl.scores);
+  float2* ml = reinterpret_cast<float2*>(ws + wl.ml);
+  int e = launch_ex(bf16_split_kernel<G, NBUF, true>, dim3(resident), dim3(128), size_t(kBf16KernelSmem(G, NBUF)), stream,
+                    kp, layer, static_cast<const uint16_t*>(q), ws + wl.partials, static_cast<uint16_t*>(out), out_f32,
+                    scores, ml);
+  if (e) return e;
+  *launches += 1;
+  e = launch_ex(bf16_weights_kernel<G>, dim3(4 * n_sm, 4), dim3(kWeightsThreads), 0, stream, kp,
+                static_cast<const float*>(scores), static_cast<const float2*>(ml), w_in, w_out);
   if (!e) *launches += 1;
   return e;
 }
@@ -148,6 +234,18 @@ int bf16_decode_resident_ctas(int gqa, bool deep, int n_sm) {
   if (gqa == 4) return deep ? resident_ctas<4, 3>(n_sm) : resident_ctas<4, 2>(n_sm);
   if (gqa == 8) return deep ? resident_ctas<8, 3>(n_sm) : resident_ctas<8, 2>(n_sm);
   return n_sm;
+}
+
+int launch_bf16_decode_weights(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32,
+                               const float* w_in, float* w_out, uint8_t* ws, const WeightsWorkspace& wl, bool deep,
+                               int n_sm, void* stream, int* launches) {
+  if (kp.gqa == 4)
+    return deep ? launch_weights_t<4, 3>(kp, layer, q, out, out_f32, w_in, w_out, ws, wl, n_sm, stream, launches)
+                : launch_weights_t<4, 2>(kp, layer, q, out, out_f32, w_in, w_out, ws, wl, n_sm, stream, launches);
+  if (kp.gqa == 8)
+    return deep ? launch_weights_t<8, 3>(kp, layer, q, out, out_f32, w_in, w_out, ws, wl, n_sm, stream, launches)
+                : launch_weights_t<8, 2>(kp, layer, q, out, out_f32, w_in, w_out, ws, wl, n_sm, stream, launches);
+  return int(cudaErrorInvalidValue);
 }
 
 int launch_bf16_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,

@@ -209,9 +209,16 @@ __device__ void bf16_prestage(RowK rowK, RowV rowV, int begin, int upto, uint8_t
   cp_async_commit();
 }
 
-template <int G, int NW, int NBUF, typename RowK, typename RowV, typename BeforeRest>
+// on_score(head, token, score in log2 units) sees every token's scores (nothing by default).
+// BF16_Q: q holds bf16 values, so the lo columns are zero and the scores leave them out
+// (an infinite key times that zero would make a NaN of an infinite score).
+struct NoScores {
+  __device__ __forceinline__ void operator()(int, int, float) const {}
+};
+template <int G, int NW, int NBUF, typename RowK, typename RowV, typename BeforeRest, typename OnScore = NoScores,
+          bool BF16_Q = false>
 __device__ void bf16_rows_mma(RowK rowK, RowV rowV, int begin, int end, const float* qg, uint8_t* part, uint8_t* smem,
-                              int staged, BeforeRest before_rest) {
+                              int staged, BeforeRest before_rest, OnScore on_score = OnScore()) {
   constexpr int NT = G / 4;
   using B = Bf16Rows<NW, NBUF>;
   constexpr int kChunkTok = B::kChunk;
@@ -305,8 +312,10 @@ __device__ void bf16_rows_mma(RowK rowK, RowV rowV, int begin, int end, const fl
     bool rescale = false;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      lg[j][0] = u0 < end ? (acc[j][0] + acc[j][1]) * scale : -INFINITY;
-      lg[j][1] = u1 < end ? (acc[j][2] + acc[j][3]) * scale : -INFINITY;
+      lg[j][0] = u0 < end ? (BF16_Q ? acc[j][0] : acc[j][0] + acc[j][1]) * scale : -INFINITY;
+      lg[j][1] = u1 < end ? (BF16_Q ? acc[j][2] : acc[j][2] + acc[j][3]) * scale : -INFINITY;
+      if (u0 < end) on_score(4 * j + tig, u0, lg[j][0]);
+      if (u1 < end) on_score(4 * j + tig, u1, lg[j][1]);
       float mx = fmaxf(lg[j][0], lg[j][1]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));

@@ -118,6 +118,8 @@ DeviceLayout compute_layout(const oscar_config& c) {
     L.bf16_page_stride = Hkv * L.bf16_head_stride;
     L.bf16_layer_stride = pages * L.bf16_page_stride;
     L.bf16_pages = take(layers * L.bf16_layer_stride);
+    L.evict_plan = take(256 + reqs * sizeof(EvictReq));
+    L.evict_pages = take(reqs * size_t(c.max_pages_per_request) * 4);
   }
   L.page_table = take(reqs * size_t(c.max_pages_per_request) * 4);
   L.status = take(256);
@@ -172,6 +174,11 @@ struct oscar_cache {
   bool plan_covers_reservation = false;  // the plan lists every slot of the pending reservation
   bool dec_wide = false;                  // INT2: the plan is for 16-warp split-kernel CTAs; BF16: for the deep pipeline
   bool dec_folded = false;                // OSCAR_PLAN_FOLDED_ROTATIONS: q~ in, o~ out
+  // pending eviction (BF16 format)
+  bool evicting = false;
+  std::vector<EvictReq> ev_reqs;
+  std::vector<std::vector<int>> ev_pages;  // new pages of each request that gives tokens up
+  int ev_max_pages = 0;
   // decode plan
   bool planned = false;
   bool planned_with_reservation = false;  // the plan already counts the reserved tokens
@@ -206,6 +213,7 @@ KernelParams kernel_params(const oscar_cache* c) {
   kp.max_pages_per_request = c->cfg.max_pages_per_request;
   kp.counter_polls = c->counter_polls ? c->counter_polls : kDefaultCounterPolls;
   kp.v_cm = c->cfg.format == OSCAR_FORMAT_INT2_CM;
+  kp.weights_stride = oscar_weights_stride(c);
   kp.folded = c->dec_folded;
   kp.lay = c->lay;
   return kp;
@@ -272,6 +280,27 @@ oscar_status check_slot(const oscar_cache* c, int slot) {
   if (slot < 0 || slot >= c->cfg.max_requests) return fail(OSCAR_ERR_INVALID_ARG, "slot %d out of range", slot);
   if (!c->reqs[slot].in_use) return fail(OSCAR_ERR_INVALID_ARG, "slot %d is not allocated", slot);
   return OSCAR_OK;
+}
+
+// The calls that look at device memory through the current device.
+oscar_status check_device(const oscar_cache* c) {
+  int dev = -1;
+  CUDA_TRY(cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(OSCAR_ERR_INVALID_ARG, "current device %d is not the cache's device %d", dev, c->device);
+  return OSCAR_OK;
+}
+
+// Workspace of a decode with weights over n_req requests.  Only the total depends on the
+// plan: a captured launch keeps its offsets.
+WeightsWorkspace weights_workspace(const oscar_cache* c, int n_req) {
+  const size_t Hq = c->cfg.n_q_heads, G = Hq / c->cfg.n_kv_heads;
+  WeightsWorkspace w;
+  w.ml = 0;
+  w.partials = align256(size_t(c->cfg.max_requests) * Hq * 8);
+  w.scores = w.partials + align256(c->lay.max_decode_items * G * (8 + 4 * kHeadDim));
+  w.total = w.scores + size_t(n_req) * Hq * size_t(oscar_weights_stride(c)) * 4;
+  return w;
 }
 
 }  // namespace
@@ -421,6 +450,7 @@ oscar_status oscar_request_alloc(oscar_cache* c, int* slot) {
 oscar_status oscar_request_free(oscar_cache* c, int slot) {
   oscar_status st = check_slot(c, slot);
   if (st) return st;
+  if (c->evicting) return fail(OSCAR_ERR_STATE, "an eviction is pending");
   if (c->reserved)
     for (const AppendReq& r : c->app_reqs)
       if (r.slot == slot) return fail(OSCAR_ERR_STATE, "slot %d has a pending reservation", slot);
@@ -472,6 +502,7 @@ oscar_status oscar_request_share_prefix(oscar_cache* c, int dst, int src, int n_
   if (st) return st;
   if (dst == src) return fail(OSCAR_ERR_INVALID_ARG, "dst == src");
   if (c->reserved) return fail(OSCAR_ERR_STATE, "a reservation is pending");
+  if (c->evicting) return fail(OSCAR_ERR_STATE, "an eviction is pending");
   Request& d = c->reqs[dst];
   const Request& s = c->reqs[src];
   if (d.L != 0 || !d.pages.empty()) return fail(OSCAR_ERR_INVALID_ARG, "dst must be empty");
@@ -509,6 +540,7 @@ oscar_status oscar_reserve(oscar_cache* c, const int* slots, const int* n_new, i
   if (!c || !slots || !n_new || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad reserve arguments");
   if (c->reserved) return fail(OSCAR_ERR_STATE, "previous reservation not committed");
+  if (c->evicting) return fail(OSCAR_ERR_STATE, "an eviction is pending");
   std::vector<char> seen(c->cfg.max_requests, 0);
   long long rows = 0;
   int new_pages = 0;
@@ -956,6 +988,188 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   int e = launch_bf16_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws,
                              c->dec_wide, c->n_sm, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "bf16 decode launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+int oscar_weights_stride(const oscar_cache* c) {
+  if (!c || is_int2(c)) return 0;
+  return kPage * std::min(c->cfg.max_pages_per_request, c->cfg.max_pages);
+}
+
+size_t oscar_decode_weights_workspace_bytes(const oscar_cache* c) {
+  return c && c->planned && !is_int2(c) ? weights_workspace(c, c->dec_n_req).total : 0;
+}
+
+size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* c) {
+  return c && !is_int2(c) ? weights_workspace(c, c->cfg.max_requests).total : 0;
+}
+
+oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q, void* out, const float* weights_in,
+                                       float* weights_out, void* workspace, size_t ws_bytes, float* out_f32,
+                                       void* stream) {
+  g_launches = 0;
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_weights needs the BF16 format");
+  if (!c->planned) return fail(OSCAR_ERR_STATE, "no decode plan (plan after every append commit)");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (!q || !out || !weights_out || !workspace)
+    return fail(OSCAR_ERR_INVALID_ARG, "NULL q, out, weights_out or workspace");
+  if ((reinterpret_cast<uintptr_t>(weights_in) | reinterpret_cast<uintptr_t>(weights_out)) % 4)
+    return fail(OSCAR_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(OSCAR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const WeightsWorkspace w = weights_workspace(c, c->dec_n_req);
+  if (ws_bytes < w.total) return fail(OSCAR_ERR_INVALID_ARG, "workspace %zu < %zu bytes", ws_bytes, w.total);
+  oscar_status st = check_device(c);
+  if (st) return st;
+  const int e = launch_bf16_decode_weights(kernel_params(c), layer, q, out, out_f32, weights_in, weights_out,
+                                           static_cast<uint8_t*>(workspace), w, c->dec_wide, c->n_sm, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "decode with weights launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+oscar_status oscar_evict_begin(oscar_cache* c, const int* slots, const int* keep, int n_req, int n_sink, int n_recent,
+                               void* stream) {
+  if (!c || !slots || !keep || n_req <= 0 || n_req > c->cfg.max_requests)
+    return fail(OSCAR_ERR_INVALID_ARG, "bad evict arguments");
+  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "eviction needs the BF16 format");
+  if (c->reserved) return fail(OSCAR_ERR_STATE, "a reservation is pending");
+  if (c->evicting) return fail(OSCAR_ERR_STATE, "an eviction is pending");
+  if (n_sink < 0 || n_recent < 0) return fail(OSCAR_ERR_INVALID_ARG, "negative n_sink or n_recent");
+  std::vector<char> seen(c->cfg.max_requests, 0);
+  std::vector<EvictReq> reqs(n_req);
+  int new_pages = 0, max_pages = 0;
+  for (int i = 0; i < n_req; ++i) {
+    oscar_status st = check_slot(c, slots[i]);
+    if (st) return st;
+    if (seen[slots[i]]) return fail(OSCAR_ERR_INVALID_ARG, "slot %d listed twice", slots[i]);
+    seen[slots[i]] = 1;
+    if (keep[i] < 0) return fail(OSCAR_ERR_INVALID_ARG, "negative keep");
+    EvictReq& r = reqs[i];
+    r.slot = slots[i];
+    r.L = c->reqs[slots[i]].L;
+    r.keep = std::min(keep[i], r.L);
+    r.n_sink = std::min(n_sink, r.L);
+    r.n_recent = std::min(n_recent, r.L - r.n_sink);
+    if (r.keep < r.L && r.n_sink + r.n_recent > r.keep)
+      return fail(OSCAR_ERR_INVALID_ARG, "slot %d: keep %d < %d protected tokens", slots[i], r.keep, r.n_sink + r.n_recent);
+    if (r.keep < r.L) {
+      new_pages += ceil_div(r.keep, kPage);
+      max_pages = std::max(max_pages, ceil_div(r.keep, kPage));
+    }
+  }
+  if (new_pages > int(c->free_pages.size()))
+    return fail(OSCAR_ERR_OUT_OF_PAGES, "need %d pages, %zu free", new_pages, c->free_pages.size());
+  Upload u;
+  oscar_status st = begin_upload(c, &u);
+  if (st) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t row = size_t(c->cfg.max_pages_per_request);
+  int32_t* counts = reinterpret_cast<int32_t*>(u.staging);
+  counts[0] = n_req;
+  counts[1] = counts[2] = counts[3] = 0;
+  std::memcpy(u.staging + 256, reqs.data(), reqs.size() * sizeof(EvictReq));
+  std::vector<std::vector<int>> pages(n_req);
+  size_t at = c->free_pages.size();  // taken from the end; given out once the uploads are enqueued
+  for (int i = 0; i < n_req; ++i) {
+    if (reqs[i].keep >= reqs[i].L) continue;
+    for (int k = 0; k < ceil_div(reqs[i].keep, kPage); ++k) pages[i].push_back(c->free_pages[--at]);
+    if (pages[i].empty()) continue;
+    int32_t* src = u.rows + size_t(i) * row;
+    std::copy(pages[i].begin(), pages[i].end(), src);
+    CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.evict_pages + size_t(i) * row * 4, src, pages[i].size() * 4,
+                             cudaMemcpyHostToDevice, s));
+  }
+  CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.evict_plan, u.staging, 256 + reqs.size() * sizeof(EvictReq),
+                           cudaMemcpyHostToDevice, s));
+  st = end_upload(c, u, s);
+  if (st) return st;
+  c->free_pages.resize(at);
+  for (const auto& v : pages)
+    for (int p : v) c->refcount[p] = 1;
+  c->ev_reqs = std::move(reqs);
+  c->ev_pages = std::move(pages);
+  c->ev_max_pages = max_pages;
+  c->evicting = true;
+  return OSCAR_OK;
+}
+
+oscar_status oscar_evict(oscar_cache* c, int layer, const float* weights, float* weights_out, int* kept, void* stream) {
+  g_launches = 0;
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->evicting) return fail(OSCAR_ERR_STATE, "no eviction begun");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (!weights || !weights_out || !kept) return fail(OSCAR_ERR_INVALID_ARG, "NULL weights, weights_out or kept");
+  if (reinterpret_cast<uintptr_t>(weights) % 16) return fail(OSCAR_ERR_INVALID_ARG, "weights must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(weights_out) | reinterpret_cast<uintptr_t>(kept)) % 4)
+    return fail(OSCAR_ERR_INVALID_ARG, "weights_out and kept must be 4-byte aligned");
+  const uintptr_t bytes = uintptr_t(c->cfg.max_requests) * c->cfg.n_kv_heads * uintptr_t(oscar_weights_stride(c)) * 4;
+  const uintptr_t at[3] = {reinterpret_cast<uintptr_t>(weights), reinterpret_cast<uintptr_t>(weights_out),
+                           reinterpret_cast<uintptr_t>(kept)};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if (at[i] < at[j] + bytes && at[j] < at[i] + bytes)
+        return fail(OSCAR_ERR_INVALID_ARG, "weights, weights_out and kept must not overlap");
+  oscar_status st = check_device(c);
+  if (st) return st;
+  const int e = launch_evict(kernel_params(c), layer, weights, weights_out, kept, int(c->ev_reqs.size()), c->ev_max_pages,
+                             c->n_sm, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "evict launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+oscar_status oscar_evict_pages(const oscar_cache* c, int slot, int* pages, int n, int* n_pages) {
+  oscar_status st = check_slot(c, slot);
+  if (st) return st;
+  if (!c->evicting) return fail(OSCAR_ERR_STATE, "no eviction begun");
+  const std::vector<int>* v = &c->reqs[slot].pages;  // a request that gives nothing up keeps its pages
+  for (size_t i = 0; i < c->ev_reqs.size(); ++i)
+    if (c->ev_reqs[i].slot == slot && c->ev_reqs[i].keep < c->ev_reqs[i].L) v = &c->ev_pages[i];
+  if (n_pages) *n_pages = int(v->size());
+  if (n < 0 || (n > 0 && !pages)) return fail(OSCAR_ERR_INVALID_ARG, "bad page buffer");
+  std::copy(v->begin(), v->begin() + std::min<size_t>(size_t(n), v->size()), pages);
+  return OSCAR_OK;
+}
+
+oscar_status oscar_evict_commit(oscar_cache* c, void* stream) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->evicting) return fail(OSCAR_ERR_STATE, "no eviction begun");
+  Upload u;
+  oscar_status st = begin_upload(c, &u);
+  if (st) return st;
+  std::vector<int> changed;
+  for (size_t i = 0; i < c->ev_reqs.size(); ++i) {
+    const EvictReq& e = c->ev_reqs[i];
+    if (e.keep >= e.L) continue;
+    Request& r = c->reqs[e.slot];
+    for (int p : r.pages)
+      if (--c->refcount[p] == 0) c->free_pages.push_back(p);
+    r.pages = c->ev_pages[i];
+    r.L = r.H = e.keep;
+    int32_t* row = c->h_page_table + size_t(e.slot) * c->cfg.max_pages_per_request;
+    std::fill(row, row + c->cfg.max_pages_per_request, -1);
+    std::copy(r.pages.begin(), r.pages.end(), row);
+    changed.push_back(e.slot);
+  }
+  c->evicting = false;
+  c->ev_reqs.clear();
+  c->ev_pages.clear();
+  if (!changed.empty()) c->planned = false;  // lengths changed: plan again
+  st = upload_rows(c, u, changed, static_cast<cudaStream_t>(stream));
+  if (st) return st;
+  return end_upload(c, u, static_cast<cudaStream_t>(stream));
+}
+
+oscar_status oscar_evict_cancel(oscar_cache* c) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->evicting) return fail(OSCAR_ERR_STATE, "no eviction begun");
+  for (size_t i = c->ev_pages.size(); i-- > 0;)
+    for (size_t k = c->ev_pages[i].size(); k-- > 0;) {
+      c->refcount[c->ev_pages[i][k]] = 0;
+      c->free_pages.push_back(c->ev_pages[i][k]);
+    }
+  c->evicting = false;
+  c->ev_reqs.clear();
+  c->ev_pages.clear();
   return OSCAR_OK;
 }
 

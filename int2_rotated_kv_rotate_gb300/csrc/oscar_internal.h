@@ -80,6 +80,14 @@ OSCAR_HOST_DEVICE constexpr int decode_warps(int gqa, bool wide) { return gqa ==
 // covers nw tokens of the item's 16).
 OSCAR_HOST_DEVICE constexpr int append_task_split(int nw) { return 16 / nw; }
 
+// One request of an eviction plan (same for every layer): of its L tokens `keep` stay, the
+// first n_sink and the last n_recent of them in any case.  keep >= L: all stay where they are.
+struct EvictReq {
+  int slot;
+  int L, keep;
+  int n_sink, n_recent;
+};
+
 struct DeviceLayout {
   // pools (byte offsets in the device block)
   size_t codes, sz, sink, ring, bf16_pages;
@@ -103,6 +111,9 @@ struct DeviceLayout {
   size_t app_done;      // uint32 [layer][max_requests][H_kv][2]: append tasks of the running fused
                         // launch that have stored their sink and ring rows ([0]) and their INT2
                         // rows ([1]); the request's final merge takes the launch's count off again
+  // BF16 format: the eviction plan (int32 counts[4] at +0: requests; EvictReq at +256) and
+  // the new page ids of its requests, int32 [max_requests][max_pages_per_request]
+  size_t evict_plan, evict_pages;
   size_t max_append_items, max_decode_items;
   size_t total;
 };
@@ -114,6 +125,7 @@ struct KernelParams {
   int max_requests, max_pages, max_pages_per_request;
   uint32_t counter_polls;  // bounded waits on append-dependency counters give up after this many polls
   int v_cm;                // INT2 value pages channel-major (OSCAR_FORMAT_INT2_CM)
+  int weights_stride;      // BF16 format: tokens of a row of accumulated weights
   int folded;              // decode: q arrives rotated, the output stays rotated (OSCAR_PLAN_FOLDED_ROTATIONS)
   DeviceLayout lay;
 };
@@ -145,6 +157,25 @@ int launch_decode(const KernelParams& kp, int layer, const void* q, void* out, f
 // for it).
 int launch_bf16_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
                        const DecodeWorkspace& wl, bool deep, int n_sm, void* stream, int* launches);
+
+// BF16 decode that also adds each token's attention weight (summed over the query heads of
+// its kv-head) to weights_in (nullable: zero) into weights_out, fp32 [slot][kv-head]
+// [weights_stride]: the decode stores its scores (log2 units) in the workspace, a second
+// kernel turns them into probabilities once the softmax denominators are known.
+struct WeightsWorkspace {
+  size_t ml;        // float2 [plan request][H_q]: maximum (log2 units), 1 / denominator
+  size_t partials;  // as DecodeWorkspace, room for every plan
+  size_t scores;    // fp32 [plan request][kv-head][weights_stride][G]
+  size_t total;
+};
+int launch_bf16_decode_weights(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32,
+                               const float* weights_in, float* weights_out, uint8_t* ws, const WeightsWorkspace& wl,
+                               bool deep, int n_sm, void* stream, int* launches);
+
+// Eviction of one layer (evict.cu): kept int32 as the weights' shape.  max_keep_pages: the
+// most new pages of a request of the plan.
+int launch_evict(const KernelParams& kp, int layer, const float* weights, float* weights_out, int* kept, int n_req,
+                 int max_keep_pages, int n_sm, void* stream, int* launches);
 
 // CTAs of the decode kernel of this shape that fit on the GPU at once (occupancy x SMs);
 // the planner sizes work items so that one wave holds them all.
