@@ -184,6 +184,15 @@ oscar_status oscar_plan_decode(oscar_cache* cache, const int* slots, int n_req, 
  * the model).  The stored cache is the same; only the two matrix-vector products at the
  * ends of the decode are skipped. */
 #define OSCAR_PLAN_FOLDED_ROTATIONS 0x2u
+/* OSCAR_PLAN_SHARED_PREFIX (format OSCAR_FORMAT_BF16): requests of the plan whose page-table
+ * rows begin with the same pages (oscar_request_share_prefix, at any depth: a prefix under
+ * several longer ones) have those pages attended once for all of them, as one more launch
+ * of oscar_bf16_decode_attention before the decode's own; each request's further pages and
+ * the merge are as without the flag.  Results are those of the plan without it, up to the
+ * rounding of the sums.  A captured decode may be replayed under later plans that have the
+ * flag (or, without shared pages, do not); one captured without it may not be replayed
+ * under a plan with shared runs. */
+#define OSCAR_PLAN_SHARED_PREFIX 0x4u
 oscar_status oscar_plan_decode_ex(oscar_cache* cache, const int* slots, int n_req, int max_split_pages, uint32_t flags,
                                   void* stream);
 
@@ -198,6 +207,10 @@ size_t oscar_decode_workspace_max_bytes(const oscar_cache* cache);
 
 /* Number of split-K work items of the current plan, and of them BF16 (sink/ring) items. */
 oscar_status oscar_plan_info(const oscar_cache* cache, int* n_items, int* n_bf16_items, int* max_item_pages);
+
+/* Of a plan with OSCAR_PLAN_SHARED_PREFIX: the shared launch's work items, and the pages of
+ * a kv-head that it attends once for several requests (0 and 0 without sharing). */
+oscar_status oscar_plan_shared_info(const oscar_cache* cache, int* n_items, int* n_pages);
 
 /* Decode, step 2 (device, per layer): fused decode attention over the mixed-precision
  * cache ([OSCAR] §2.2-B): q~ = R_K^T q per query head; scores q~.k / sqrt(d) in the
@@ -245,7 +258,8 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const vo
  * planned requests; weights_in NULL counts as zeros and may be weights_out (it must not
  * overlap it otherwise).  Other entries of weights_out stay as they are.  The workspace
  * (oscar_decode_weights_workspace_bytes for the current plan, _max_bytes for every plan)
- * also holds the scores, 4 bytes a query head and token of a row.  Two launches. */
+ * also holds the scores, 4 bytes a query head and token of a row.  Two launches.  Not with
+ * a plan of OSCAR_PLAN_SHARED_PREFIX (OSCAR_ERR_STATE). */
 int oscar_weights_stride(const oscar_cache* cache);
 size_t oscar_decode_weights_workspace_bytes(const oscar_cache* cache);
 size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* cache);

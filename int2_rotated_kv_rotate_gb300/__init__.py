@@ -5,8 +5,9 @@ this package is a ctypes binding (_native), a torch-facing cache handle (cache),
 offline calibration step (calibrate), rotary positions (rotary) and seeded synthetic workloads (workloads).
 """
 from . import _native
-from ._native import OSCAR_FORMAT_BF16, OSCAR_FORMAT_INT2, OSCAR_FORMAT_INT2_CM, OscarError
+from ._native import OSCAR_FORMAT_BF16, OSCAR_FORMAT_INT2, OSCAR_FORMAT_INT2_CM, OSCAR_PLAN_SHARED_PREFIX, OscarError
 from .cache import KVCache
 from .rotary import RotaryEmbedding
 
-__all__ = ["KVCache", "RotaryEmbedding", "OscarError", "OSCAR_FORMAT_INT2", "OSCAR_FORMAT_INT2_CM", "OSCAR_FORMAT_BF16", "_native"]
+__all__ = ["KVCache", "RotaryEmbedding", "OscarError", "OSCAR_FORMAT_INT2", "OSCAR_FORMAT_INT2_CM", "OSCAR_FORMAT_BF16",
+           "OSCAR_PLAN_SHARED_PREFIX", "_native"]

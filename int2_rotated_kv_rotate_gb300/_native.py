@@ -62,7 +62,8 @@ EXPORTS = [
     "oscar_decode_workspace_max_bytes", "oscar_plan_info",
     "oscar_decode_attention", "oscar_append_decode_attention", "oscar_decode_attention_noalloc", "oscar_bf16_append",
     "oscar_bf16_decode_attention", "oscar_calibration_workspace_bytes", "oscar_calibrate_layer",
-    "oscar_rope_steps", "oscar_rope", "oscar_weights_stride", "oscar_decode_weights_workspace_bytes",
+    "oscar_rope_steps", "oscar_rope", "oscar_plan_shared_info", "oscar_weights_stride",
+    "oscar_decode_weights_workspace_bytes",
     "oscar_decode_weights_workspace_max_bytes", "oscar_bf16_decode_weights", "oscar_evict_begin", "oscar_evict",
     "oscar_evict_pages", "oscar_evict_commit", "oscar_evict_cancel",
     "oscar_set_wait_limit", "oscar_inject_fault", "oscar_get_status",
@@ -111,6 +112,7 @@ def lib() -> ctypes.CDLL:
                 "oscar_bf16_decode_attention": (I, [P, I, P, P, P, S, P, P]),
                 "oscar_calibration_workspace_bytes": (S, [I, I, I]),
                 "oscar_calibrate_layer": (I, [P, P, P, I, I, I, ctypes.c_longlong, I, P, P, P, P, P, P, S, P]),
+                "oscar_plan_shared_info": (I, [P, IP, IP]),
                 "oscar_weights_stride": (I, [P]),
                 "oscar_decode_weights_workspace_bytes": (S, [P]),
                 "oscar_decode_weights_workspace_max_bytes": (S, [P]),
@@ -254,6 +256,7 @@ def oscar_plan_decode(handle: int, slots, max_split_pages: int = 0, stream=None)
 
 OSCAR_PLAN_NARROW = 0x1
 OSCAR_PLAN_FOLDED_ROTATIONS = 0x2  # q arrives rotated (R_K folded into W_q), the output stays rotated
+OSCAR_PLAN_SHARED_PREFIX = 0x4  # BF16 format: pages that requests share are attended once for all of them
 
 
 def oscar_plan_decode_ex(handle: int, slots, max_split_pages: int = 0, flags: int = 0, stream=None) -> None:
@@ -297,6 +300,13 @@ def oscar_bf16_decode_attention(handle: int, layer: int, q, out, workspace, out_
     _check(lib().oscar_bf16_decode_attention(handle, layer, _ptr(q), _ptr(out), _ptr(workspace),
                                              workspace.numel() * workspace.element_size(), _ptr(out_f32),
                                              _stream(stream)))
+
+
+def oscar_plan_shared_info(handle: int):
+    """(work items, pages) that the plan attends once for several requests."""
+    a, b = ctypes.c_int(), ctypes.c_int()
+    _check(lib().oscar_plan_shared_info(handle, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
 
 
 def oscar_weights_stride(handle: int) -> int:

@@ -114,6 +114,10 @@ class KVCache:
     def plan_info(self):
         return N.oscar_plan_info(self.handle)
 
+    def shared_info(self):
+        """(work items, pages) that the plan attends once for several requests."""
+        return N.oscar_plan_shared_info(self.handle)
+
     def _check_decode(self, q, out, out_f32):
         shape = (self._n_plan, self.cfg.n_q_heads, self.cfg.head_dim)
         if tuple(q.shape) != shape or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != self.mem.device:

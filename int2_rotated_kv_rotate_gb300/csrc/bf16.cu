@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
         rowK, rowV, t0, t1, qs, part, smem, staged, nothing, keep);
 
     MergeAcc<G, 128> acc;
-    if (merge_partial<G, 128>(kp, it, partials, acc, s_last_p, smem, kBf16SlabSlots<G, NBUF>, smem_u32(slab_bar), slab_phase,
+    if (merge_partial<G, 128>(kp, it, it.head_count - dr.n_shared, partials, acc, s_last_p, smem, kBf16SlabSlots<G, NBUF>, smem_u32(slab_bar), slab_phase,
                               [] {})) {
       const int c = threadIdx.x;
 #pragma unroll

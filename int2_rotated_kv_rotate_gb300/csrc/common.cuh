@@ -457,9 +457,10 @@ __device__ void merge_slab(const uint8_t* slab, int n, MergeAcc<G, NTH>& acc) {
 // return false.  on_last() runs (all threads) as soon as this CTA knows it merges.  The
 // slots are bulk-copied into slab (shared, slab_slots of them per round) on the mbarrier
 // slab_bar (phase tracked in slab_phase); waits are bounded.  s_flag: one int of shared
-// memory.
+// memory.  `arrivals` items of the (request, kv-head) finish in this launch; the slots in
+// front of theirs, if any, were written by an earlier one.
 template <int G, int NTH, typename OnLast>
-__device__ bool merge_partial(const KernelParams& kp, const DecodeItem& it, const uint8_t* partials,
+__device__ bool merge_partial(const KernelParams& kp, const DecodeItem& it, int arrivals, const uint8_t* partials,
                               MergeAcc<G, NTH>& acc, int* s_flag, uint8_t* slab, int slab_slots, uint32_t slab_bar,
                               uint32_t& slab_phase, OnLast on_last) {
   constexpr int S = PartialSlot<G>::kBytes;
@@ -468,7 +469,7 @@ __device__ bool merge_partial(const KernelParams& kp, const DecodeItem& it, cons
   if (threadIdx.x == 0) {
     unsigned* hc = reinterpret_cast<unsigned*>(kp.base + kp.lay.counters) + size_t(it.req) * kp.n_kv_heads + it.kvh;
     const unsigned prev = atomic_add_acq_rel(hc, 1u);
-    *s_flag = prev == unsigned(it.head_count - 1);
+    *s_flag = prev == unsigned(arrivals - 1);
     if (*s_flag) *hc = 0u;  // every partial of (request, kv-head) has arrived
   }
   __syncthreads();

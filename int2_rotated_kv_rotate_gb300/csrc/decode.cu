@@ -1425,7 +1425,7 @@ __global__ void __launch_bounds__(Shape<NW>::NTH, Cfg<G, GROUP, NW, CM>::kPerSM)
     // ---- merge by the last CTA of (request, kv-head): R_V^T is fetched as soon as this CTA
     // knows it merges, the partial slots are bulk-copied after it
     MergeAcc<G, kThreads> acc;
-    if (merge_partial<G, kThreads>(kp, it, partials, acc, s_last, smem + C::kSlabOff, C::kSlabSlots,
+    if (merge_partial<G, kThreads>(kp, it, it.head_count, partials, acc, s_last, smem + C::kSlabOff, C::kSlabSlots,
                                    smem_u32(slab_bar), slab_phase,
                                    [&] {
                                      if (!folded) fetch_rvt(kp, layer, it.kvh, smem, smem_u32(merge_bar));

@@ -47,10 +47,13 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // offsets of the items inside a plan block (counts at 0, requests at 256)
 size_t append_items_offset(size_t reqs) { return 256 + align256(reqs * sizeof(AppendReq)); }
 size_t decode_items_offset(size_t reqs) { return 256 + align256(reqs * sizeof(DecodeReq)); }
+// offset of the items behind the order of a plan's shared runs
+size_t shared_items_offset(size_t reqs) { return align256(reqs * 4); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kAppendChunk = 16;     // tokens (or ring slots) per append work item
 constexpr int kMaxAppendTokenItems = 65536;
+constexpr int kSharedMinPages = 1;    // shorter shared runs stay with their requests' private items
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
 bool config_ok(const oscar_config* c, std::string* why) {
@@ -134,6 +137,11 @@ DeviceLayout compute_layout(const oscar_config& c) {
   L.decode_counts = L.decode_plan;
   L.decode_reqs = L.decode_plan + 256;
   L.decode_items = L.decode_plan + decode_items_offset(reqs);
+  if (c.format == OSCAR_FORMAT_BF16) {
+    L.max_shared_items = 16384;
+    L.shared_order = take(shared_items_offset(reqs) + L.max_shared_items * sizeof(SharedItem));
+    L.shared_items = L.shared_order + shared_items_offset(reqs);
+  }
   L.sched = take(16);
   L.app_done = take(layers * reqs * Hkv * 8);
   L.total = off;
@@ -182,6 +190,10 @@ struct oscar_cache {
   // decode plan
   bool planned = false;
   bool planned_with_reservation = false;  // the plan already counts the reserved tokens
+  bool dec_shared = false;  // OSCAR_PLAN_SHARED_PREFIX: the shared launch goes before the decode's
+  int dec_shared_items = 0, dec_shared_pages = 0;
+  bool map_ready = false;
+  alignas(64) unsigned char page_map[128];  // tensor map of the BF16 page pool
   int dec_n_req = 0, dec_items = 0, dec_bf16_items = 0, dec_max_pages = 0;
   DecodeWorkspace ws{};
   int device = 0;              // the device current at creation (the device of `base`)
@@ -291,6 +303,89 @@ oscar_status check_device(const oscar_cache* c) {
   return OSCAR_OK;
 }
 
+// The runs of pages that several requests of a plan map, as work items of the shared launch.
+struct SharedRuns {
+  std::vector<int> order;          // plan indices; the members of every run are neighbours
+  std::vector<int> first_private;  // per plan index: pages before it are in shared runs
+  std::vector<int> n_segs;         // per plan index: partial slots per head of its shared runs
+  std::vector<SharedItem> items;
+  int pages = 0;                   // pages attended once for several requests
+};
+
+SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::vector<int>& Ls) {
+  SharedRuns out;
+  const int n = int(Ls.size()), Hkv = c->cfg.n_kv_heads, G = c->cfg.n_q_heads / Hkv;
+  out.order.resize(n);
+  for (int i = 0; i < n; ++i) out.order[i] = i;
+  out.first_private.assign(n, 0);
+  out.n_segs.assign(n, 0);
+  // page p of plan index i, -1 past its whole pages (only whole pages are shared)
+  auto page = [&](int i, int p) {
+    const std::vector<int>& v = c->reqs[slots[i]].pages;
+    return p < Ls[i] / kPage && p < int(v.size()) ? v[p] : -1;
+  };
+  // Runs form a forest: the members of one that part ways in ever smaller sets.
+  struct Run {
+    int lo, hi, begin, end, parent;
+  };
+  struct Group {
+    int lo, hi, begin, parent;
+  };
+  std::vector<Run> runs;
+  std::vector<Group> todo{{0, n, 0, -1}};
+  while (!todo.empty()) {
+    const Group g = todo.back();
+    todo.pop_back();
+    if (g.hi - g.lo < 2) continue;
+    int end = g.begin, parent = g.parent;
+    for (int first; (first = page(out.order[g.lo], end)) >= 0; ++end) {
+      bool same = true;
+      for (int k = g.lo + 1; same && k < g.hi; ++k) same = page(out.order[k], end) == first;
+      if (!same) break;
+    }
+    if (end > g.begin) {
+      if (end - g.begin < kSharedMinPages) continue;
+      runs.push_back({g.lo, g.hi, g.begin, end, g.parent});
+      parent = int(runs.size()) - 1;
+      for (int k = g.lo; k < g.hi; ++k) out.first_private[out.order[k]] = end;
+    }
+    std::stable_sort(out.order.begin() + g.lo, out.order.begin() + g.hi,
+                     [&](int a, int b) { return page(a, end) < page(b, end); });
+    for (int lo = g.lo; lo < g.hi;) {
+      const int p = page(out.order[lo], end);
+      int hi = lo + 1;
+      while (hi < g.hi && page(out.order[hi], end) == p) ++hi;
+      if (p >= 0 && hi - lo > 1) todo.push_back({lo, hi, end, parent});
+      lo = hi;
+    }
+  }
+  // One wave of items, one a CTA; the row blocks of a run's pages are items of their own.
+  const int per_item = kSharedRows / G;  // members of an item at most
+  auto count = [&](int chunk) {
+    long long items = 0;
+    for (const Run& r : runs) items += (long long)Hkv * ceil_div(r.hi - r.lo, per_item) * ceil_div(r.end - r.begin, chunk);
+    return items;
+  };
+  int chunk = 1, longest = 1;
+  for (const Run& r : runs) longest = std::max(longest, r.end - r.begin);
+  chunk = int(std::min<long long>(longest, std::max<long long>(2, (count(1) + c->n_sm - 1) / c->n_sm)));
+  while (chunk < longest && count(chunk) > c->n_sm) ++chunk;
+  std::vector<int> seg_end(runs.size());
+  for (size_t k = 0; k < runs.size(); ++k) {  // parents come before their children
+    const Run& r = runs[k];
+    const int seg0 = r.parent < 0 ? 0 : seg_end[r.parent], segs = ceil_div(r.end - r.begin, chunk);
+    seg_end[k] = seg0 + segs;
+    out.pages += r.end - r.begin;
+    for (int m = r.lo; m < r.hi; ++m) out.n_segs[out.order[m]] = seg_end[k];
+    for (int s = 0; s < segs; ++s)
+      for (int h = 0; h < Hkv; ++h)
+        for (int lo = r.lo; lo < r.hi; lo += per_item)
+          out.items.push_back({lo, std::min(r.hi, lo + per_item), r.begin + s * chunk,
+                               std::min(r.end, r.begin + (s + 1) * chunk), h, seg0 + s});
+  }
+  return out;
+}
+
 // Workspace of a decode with weights over n_req requests.  Only the total depends on the
 // plan: a captured launch keeps its offsets.
 WeightsWorkspace weights_workspace(const oscar_cache* c, int n_req) {
@@ -345,6 +440,8 @@ oscar_status oscar_cache_create(const oscar_config* cfg, void* device_mem, size_
   // a plan block's image (the larger of the two)
   c->staging_bytes = std::max(append_items_offset(cfg->max_requests) + lay.max_append_items * sizeof(AppendItem),
                               decode_items_offset(cfg->max_requests) + lay.max_decode_items * sizeof(DecodeItem));
+  if (cfg->format == OSCAR_FORMAT_BF16)  // a plan's shared runs go up behind its items
+    c->staging_bytes += 256 + shared_items_offset(cfg->max_requests) + lay.max_shared_items * sizeof(SharedItem);
   c->upload_bytes = align256(pt_bytes) + align256(c->staging_bytes);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&c->h_page_table), pt_bytes);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&c->h_upload), kUploadSlots * c->upload_bytes);
@@ -688,10 +785,13 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
                                   void* stream) {
   if (!c || !slots || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad plan arguments");
-  if (flags & ~(OSCAR_PLAN_NARROW | OSCAR_PLAN_FOLDED_ROTATIONS))
+  if (flags & ~(OSCAR_PLAN_NARROW | OSCAR_PLAN_FOLDED_ROTATIONS | OSCAR_PLAN_SHARED_PREFIX))
     return fail(OSCAR_ERR_INVALID_ARG, "unknown plan flags %#x", flags);
   if ((flags & OSCAR_PLAN_FOLDED_ROTATIONS) && !is_int2(c))
     return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_FOLDED_ROTATIONS applies to the INT2 formats");
+  const bool shared = (flags & OSCAR_PLAN_SHARED_PREFIX) != 0;
+  if (shared && is_int2(c))
+    return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_SHARED_PREFIX applies to the BF16 format");
   if (max_split_pages < 0) return fail(OSCAR_ERR_INVALID_ARG, "max_split_pages < 0");
   std::vector<char> seen(c->cfg.max_requests, 0);
   const int Hkv = c->cfg.n_kv_heads, S = is_int2(c) ? c->cfg.n_sink : 0;
@@ -721,8 +821,25 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
           ++n_reserved_planned;
         }
       }
-    total_pages += (long long)Hkv * pages_needed(c, Ls[i], Hs[i]);
   }
+  SharedRuns runs;
+  if (shared) {
+    if (!c->map_ready) {
+      const unsigned long long rows = 2ull * kPage * c->cfg.n_layers * c->cfg.max_pages * Hkv;
+      if (rows > 0x7fffffffull)
+        return fail(OSCAR_ERR_UNSUPPORTED, "OSCAR_PLAN_SHARED_PREFIX: a pool of %llu rows is too large", rows);
+      const int e = encode_page_map(kernel_params(c), c->page_map);
+      if (e) return fail(OSCAR_ERR_CUDA, "tensor map of the page pool: %s", cudaGetErrorString(cudaError_t(e)));
+      c->map_ready = true;
+    }
+    runs = find_shared_runs(c, slots, Ls);
+    if (runs.items.size() > c->lay.max_shared_items)
+      return fail(OSCAR_ERR_INVALID_ARG, "plan of %zu shared items exceeds %zu", runs.items.size(), c->lay.max_shared_items);
+  } else {
+    runs.first_private.assign(n_req, 0);
+    runs.n_segs.assign(n_req, 0);
+  }
+  for (int i = 0; i < n_req; ++i) total_pages += (long long)Hkv * (pages_needed(c, Ls[i], Hs[i]) - runs.first_private[i]);
   // Work items: per (request, kv-head) the BF16 sink+ring items and page ranges of
   // `chunk` pages.  Automatic chunk, from the bytes each resident CTA would stream:
   //  - small steps (latency-bound): the smallest chunk that lets one wave of resident CTAs
@@ -733,6 +850,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   // Per request: INT2 pages np, BF16 sink+ring tokens n_bf, and the split points of the
   // items that do not (before) and may (after) read rows of this step's append: bf_new in
   // the BF16 list, pg_new in the pages.
+  // Pages before p0_of, attended by the shared launch, are not counted.
+  const std::vector<int>& p0_of = runs.first_private;
   std::vector<int> np_of(n_req), nbf_of(n_req), bfnew_of(n_req), pgnew_of(n_req);
   int max_np = 1;
   const int ng = kHeadDim / (is_int2(c) ? c->cfg.group : kHeadDim);
@@ -748,8 +867,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
     // eviction rows are signalled before the launch's wait, and the one warp whose page
     // holds them waits for that signal before copying it.
     if (app_items[i] > 0) bfnew_of[i] = 0;
-    max_np = std::max(max_np, np_of[i]);
-    total_bytes += (long long)Hkv * (np_of[i] * page_bytes + nbf_of[i] * 2LL * kHeadDim * 2);
+    max_np = std::max(max_np, np_of[i] - p0_of[i]);
+    total_bytes += (long long)Hkv * ((np_of[i] - p0_of[i]) * page_bytes + nbf_of[i] * 2LL * kHeadDim * 2);
   }
   // CTA shape: at GQA 4 a step that one wave of 16-warp CTAs holds (one per SM) is planned
   // for them ("wide"); larger steps for 8-warp CTAs, two per SM.
@@ -782,7 +901,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   auto count_items = [&](int ch) {
     long long n = n_bf_items;
     for (int i = 0; i < n_req; ++i) {
-      const int pg = split_count(pgnew_of[i], np_of[i], ch);
+      const int pg = split_count(pgnew_of[i] - p0_of[i], np_of[i] - p0_of[i], ch);
       const int bf = split_count(bfnew_of[i], nbf_of[i], bf_item);
       n += (long long)Hkv * (pg + bf > 0 ? pg : 1);
     }
@@ -810,7 +929,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   }
   std::vector<DecodeReq> reqs(n_req);
   std::vector<DecodeItem> items;
-  int n_bf16 = 0, max_pages = 0;
+  int n_bf16 = 0, max_pages = 0, n_slots = 0;
   for (int i = 0; i < n_req; ++i) {
     DecodeReq& q = reqs[i];
     q.slot = slots[i];
@@ -818,7 +937,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
     q.H = is_int2(c) ? Hs[i] : Ls[i];
     q.H_pre = is_int2(c) ? Hpre[i] : Lpre[i];
     q.app_expect = is_int2(c) ? app_expect[i] : 0;
-    const int np = np_of[i], n_bf = nbf_of[i], bf_new = bfnew_of[i], pg_new = pgnew_of[i];
+    const int np = np_of[i], n_bf = nbf_of[i], bf_new = bfnew_of[i], pg_new = pgnew_of[i], page0 = p0_of[i];
     // BF16 list index of this step's first new row (index < min(L, S): sink, else ring
     // position H + index - min(L, S)); rows before it are final before the launch's wait
     int u_new = n_bf;
@@ -826,13 +945,17 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       const int n_s = std::min(q.L, S);
       u_new = std::min(n_bf, Lpre[i] < n_s ? Lpre[i] : n_s + std::max(0, Lpre[i] - q.H));
     }
-    q.first_item = int(items.size());
+    q.first_item = n_slots;
+    q.n_shared = runs.n_segs[i];
     for (int h = 0; h < Hkv; ++h) {
-      const int first = int(items.size());
+      const size_t first = items.size();
+      const int first_slot = n_slots;
+      n_slots += q.n_shared;
       auto add = [&](int kind, int b, int e, int dep) {
-        items.push_back({i, h, kind, b, e, first, 0, dep, kind == 1 ? std::min(e, std::max(b, u_new)) : e});
+        items.push_back({i, h, kind, b, e, first_slot, 0, dep, kind == 1 ? std::min(e, std::max(b, u_new)) : e, n_slots++});
       };
-      if (n_bf == 0 && np == 0) add(1, 0, 0, kDepNone);  // empty request: one empty item writes zeros
+      // no private tokens: one empty item, which merges (an empty request's writes zeros)
+      if (n_bf == 0 && np == page0) add(1, 0, 0, kDepNone);
       // BF16 sink+ring list, split where this step's new tokens start (those items wait for
       // a fused launch's append tasks; the others do not)
       for (int part = 0; part < 2; ++part) {
@@ -844,18 +967,18 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       }
       // INT2 pages, split where pages that this step's append writes begin
       for (int part = 0; part < 2; ++part) {
-        const int p0 = part == 0 ? 0 : pg_new, p1 = part == 0 ? pg_new : np;
+        const int p0 = part == 0 ? page0 : pg_new, p1 = part == 0 ? pg_new : np;
         for (int p = p0; p < p1; p += chunk) {
           add(0, p, std::min(p1, p + chunk), part == 0 ? kDepNone : kDepPages);
           max_pages = std::max(max_pages, std::min(p1, p + chunk) - p);
         }
       }
-      for (size_t k = first; k < items.size(); ++k) items[k].head_count = int(items.size()) - first;
+      for (size_t k = first; k < items.size(); ++k) items[k].head_count = n_slots - first_slot;
     }
-    q.items_per_head = (int(items.size()) - q.first_item) / Hkv;
+    q.items_per_head = (n_slots - q.first_item) / Hkv;
   }
-  if (items.size() > c->lay.max_decode_items)
-    return fail(OSCAR_ERR_INVALID_ARG, "plan of %zu items exceeds %zu; raise max_split_pages", items.size(),
+  if (size_t(n_slots) > c->lay.max_decode_items)
+    return fail(OSCAR_ERR_INVALID_ARG, "plan of %d items exceeds %zu; raise max_split_pages", n_slots,
                 c->lay.max_decode_items);
   // the order CTAs take items in (when they are more than one wave): the items that wait
   // on no append task first, then those that may wait; largest first within each (stable)
@@ -882,12 +1005,17 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   counts[0] = int(items.size());
   counts[1] = n_req;
   counts[2] = n_front;
-  counts[3] = 0;
+  counts[3] = int(runs.items.size());
   std::memcpy(u.staging + 256, reqs.data(), reqs.size() * sizeof(DecodeReq));
   DecodeItem* staged = reinterpret_cast<DecodeItem*>(u.staging + items_off);
-  for (size_t k = 0; k < order.size(); ++k) {
-    staged[k] = items[order[k]];
-    staged[k].slot = order[k];
+  for (size_t k = 0; k < order.size(); ++k) staged[k] = items[order[k]];
+  if (!runs.items.empty()) {
+    const size_t at = shared_items_offset(c->cfg.max_requests);
+    uint8_t* to = u.staging + align256(items_off + items.size() * sizeof(DecodeItem));
+    std::memcpy(to, runs.order.data(), runs.order.size() * 4);
+    std::memcpy(to + at, runs.items.data(), runs.items.size() * sizeof(SharedItem));
+    CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.shared_order, to, at + runs.items.size() * sizeof(SharedItem),
+                             cudaMemcpyHostToDevice, s));
   }
   CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.decode_plan, u.staging, items_off + items.size() * sizeof(DecodeItem),
                            cudaMemcpyHostToDevice, s));
@@ -896,7 +1024,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   DecodeWorkspace w;
   size_t off = 0;
   w.partials = off;
-  off = align256(off + items.size() * size_t(G) * (8 + 4 * kHeadDim));  // partial slots
+  off = align256(off + size_t(n_slots) * size_t(G) * (8 + 4 * kHeadDim));  // partial slots
   w.total = off;
   c->ws = w;
   c->dec_n_req = n_req;
@@ -907,6 +1035,9 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   c->planned_with_reservation = c->reserved;
   c->dec_wide = wide;
   c->dec_folded = (flags & OSCAR_PLAN_FOLDED_ROTATIONS) != 0;
+  c->dec_shared = shared;
+  c->dec_shared_items = int(runs.items.size());
+  c->dec_shared_pages = runs.pages;
   c->plan_covers_reservation = c->reserved && n_reserved_planned == int(c->app_reqs.size());
   return OSCAR_OK;
 }
@@ -925,6 +1056,14 @@ oscar_status oscar_plan_info(const oscar_cache* c, int* n_items, int* n_bf16_ite
   if (n_items) *n_items = c->dec_items;
   if (n_bf16_items) *n_bf16_items = c->dec_bf16_items;
   if (max_item_pages) *max_item_pages = c->dec_max_pages;
+  return OSCAR_OK;
+}
+
+oscar_status oscar_plan_shared_info(const oscar_cache* c, int* n_items, int* n_pages) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->planned) return fail(OSCAR_ERR_STATE, "no decode plan");
+  if (n_items) *n_items = c->dec_shared_items;
+  if (n_pages) *n_pages = c->dec_shared_pages;
   return OSCAR_OK;
 }
 
@@ -985,8 +1124,16 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   oscar_status st = check_decode(c, layer, q, out, workspace, ws_bytes);
   if (st) return st;
   if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_attention needs the BF16 format");
-  int e = launch_bf16_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws,
-                             c->dec_wide, c->n_sm, stream, &g_launches);
+  int e = 0;
+  if (c->dec_shared) {
+    st = check_device(c);
+    if (st) return st;
+    e = launch_shared(kernel_params(c), layer, c->page_map, q, static_cast<uint8_t*>(workspace) + c->ws.partials, c->n_sm,
+                      stream, &g_launches);
+  }
+  if (!e)
+    e = launch_bf16_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws, c->dec_wide,
+                           c->n_sm, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "bf16 decode launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }
@@ -1012,6 +1159,8 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q,
   if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_weights needs the BF16 format");
   if (!c->planned) return fail(OSCAR_ERR_STATE, "no decode plan (plan after every append commit)");
   if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (c->dec_shared)
+    return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_weights needs a plan without OSCAR_PLAN_SHARED_PREFIX");
   if (!q || !out || !weights_out || !workspace)
     return fail(OSCAR_ERR_INVALID_ARG, "NULL q, out, weights_out or workspace");
   if ((reinterpret_cast<uintptr_t>(weights_in) | reinterpret_cast<uintptr_t>(weights_out)) % 4)

@@ -44,6 +44,18 @@ struct DecodeReq {
                      // V, times append_task_split, per append item); 0 = nothing to wait for
   int first_item;    // items of this request, kv-head-major: first_item + kvh*items_per_head ..
   int items_per_head;
+  int n_shared;      // of each head's partial slots, the first n_shared are the shared launch's
+};
+
+// One work item of the launch that attends shared runs (BF16 format): pages [begin, end) of
+// kv-head kvh for the requests order[lo .. hi), who map the same pages there; member i's
+// partial slot is its head's first + seg.
+constexpr int kSharedRows = 256;  // query rows (members x G) of an item at most
+struct SharedItem {
+  int lo, hi;
+  int begin, end;
+  int kvh;
+  int seg;
 };
 
 // One split-K work item: pages [p0, p1) of the INT2 history (kind 0) or BF16 tokens
@@ -114,6 +126,10 @@ struct DeviceLayout {
   // BF16 format: the eviction plan (int32 counts[4] at +0: requests; EvictReq at +256) and
   // the new page ids of its requests, int32 [max_requests][max_pages_per_request]
   size_t evict_plan, evict_pages;
+  // BF16 format: the shared runs of the decode plan, uploaded as one block: int32
+  // order[max_requests] (plan indices) and the items, whose number is decode counts [3]
+  size_t shared_order, shared_items;
+  size_t max_shared_items;
   size_t max_append_items, max_decode_items;
   size_t total;
 };
@@ -171,6 +187,12 @@ struct WeightsWorkspace {
 int launch_bf16_decode_weights(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32,
                                const float* weights_in, float* weights_out, uint8_t* ws, const WeightsWorkspace& wl,
                                bool deep, int n_sm, void* stream, int* launches);
+
+// The launch that attends a plan's shared runs (shared.cu), before launch_bf16_decode; map:
+// the 128 bytes that encode_page_map wrote.
+int encode_page_map(const KernelParams& kp, void* map);
+int launch_shared(const KernelParams& kp, int layer, const void* map, const void* q, uint8_t* partials, int n_sm,
+                  void* stream, int* launches);
 
 // Eviction of one layer (evict.cu): kept int32 as the weights' shape.  max_keep_pages: the
 // most new pages of a request of the plan.

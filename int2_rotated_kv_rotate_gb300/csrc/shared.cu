@@ -1,0 +1,387 @@
+// Decode attention over the runs of BF16 pages that several requests of a plan share: each
+// run is read once for all of them.  The launch comes before the decode's own and writes the
+// partial slots (maximum, denominator, output) that the decode's merge then joins with each
+// request's private items.
+//
+// An item is a range of pages of one kv-head and up to 256 query rows: the G heads of the
+// members that share it, 128 rows a block.  Per 64-token page, on the tcgen05 tensor cores:
+//   S = Q K^T      M = 128 rows, N = 64 tokens, K = 128 channels: Q and the page's keys in
+//                  shared memory, 128-byte swizzle, S in tensor memory;
+//   P = 2^(S - m)  one thread a row: the whole row of the page in registers, so its maximum
+//                  and sum need no other thread; P goes back over S as bf16 hi and lo halves
+//                  (16 bits, as the private items keep);
+//   O += P V       M = 128, N = 128 channels, K = 64 tokens, hi then lo: P from tensor memory,
+//                  the page's values in shared memory as they are stored (channels contiguous).
+// The reference m of a row moves only when a score exceeds it by more than 8 (base 2), so
+// p <= 2^8 and O is rarely rescaled in tensor memory.
+//
+// Roles: warp 0 copies pages (TMA, kStages of them in flight), warp 1 issues the MMAs, warps
+// 4-7 and 8-11 are the softmax of row blocks 0 and 1.  S of the next page is computed while
+// the softmax works on this one (two S / P buffers a block, 512 tensor-memory columns in
+// all).  Bound by HBM up to some 256 rows: a page is 32 KB, 1470 cycles of an SM's share of
+// the copy rate, against 900 cycles of tensor core and shared memory for one block.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "oscar_internal.h"
+#include "tmem.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kBlockRows = 128;
+constexpr int kPageKv = 2 * kPage * kHeadDim * 2;         // bytes of a page's K and V rows of a head
+constexpr int kQBlock = kBlockRows * kHeadDim * 2;        // bytes of a row block of Q
+constexpr int kThreads = 384;
+constexpr int kBlocks = kSharedRows / kBlockRows;
+static_assert(kBlocks == 2, "warps 4-7 and 8-11");
+
+struct Control {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[kBlocks];
+  uint64_t s_full[kBlocks][2], p_full[kBlocks][2];
+  uint64_t o_done[kBlocks];  // one completion a page: O holds the pages so far, P is read
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kOffStages = kBlocks * kQBlock;
+constexpr int kOffControl = kOffStages + kStages * kPageKv;
+constexpr int kSmemBytes = kOffControl + int(sizeof(Control)) + 1024;  // + alignment to 1024
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+// Tensor-memory columns of block b: two S / P buffers of 64, then O of 128.
+constexpr uint32_t kBlockCols = 256, kColO = 128;
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Everything a role needs of an item.
+struct Work {
+  SharedItem it;
+  int rows, blocks, pages;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_kernel(KernelParams kp, int layer, const __grid_constant__ CUtensorMap map, const uint16_t* __restrict__ q,
+                  uint8_t* __restrict__ partials) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Control* ctl = reinterpret_cast<Control*>(smem + kOffControl);
+  const uint32_t sq = smem_u32(smem), sst = sq + kOffStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int b = 0; b < kBlocks; ++b) {
+      mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(smem_u32(&ctl->s_full[b][k]), 1);
+        mbar_init(smem_u32(&ctl->p_full[b][k]), kBlockRows);
+      }
+      mbar_init(smem_u32(&ctl->o_done[b]), 1);
+    }
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem::alloc(smem_u32(&ctl->tmem), 512);
+  tmem::fence_before();
+  __syncthreads();
+  tmem::fence_after();
+  const uint32_t tm = ctl->tmem;
+  pdl_wait();
+  pdl_trigger();
+  const int n_items = reinterpret_cast<const int*>(kp.base + kp.lay.decode_counts)[3];
+  const DecodeReq* reqs = reinterpret_cast<const DecodeReq*>(kp.base + kp.lay.decode_reqs);
+  const int* order = reinterpret_cast<const int*>(kp.base + kp.lay.shared_order);
+  const SharedItem* items = reinterpret_cast<const SharedItem*>(kp.base + kp.lay.shared_items);
+  auto load_work = [&](int ix) {
+    Work w;
+    w.it = items[ix];
+    w.rows = (w.it.hi - w.it.lo) * kp.gqa;
+    w.blocks = (w.rows + kBlockRows - 1) / kBlockRows;
+    w.pages = w.it.end - w.it.begin;
+    return w;
+  };
+  // Bounded wait of a whole warp for completion `index` of a barrier; once one runs out,
+  // every role leaves its loop.
+  auto wait = [&](uint64_t& bar, uint32_t index) -> bool {
+    const uint32_t a = smem_u32(&bar);
+    bool done = false;
+    for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+      done = mbar_try_wait_for(a, index & 1u, 1000000u);
+      if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+    }
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (lane == 0) {
+      *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+      flag(kp, OSCAR_FLAG_TIMEOUT);
+    }
+    return false;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- pages
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      const int slot = reqs[order[w.it.lo]].slot;  // every member maps the same pages
+      const bool slot_ok = slot >= 0 && slot < kp.max_requests;
+      if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
+      const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
+                        size_t(slot_ok ? slot : 0) * kp.max_pages_per_request;
+      for (int p = 0; p < w.pages; ++p, ++cnt) {
+        const uint32_t st = cnt % kStages;
+        if (cnt >= kStages && !wait(ctl->empty[st], cnt / kStages - 1)) {
+          ok = false;
+          break;
+        }
+        int phys = w.it.begin + p < kp.max_pages_per_request ? ptab[w.it.begin + p] : -1;
+        if (phys < 0 || phys >= kp.max_pages) {  // page 0 instead, and the flag
+          if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+          phys = 0;
+        }
+        const int y = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&ctl->full[st]), dst = sst + st * kPageKv;
+          mbar_expect_tx(bar, kPageKv);
+          tma_load(dst, &map, 0, y, bar);
+          tma_load(dst + 8192, &map, 64, y, bar);
+          tma_load(dst + 16384, &map, 0, y + kPage, bar);
+          tma_load(dst + 24576, &map, 64, y + kPage, bar);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok)  // copies still in flight land before the CTA leaves
+      for (uint32_t k = cnt > kStages ? cnt - kStages : 0; k < cnt; ++k)
+        mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
+    constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
+    uint32_t cnt = 0, qn[kBlocks] = {0, 0}, sn[kBlocks] = {0, 0};  // pages; items and pages of each block
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      for (int b = 0; ok && b < w.blocks; ++b) ok = wait(ctl->q_full[b], qn[b]++);
+      for (int i = 0; ok && i <= w.pages; ++i) {
+        if (i < w.pages) {
+          const uint32_t st = (cnt + i) % kStages;
+          ok = wait(ctl->full[st], (cnt + i) / kStages);
+          for (int b = 0; ok && b < w.blocks; ++b) {
+            const uint32_t n = sn[b] + i;
+            // the buffer's last P (page n - 2) has been read
+            if (n >= 2) ok = wait(ctl->o_done[b], n - 2);
+            if (!ok) break;
+            tmem::fence_after();
+            if (elect_one()) {
+              const uint32_t d = tm + b * kBlockCols + (n & 1) * kPage;
+              const uint32_t qa = sq + b * kQBlock, ka = sst + st * kPageKv;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tmem::mma_ss(d, tmem::sdesc_sw128(qa + (k >> 2) * (kQBlock / 2) + (k & 3) * 32, 16, 1024),
+                             tmem::sdesc_sw128(ka + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), kIdS, k > 0);
+              tmem::commit(smem_u32(&ctl->s_full[b][n & 1]));
+            }
+            __syncwarp();
+          }
+        }
+        if (ok && i > 0) {
+          const uint32_t st = (cnt + i - 1) % kStages;
+          for (int b = 0; ok && b < w.blocks; ++b) {
+            const uint32_t n = sn[b] + i - 1;
+            ok = wait(ctl->p_full[b][n & 1], n >> 1);
+            if (!ok) break;
+            tmem::fence_after();
+            if (elect_one()) {
+              const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + (n & 1) * kPage;
+              const uint32_t va = sst + st * kPageKv + 16384;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // hi then lo
+                tmem::mma_ts(d, a + 8 * k, tmem::sdesc_sw128(va + (k & 3) * 2048, 8192, 1024), kIdO, i > 1 || k > 0);
+              tmem::commit(smem_u32(&ctl->o_done[b]));
+              if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      cnt += w.pages;
+      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages;
+    }
+    if (!ok) {  // MMAs in flight end before the tensor memory is freed
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain));
+      __syncwarp();
+      mbar_wait(smem_u32(&ctl->drain), 0);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax of block b
+    const int b = (warp - 4) >> 2, wq = warp & 3, r = (wq << 5) | lane;
+    const float scale = kLog2e * rsqrtf(float(kHeadDim));
+    const uint32_t tl = tm + b * kBlockCols + (uint32_t(32 * wq) << 16);
+    const int G = kp.gqa;
+    uint32_t n = 0;  // pages of this block so far
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      if (b >= w.blocks) continue;
+      // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
+      for (int k = 0; k < 16; ++k) {
+        const int row = 32 * wq + 2 * k + (lane >> 4), c = lane & 15, m = b * kBlockRows + row;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (m < w.rows) {
+          const int req = order[w.it.lo + m / G];
+          v = reinterpret_cast<const uint4*>(q + (size_t(req) * kp.n_q_heads + size_t(w.it.kvh) * G + m % G) * kHeadDim)[c];
+        }
+        *reinterpret_cast<uint4*>(smem + b * kQBlock + (c >> 3) * (kQBlock / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+      }
+      fence_proxy_async();
+      mbar_arrive(smem_u32(&ctl->q_full[b]));
+      float m_ref = -INFINITY, l = 0.f;
+      for (int i = 0; i < w.pages; ++i, ++n) {
+        const uint32_t buf = tl + (n & 1) * kPage;
+        ok = wait(ctl->s_full[b][n & 1], n >> 1);
+        if (!ok) break;
+        tmem::fence_after();
+        uint32_t s0[32], s1[32];
+        tmem::ld_x32(buf, s0);
+        tmem::ld_x32(buf + 32, s1);
+        tmem::wait_ld();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        mx *= scale;
+        const bool raise = mx > m_ref + 8.f;  // also from -inf
+        if (i == 0) {
+          m_ref = mx;
+        } else if (__any_sync(0xffffffffu, raise)) {
+          ok = wait(ctl->o_done[b], n - 1);  // (S of page n was issued after completion n - 2)
+          if (!ok) break;
+          tmem::fence_after();
+          const float f = raise ? ex2(m_ref - mx) : 1.f;
+          if (raise) m_ref = mx;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < kHeadDim; c += 32) {
+            uint32_t o[32];
+            tmem::ld_x32(tl + kColO + c, o);
+            tmem::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem::st_x32(tl + kColO + c, o);
+          }
+        }
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        uint32_t hi[32], lo[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
+          const float pa = ex2(fmaf(__uint_as_float(s[0]), scale, -ref)), pb = ex2(fmaf(__uint_as_float(s[1]), scale, -ref));
+          l += pa + pb;
+          hi[j] = pack_bf16(pa, pb);
+          lo[j] = pack_bf16(pa - bf16_lo(hi[j]), pb - bf16_hi(hi[j]));
+        }
+        tmem::st_x32(buf, hi);
+        tmem::st_x32(buf + 32, lo);
+        tmem::wait_st();
+        tmem::fence_before();
+        mbar_arrive(smem_u32(&ctl->p_full[b][n & 1]));
+      }
+      if (!ok) break;
+      // ---- the rows' partials
+      // (a parity tells a completion from its neighbours only: the last but one first, which
+      // no page of this item may have waited for)
+      ok = n < 2 || wait(ctl->o_done[b], n - 2);
+      if (ok) ok = wait(ctl->o_done[b], n - 1);
+      if (!ok) break;
+      tmem::fence_after();
+      const int m = b * kBlockRows + r;
+      const bool mine = m < w.rows;
+      uint8_t* slot = partials;
+      const int h = m % G;
+      if (mine) {
+        const DecodeReq& dr = reqs[order[w.it.lo + m / G]];
+        slot += (size_t(dr.first_item) + size_t(w.it.kvh) * dr.items_per_head + w.it.seg) * size_t(G) * (8 + 4 * kHeadDim);
+        reinterpret_cast<float2*>(slot)[h] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
+      }
+      float4* dst = reinterpret_cast<float4*>(slot + G * 8) + h * (kHeadDim / 4);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < kHeadDim; c += 32) {
+        uint32_t o[32];
+        tmem::ld_x32(tl + kColO + c, o);
+        tmem::wait_ld();
+        if (mine)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            dst[(c + j) / 4] = make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
+                                           __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+      }
+      tmem::fence_before();  // O is read before the next item's first MMA writes it
+    }
+  }
+  __syncwarp();
+  tmem::fence_before();
+  __syncthreads();
+  tmem::fence_after();
+  if (warp == 0) tmem::dealloc(tm, 512);
+}
+
+}  // namespace
+
+int encode_page_map(const KernelParams& kp, void* map) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return int(e);
+  if (!fn || found != cudaDriverEntryPointSuccess) return int(cudaErrorNotSupported);
+  // the pool as rows of 128 channels: [layer][page][kv-head][K|V][64 tokens]
+  const cuuint64_t rows = cuuint64_t(kp.n_layers) * kp.max_pages * kp.n_kv_heads * 2 * kPage;
+  const cuuint64_t dims[2] = {kHeadDim, rows}, strides[1] = {kHeadDim * 2};
+  const cuuint32_t box[2] = {64, kPage}, step[2] = {1, 1};
+  const CUresult r = reinterpret_cast<Encode>(fn)(
+      static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kp.base + kp.lay.bf16_pages, dims, strides, box,
+      step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : int(cudaErrorInvalidValue);
+}
+
+int launch_shared(const KernelParams& kp, int layer, const void* map, const void* q, uint8_t* partials, int n_sm,
+                  void* stream, int* launches) {
+  static bool attr = false;
+  if (!attr) {
+    const int e = int(cudaFuncSetAttribute(shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    if (e) return e;
+    attr = true;
+  }
+  const int e = launch_ex(shared_kernel, dim3(n_sm), dim3(kThreads), size_t(kSmemBytes), stream, kp, layer,
+                          *static_cast<const CUtensorMap*>(map), static_cast<const uint16_t*>(q), partials);
+  if (!e) *launches += 1;
+  return e;
+}
+
+}  // namespace oscar

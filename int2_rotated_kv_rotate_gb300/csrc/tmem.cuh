@@ -79,6 +79,25 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
          | (uint32_t(b_mn_major) << 16)         // B major
          | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
+// The same with bf16 A and B.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
+  return idesc_f16(M, N, b_mn_major) | (1u << 7) | (1u << 10);
+}
+// Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, eight of them an atom
+// of 1024 (atoms on 1024-byte boundaries), 16-byte chunk c of row r at chunk c ^ (r & 7).
+// K-major: rows are M or N indices, sbo the distance of eight rows, lbo unused; MN-major: rows
+// are K indices, sbo the distance of eight of them, lbo that of the next 64 M or N indices.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr >> 4) & 0x3fffu) | (uint64_t((lbo >> 4) & 0x3fffu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3fffu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// D (tensor memory) (+)= A x B, both in shared memory; one thread issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(uint32_t(accumulate))
+      : "memory");
+}
 // Shared-memory matrix descriptor, no swizzle: start address, leading (K) and stride (N)
 // byte offsets of the core matrices.
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
