@@ -53,6 +53,7 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kAppendChunk = 16;     // tokens (or ring slots) per append work item
 constexpr int kMaxAppendTokenItems = 65536;
+constexpr int kSharedItemPages = 16;  // an item's fixed time in the shared launch, in pages
 constexpr int kSharedMinPages = 1;    // shorter shared runs stay with their requests' private items
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
@@ -359,29 +360,38 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
       lo = hi;
     }
   }
-  // One wave of items, one a CTA; the row blocks of a run's pages are items of their own.
+  // Pages of an item: the CTAs, one an SM, take the items in turn, so the launch lasts as
+  // long as its rounds of items, each about kSharedItemPages pages' time longer than its
+  // pages (the queries, the pipeline's fill, the partials).  The row blocks of a run's pages
+  // are items of their own.
   const int per_item = kSharedRows / G;  // members of an item at most
-  auto count = [&](int chunk) {
-    long long items = 0;
-    for (const Run& r : runs) items += (long long)Hkv * ceil_div(r.hi - r.lo, per_item) * ceil_div(r.end - r.begin, chunk);
-    return items;
-  };
-  int chunk = 1, longest = 1;
+  long long best = -1;
+  int chunk = 1, longest = 0;
   for (const Run& r : runs) longest = std::max(longest, r.end - r.begin);
-  chunk = int(std::min<long long>(longest, std::max<long long>(2, (count(1) + c->n_sm - 1) / c->n_sm)));
-  while (chunk < longest && count(chunk) > c->n_sm) ++chunk;
+  for (int parts = 1; parts <= std::min(longest, 64); ++parts) {
+    const int ch = ceil_div(longest, parts);
+    long long items = 0;
+    for (const Run& r : runs) items += (long long)Hkv * ceil_div(r.hi - r.lo, per_item) * ceil_div(r.end - r.begin, ch);
+    const long long cost = (items + c->n_sm - 1) / c->n_sm * (ch + kSharedItemPages);
+    if (best < 0 || cost < best) {
+      best = cost;
+      chunk = ch;
+    }
+  }
   std::vector<int> seg_end(runs.size());
   for (size_t k = 0; k < runs.size(); ++k) {  // parents come before their children
     const Run& r = runs[k];
-    const int seg0 = r.parent < 0 ? 0 : seg_end[r.parent], segs = ceil_div(r.end - r.begin, chunk);
-    seg_end[k] = seg0 + segs;
+    const int segs = ceil_div(r.end - r.begin, chunk);
+    const int split = (r.hi - r.lo) * G <= kSharedRows / 2;  // two slots a segment
+    const int seg0 = r.parent < 0 ? 0 : seg_end[r.parent];
+    seg_end[k] = seg0 + segs * (1 + split);
     out.pages += r.end - r.begin;
     for (int m = r.lo; m < r.hi; ++m) out.n_segs[out.order[m]] = seg_end[k];
     for (int s = 0; s < segs; ++s)
       for (int h = 0; h < Hkv; ++h)
         for (int lo = r.lo; lo < r.hi; lo += per_item)
           out.items.push_back({lo, std::min(r.hi, lo + per_item), r.begin + s * chunk,
-                               std::min(r.end, r.begin + (s + 1) * chunk), h, seg0 + s});
+                               std::min(r.end, r.begin + (s + 1) * chunk), h, seg0 + s * (1 + split), split});
   }
   return out;
 }

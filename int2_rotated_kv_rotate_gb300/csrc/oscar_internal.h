@@ -49,13 +49,15 @@ struct DecodeReq {
 
 // One work item of the launch that attends shared runs (BF16 format): pages [begin, end) of
 // kv-head kvh for the requests order[lo .. hi), who map the same pages there; member i's
-// partial slot is its head's first + seg.
+// partial slot is its head's first + seg.  split (at most 128 query rows): the even pages go
+// to that slot, the odd ones to the next.
 constexpr int kSharedRows = 256;  // query rows (members x G) of an item at most
 struct SharedItem {
   int lo, hi;
   int begin, end;
   int kvh;
   int seg;
+  int split;
 };
 
 // One split-K work item: pages [p0, p1) of the INT2 history (kind 0) or BF16 tokens

@@ -12,14 +12,18 @@
 //                  (16 bits, as the private items keep);
 //   O += P V       M = 128, N = 128 channels, K = 64 tokens, hi then lo: P from tensor memory,
 //                  the page's values in shared memory as they are stored (channels contiguous).
-// The reference m of a row moves only when a score exceeds it by more than 8 (base 2), so
-// p <= 2^8 and O is rarely rescaled in tensor memory.
+// The reference m of a row moves only when a score exceeds it by more than 32 (base 2), so O is
+// rarely rescaled in tensor memory; p <= 2^32 loses nothing in bf16 and fp32, whose range is
+// 2^127 (values up to 2^78 and 100000 tokens stay inside).
 //
-// Roles: warp 0 copies pages (TMA, kStages of them in flight), warp 1 issues the MMAs, warps
-// 4-7 and 8-11 are the softmax of row blocks 0 and 1.  S of the next page is computed while
-// the softmax works on this one (two S / P buffers a block, 512 tensor-memory columns in
-// all).  Bound by HBM up to some 256 rows: a page is 32 KB, 1470 cycles of an SM's share of
-// the copy rate, against 900 cycles of tensor core and shared memory for one block.
+// Roles: warp 0 copies pages (TMA, kStages of them, keys and values apart), warp 1 issues the
+// MMAs of S and warp 2 those of O (one warp for both spent 2700 cycles a page on its waits and
+// issues), warps 4-7 and 8-11 are the softmax of two blocks: two row blocks over the same pages,
+// or, for runs of at most 128 rows, the even and the odd pages of one row block, each with a
+// partial slot of its own (one block's chain of S, softmax and O took 2400 cycles a page, more
+// than the 1470 of an SM's share of the copy rate for its 32 KB).  S of a block's next page is
+// computed while its softmax works on this one: two S / P buffers a block, 512 tensor-memory
+// columns in all.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -32,7 +36,7 @@
 namespace oscar {
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kBlockRows = 128;
 constexpr int kPageKv = 2 * kPage * kHeadDim * 2;         // bytes of a page's K and V rows of a head
 constexpr int kQBlock = kBlockRows * kHeadDim * 2;        // bytes of a row block of Q
@@ -41,11 +45,14 @@ constexpr int kBlocks = kSharedRows / kBlockRows;
 static_assert(kBlocks == 2, "warps 4-7 and 8-11");
 
 struct Control {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[kBlocks];
   uint64_t s_full[kBlocks][2], p_full[kBlocks][2];
-  uint64_t o_done[kBlocks];  // one completion a page: O holds the pages so far, P is read
-  uint64_t drain;
+  // O holds the pages up to n and P n is read: barrier n & 1, completion n >> 1.  (A parity tells
+  // a completion from its neighbours only.  The warp that issues S n waits for page n - 2 when
+  // page n - 1 may be done already, but never page n.)
+  uint64_t o_done[kBlocks][2];
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -56,6 +63,9 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 // Tensor-memory columns of block b: two S / P buffers of 64, then O of 128.
 constexpr uint32_t kBlockCols = 256, kColO = 128;
+
+// A row's reference moves when a score exceeds it by this much (base 2).
+constexpr float kRaise = 32.f;
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -72,10 +82,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Everything a role needs of an item.
+// Everything a role needs of an item.  Blocks are row blocks over all pages, or (split) the
+// even and the odd pages of one row block.
 struct Work {
   SharedItem it;
   int rows, blocks, pages;
+  __device__ int pages_of(int b) const { return it.split ? (pages + 1 - b) / 2 : pages; }
+  __device__ int row0(int b) const { return it.split ? 0 : b * kBlockRows; }
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -88,18 +101,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&ctl->full[i]), 1);
-      mbar_init(smem_u32(&ctl->empty[i]), 1);
+      mbar_init(smem_u32(&ctl->k_full[i]), 1);
+      mbar_init(smem_u32(&ctl->k_empty[i]), 1);
+      mbar_init(smem_u32(&ctl->v_full[i]), 1);
+      mbar_init(smem_u32(&ctl->v_empty[i]), 1);
     }
     for (int b = 0; b < kBlocks; ++b) {
       mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
       for (int k = 0; k < 2; ++k) {
         mbar_init(smem_u32(&ctl->s_full[b][k]), 1);
         mbar_init(smem_u32(&ctl->p_full[b][k]), kBlockRows);
+        mbar_init(smem_u32(&ctl->o_done[b][k]), 1);
       }
-      mbar_init(smem_u32(&ctl->o_done[b]), 1);
     }
-    mbar_init(smem_u32(&ctl->drain), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->drain[i]), 1);
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -118,30 +133,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     Work w;
     w.it = items[ix];
     w.rows = (w.it.hi - w.it.lo) * kp.gqa;
-    w.blocks = (w.rows + kBlockRows - 1) / kBlockRows;
+    w.blocks = w.it.split ? 2 : (w.rows + kBlockRows - 1) / kBlockRows;
     w.pages = w.it.end - w.it.begin;
     return w;
   };
-  // Bounded wait of a whole warp for completion `index` of a barrier; once one runs out,
-  // every role leaves its loop.
+  // Bounded wait of a whole warp for completion `index` of a barrier (one lane polls: each
+  // lane's poll costs the barrier's bank a turn); once one runs out, every role leaves its loop.
   auto wait = [&](uint64_t& bar, uint32_t index) -> bool {
     const uint32_t a = smem_u32(&bar);
-    bool done = false;
-    for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
-      done = mbar_try_wait_for(a, index & 1u, 1000000u);
-      if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
-    }
-    if (__all_sync(0xffffffffu, done)) return true;
+    int done = 0;
     if (lane == 0) {
-      *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-      flag(kp, OSCAR_FLAG_TIMEOUT);
+      done = mbar_try_wait(a, index & 1u);
+      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+        done = mbar_try_wait_for(a, index & 1u, 1000000u);
+        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+      }
+      if (!done) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        flag(kp, OSCAR_FLAG_TIMEOUT);
+      }
     }
-    return false;
+    return __shfl_sync(0xffffffffu, done, 0);
   };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- pages
-    uint32_t cnt = 0;
+    uint32_t cnt = 0, nk = 0, nv = 0;  // pages; copies of keys and of values issued
     bool ok = true;
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
@@ -150,90 +167,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
       const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                         size_t(slot_ok ? slot : 0) * kp.max_pages_per_request;
+      int next = w.it.begin < kp.max_pages_per_request ? ptab[w.it.begin] : -1;
       for (int p = 0; p < w.pages; ++p, ++cnt) {
         const uint32_t st = cnt % kStages;
-        if (cnt >= kStages && !wait(ctl->empty[st], cnt / kStages - 1)) {
-          ok = false;
-          break;
-        }
-        int phys = w.it.begin + p < kp.max_pages_per_request ? ptab[w.it.begin + p] : -1;
+        int phys = next;
+        next = p + 1 < w.pages && w.it.begin + p + 1 < kp.max_pages_per_request ? ptab[w.it.begin + p + 1] : -1;
         if (phys < 0 || phys >= kp.max_pages) {  // page 0 instead, and the flag
           if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
           phys = 0;
         }
         const int y = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
+        const uint32_t dst = sst + st * kPageKv;
+        if (cnt >= kStages && !(ok = wait(ctl->k_empty[st], cnt / kStages - 1))) break;
         if (elect_one()) {
-          const uint32_t bar = smem_u32(&ctl->full[st]), dst = sst + st * kPageKv;
-          mbar_expect_tx(bar, kPageKv);
+          const uint32_t bar = smem_u32(&ctl->k_full[st]);
+          mbar_expect_tx(bar, kPageKv / 2);
           tma_load(dst, &map, 0, y, bar);
           tma_load(dst + 8192, &map, 64, y, bar);
+        }
+        __syncwarp();
+        nk = cnt + 1;
+        if (cnt >= kStages && !(ok = wait(ctl->v_empty[st], cnt / kStages - 1))) break;
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&ctl->v_full[st]);
+          mbar_expect_tx(bar, kPageKv / 2);
           tma_load(dst + 16384, &map, 0, y + kPage, bar);
           tma_load(dst + 24576, &map, 64, y + kPage, bar);
         }
         __syncwarp();
+        nv = cnt + 1;
       }
     }
-    if (!ok)  // copies still in flight land before the CTA leaves
-      for (uint32_t k = cnt > kStages ? cnt - kStages : 0; k < cnt; ++k)
-        mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
+    if (!ok) {  // copies still in flight land before the CTA leaves
+      for (uint32_t k = nk > kStages ? nk - kStages : 0; k < nk; ++k)
+        mbar_wait(smem_u32(&ctl->k_full[k % kStages]), (k / kStages) & 1u);
+      for (uint32_t k = nv > kStages ? nv - kStages : 0; k < nv; ++k)
+        mbar_wait(smem_u32(&ctl->v_full[k % kStages]), (k / kStages) & 1u);
+    }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMAs
+    // ---------------------------------------------------------------- S = Q K^T
     constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
-    constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
+    const uint64_t qd = tmem::sdesc_sw128(sq, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
     uint32_t cnt = 0, qn[kBlocks] = {0, 0}, sn[kBlocks] = {0, 0};  // pages; items and pages of each block
     bool ok = true;
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
       for (int b = 0; ok && b < w.blocks; ++b) ok = wait(ctl->q_full[b], qn[b]++);
-      for (int i = 0; ok && i <= w.pages; ++i) {
-        if (i < w.pages) {
-          const uint32_t st = (cnt + i) % kStages;
-          ok = wait(ctl->full[st], (cnt + i) / kStages);
-          for (int b = 0; ok && b < w.blocks; ++b) {
-            const uint32_t n = sn[b] + i;
-            // the buffer's last P (page n - 2) has been read
-            if (n >= 2) ok = wait(ctl->o_done[b], n - 2);
-            if (!ok) break;
-            tmem::fence_after();
-            if (elect_one()) {
-              const uint32_t d = tm + b * kBlockCols + (n & 1) * kPage;
-              const uint32_t qa = sq + b * kQBlock, ka = sst + st * kPageKv;
+      for (int i = 0; ok && i < w.pages; ++i) {
+        const uint32_t st = (cnt + i) % kStages;
+        ok = wait(ctl->k_full[st], (cnt + i) / kStages);
+        const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
+        for (int b = b0; ok && b < b1; ++b) {
+          const int local = w.it.split ? i >> 1 : i;
+          const uint32_t n = sn[b] + local;
+          // the buffer's last P (page n - 2) has been read; that of an earlier item was before
+          // the softmax handed over this item's queries
+          if (local >= 2) ok = wait(ctl->o_done[b][n & 1], (n >> 1) - 1);
+          if (!ok) break;
+          tmem::fence_after();
+          if (elect_one()) {
+            const uint32_t d = tm + b * kBlockCols + (n & 1) * kPage;
+            const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kPageKv >> 4);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tmem::mma_ss(d, tmem::sdesc_sw128(qa + (k >> 2) * (kQBlock / 2) + (k & 3) * 32, 16, 1024),
-                             tmem::sdesc_sw128(ka + (k >> 2) * 8192 + (k & 3) * 32, 16, 1024), kIdS, k > 0);
-              tmem::commit(smem_u32(&ctl->s_full[b][n & 1]));
-            }
-            __syncwarp();
+            for (int k = 0; k < 8; ++k)
+              tmem::mma_ss(d, qb + ((k >> 2) * (kQBlock / 2) + (k & 3) * 32) / 16, kb + ((k >> 2) * 8192 + (k & 3) * 32) / 16,
+                           kIdS, k > 0);
+            tmem::commit(smem_u32(&ctl->s_full[b][n & 1]));
+            if (b == b1 - 1) tmem::commit(smem_u32(&ctl->k_empty[st]));
           }
-        }
-        if (ok && i > 0) {
-          const uint32_t st = (cnt + i - 1) % kStages;
-          for (int b = 0; ok && b < w.blocks; ++b) {
-            const uint32_t n = sn[b] + i - 1;
-            ok = wait(ctl->p_full[b][n & 1], n >> 1);
-            if (!ok) break;
-            tmem::fence_after();
-            if (elect_one()) {
-              const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + (n & 1) * kPage;
-              const uint32_t va = sst + st * kPageKv + 16384;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)  // hi then lo
-                tmem::mma_ts(d, a + 8 * k, tmem::sdesc_sw128(va + (k & 3) * 2048, 8192, 1024), kIdO, i > 1 || k > 0);
-              tmem::commit(smem_u32(&ctl->o_done[b]));
-              if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
-            }
-            __syncwarp();
-          }
+          __syncwarp();
         }
       }
       cnt += w.pages;
-      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages;
+      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages_of(b);
     }
     if (!ok) {  // MMAs in flight end before the tensor memory is freed
-      if (elect_one()) tmem::commit(smem_u32(&ctl->drain));
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[0]));
       __syncwarp();
-      mbar_wait(smem_u32(&ctl->drain), 0);
+      mbar_wait(smem_u32(&ctl->drain[0]), 0);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- O += P V
+    constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
+    const uint64_t vd = tmem::sdesc_sw128(sst + 16384, 8192, 1024);
+    uint32_t cnt = 0, sn[kBlocks] = {0, 0};
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      for (int i = 0; ok && i < w.pages; ++i) {
+        const uint32_t st = (cnt + i) % kStages;
+        ok = wait(ctl->v_full[st], (cnt + i) / kStages);
+        const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
+        for (int b = b0; ok && b < b1; ++b) {
+          const int local = w.it.split ? i >> 1 : i;
+          const uint32_t n = sn[b] + local;
+          ok = wait(ctl->p_full[b][n & 1], n >> 1);
+          if (!ok) break;
+          tmem::fence_after();
+          if (elect_one()) {
+            const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + (n & 1) * kPage;
+            const uint64_t vb = vd + st * (kPageKv >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // hi then lo
+              tmem::mma_ts(d, a + 8 * k, vb + (k & 3) * (2048 / 16), kIdO, local > 0 || k > 0);
+            tmem::commit(smem_u32(&ctl->o_done[b][n & 1]));
+            if (b == b1 - 1) tmem::commit(smem_u32(&ctl->v_empty[st]));
+          }
+          __syncwarp();
+        }
+      }
+      cnt += w.pages;
+      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages_of(b);
+    }
+    if (!ok) {
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[1]));
+      __syncwarp();
+      mbar_wait(smem_u32(&ctl->drain[1]), 0);
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax of block b
@@ -248,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (b >= w.blocks) continue;
       // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
       for (int k = 0; k < 16; ++k) {
-        const int row = 32 * wq + 2 * k + (lane >> 4), c = lane & 15, m = b * kBlockRows + row;
+        const int row = 32 * wq + 2 * k + (lane >> 4), c = lane & 15, m = w.row0(b) + row;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (m < w.rows) {
           const int req = order[w.it.lo + m / G];
@@ -259,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async();
       mbar_arrive(smem_u32(&ctl->q_full[b]));
       float m_ref = -INFINITY, l = 0.f;
-      for (int i = 0; i < w.pages; ++i, ++n) {
+      const int pages = w.pages_of(b);
+      for (int i = 0; i < pages; ++i, ++n) {
         const uint32_t buf = tl + (n & 1) * kPage;
         ok = wait(ctl->s_full[b][n & 1], n >> 1);
         if (!ok) break;
@@ -272,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
         mx *= scale;
-        const bool raise = mx > m_ref + 8.f;  // also from -inf
+        const bool raise = mx > m_ref + kRaise;  // also from -inf
         if (i == 0) {
           m_ref = mx;
         } else if (__any_sync(0xffffffffu, raise)) {
-          ok = wait(ctl->o_done[b], n - 1);  // (S of page n was issued after completion n - 2)
+          ok = wait(ctl->o_done[b][(n - 1) & 1], (n - 1) >> 1);
           if (!ok) break;
           tmem::fence_after();
           const float f = raise ? ex2(m_ref - mx) : 1.f;
@@ -310,19 +360,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the rows' partials
-      // (a parity tells a completion from its neighbours only: the last but one first, which
-      // no page of this item may have waited for)
-      ok = n < 2 || wait(ctl->o_done[b], n - 2);
-      if (ok) ok = wait(ctl->o_done[b], n - 1);
+      if (pages > 0) ok = wait(ctl->o_done[b][(n - 1) & 1], (n - 1) >> 1);
       if (!ok) break;
       tmem::fence_after();
-      const int m = b * kBlockRows + r;
+      const int m = w.row0(b) + r;
       const bool mine = m < w.rows;
       uint8_t* slot = partials;
       const int h = m % G;
       if (mine) {
         const DecodeReq& dr = reqs[order[w.it.lo + m / G]];
-        slot += (size_t(dr.first_item) + size_t(w.it.kvh) * dr.items_per_head + w.it.seg) * size_t(G) * (8 + 4 * kHeadDim);
+        slot += (size_t(dr.first_item) + size_t(w.it.kvh) * dr.items_per_head + w.it.seg + (w.it.split ? b : 0)) * size_t(G) * (8 + 4 * kHeadDim);
         reinterpret_cast<float2*>(slot)[h] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
       }
       float4* dst = reinterpret_cast<float4*>(slot + G * 8) + h * (kHeadDim / 4);

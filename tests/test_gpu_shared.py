@@ -140,6 +140,21 @@ def test_long_prefix_and_many_heads():
     assert pages == 300 and items <= 152
 
 
+@pytest.mark.parametrize("gqa,members,pages", [(4, 2, 9), (8, 17, 4)])
+def test_more_items_than_multiprocessors(gqa, members, pages):
+    """Every CTA of the shared launch takes several items, of one row block and of two, with even
+    and odd numbers of pages."""
+    groups, hkv = 41, 8
+    b = Batch(hkv, gqa, groups * members, groups * (pages + 2) + groups * members, pages + 4)
+    slots = []
+    for g in range(groups):
+        first = b.new(64 * (pages - g % 3))
+        slots += [first] + [b.new(1 + (7 * i) % 50 if i % 2 else 0, first, pages - g % 3) for i in range(members - 1)]
+    b.check(slots, label="many")
+    items, shared = b.cache.shared_info()
+    assert items > 2 * 152 and shared == sum(pages - g % 3 for g in range(groups))
+
+
 def test_peaked_scores_move_the_reference():
     """Scores that grow along the prefix by far more than the lazy reference allows, and fall."""
     b = Batch(1, 4, 3, 60, 20)
