@@ -26,11 +26,15 @@ constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::k
 
 // WEIGHTS: the scores (log2 units) go to scores, fp32 [plan request][kv-head][stride][G], and
 // each head's (maximum, 1 / denominator) to ml, for bf16_weights_kernel.
+// after_shared: the preceding launch attends the plan's shared runs.  It waited for its own
+// predecessors before it let this one start, so q and the pages are final here, and only a
+// merge, which reads the shared runs' partials, waits for its end: the private items of the
+// SMs that it leaves free run beside it.
 template <int G, int NBUF, bool WEIGHTS>
 __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q,
                                                          uint8_t* __restrict__ partials, uint16_t* __restrict__ out,
                                                          float* __restrict__ out_f32, float* __restrict__ scores,
-                                                         float2* __restrict__ ml) {
+                                                         float2* __restrict__ ml, bool after_shared) {
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + Bf16Rows<4, NBUF>::kSmemBytes);
   int* s_last_p = reinterpret_cast<int*>(smem + Bf16Rows<4, NBUF>::kSmemBytes + G * kQRow * 4);
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
         bf16_prestage<4, NBUF>(rowK, rowV, t0, upto, smem);
         staged = upto - t0;
       }
-      pdl_wait();
+      if (!after_shared) pdl_wait();
       pdl_trigger();
       waited = true;
     }
@@ -100,7 +104,9 @@ __global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int la
 
     MergeAcc<G, 128> acc;
     if (merge_partial<G, 128>(kp, it, it.head_count - dr.n_shared, partials, acc, s_last_p, smem, kBf16SlabSlots<G, NBUF>, smem_u32(slab_bar), slab_phase,
-                              [] {})) {
+                              [&] {
+                                if (after_shared) pdl_wait();
+                              })) {
       const int c = threadIdx.x;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -198,14 +204,14 @@ int resident_ctas(int n_sm) {
 
 template <int G, int NBUF>
 int launch_t(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
-             const DecodeWorkspace& wl, int n_sm, void* stream, int* launches) {
+             const DecodeWorkspace& wl, bool after_shared, int n_sm, void* stream, int* launches) {
   uint8_t* partials = ws + wl.partials;
   const int resident = resident_ctas<G, NBUF>(n_sm);
   if (resident < 0) return -resident;
   const int grid = resident;  // persistent-style: CTAs loop over the plan's items
   int e = launch_ex(bf16_split_kernel<G, NBUF, false>, dim3(grid), dim3(128), size_t(kBf16KernelSmem(G, NBUF)), stream,
                     kp, layer, static_cast<const uint16_t*>(q), partials, static_cast<uint16_t*>(out), out_f32,
-                    static_cast<float*>(nullptr), static_cast<float2*>(nullptr));
+                    static_cast<float*>(nullptr), static_cast<float2*>(nullptr), after_shared);
   if (!e) *launches += 1;
   return e;
 }
@@ -219,7 +225,7 @@ int launch_weights_t(const KernelParams& kp, int layer, const void* q, void* out
   float2* ml = reinterpret_cast<float2*>(ws + wl.ml);
   int e = launch_ex(bf16_split_kernel<G, NBUF, true>, dim3(resident), dim3(128), size_t(kBf16KernelSmem(G, NBUF)), stream,
                     kp, layer, static_cast<const uint16_t*>(q), ws + wl.partials, static_cast<uint16_t*>(out), out_f32,
-                    scores, ml);
+                    scores, ml, false);
   if (e) return e;
   *launches += 1;
   e = launch_ex(bf16_weights_kernel<G>, dim3(4 * n_sm, 4), dim3(kWeightsThreads), 0, stream, kp,
@@ -249,13 +255,14 @@ int launch_bf16_decode_weights(const KernelParams& kp, int layer, const void* q,
 }
 
 int launch_bf16_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
-                       const DecodeWorkspace& wl, bool deep, int n_sm, void* stream, int* launches) {
+                       const DecodeWorkspace& wl, bool deep, bool after_shared, int n_sm, void* stream,
+                       int* launches) {
   if (kp.gqa == 4)
-    return deep ? launch_t<4, 3>(kp, layer, q, out, out_f32, ws, wl, n_sm, stream, launches)
-                : launch_t<4, 2>(kp, layer, q, out, out_f32, ws, wl, n_sm, stream, launches);
+    return deep ? launch_t<4, 3>(kp, layer, q, out, out_f32, ws, wl, after_shared, n_sm, stream, launches)
+                : launch_t<4, 2>(kp, layer, q, out, out_f32, ws, wl, after_shared, n_sm, stream, launches);
   if (kp.gqa == 8)
-    return deep ? launch_t<8, 3>(kp, layer, q, out, out_f32, ws, wl, n_sm, stream, launches)
-                : launch_t<8, 2>(kp, layer, q, out, out_f32, ws, wl, n_sm, stream, launches);
+    return deep ? launch_t<8, 3>(kp, layer, q, out, out_f32, ws, wl, after_shared, n_sm, stream, launches)
+                : launch_t<8, 2>(kp, layer, q, out, out_f32, ws, wl, after_shared, n_sm, stream, launches);
   return int(cudaErrorInvalidValue);
 }
 

@@ -1143,7 +1143,7 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   }
   if (!e)
     e = launch_bf16_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws, c->dec_wide,
-                           c->n_sm, stream, &g_launches);
+                           c->dec_shared, c->n_sm, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "bf16 decode launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }

@@ -172,9 +172,9 @@ int launch_decode(const KernelParams& kp, int layer, const void* q, void* out, f
                   const DecodeWorkspace& wl, bool wide, int n_sm, void* stream, int* launches,
                   const void* k_new = nullptr, const void* v_new = nullptr, bool fused = false);
 // `deep`: the BF16 kernel with the deeper row pipeline (one-wave plans; the plan was made
-// for it).
+// for it).  `after_shared`: launch_shared went just before.
 int launch_bf16_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
-                       const DecodeWorkspace& wl, bool deep, int n_sm, void* stream, int* launches);
+                       const DecodeWorkspace& wl, bool deep, bool after_shared, int n_sm, void* stream, int* launches);
 
 // BF16 decode that also adds each token's attention weight (summed over the query heads of
 // its kv-head) to weights_in (nullable: zero) into weights_out, fp32 [slot][kv-head]

@@ -137,12 +137,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.pages = w.it.end - w.it.begin;
     return w;
   };
-  // Bounded wait of a whole warp for completion `index` of a barrier (one lane polls: each
-  // lane's poll costs the barrier's bank a turn); once one runs out, every role leaves its loop.
+  // Bounded wait of a whole warp for completions of one or two barriers (index: parity of the
+  // completion).  Lane 0 polls the first, lane 1 the second: each polling lane costs the
+  // barrier's bank a turn, and two waits one after the other twice a wait's 200 cycles.  Once
+  // one runs out, every role leaves its loop.
+  auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> bool {
+    int done = 1;
+    if (lane < 2) {
+      const uint32_t a = lane ? smem_u32(&bar1) : smem_u32(&bar0), par = (lane ? index1 : index0) & 1u;
+      done = mbar_try_wait(a, par);
+      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+        done = mbar_try_wait_for(a, par, 1000000u);
+        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+      }
+      if (!done) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        flag(kp, OSCAR_FLAG_TIMEOUT);
+      }
+    }
+    return __all_sync(0xffffffffu, done);
+  };
   auto wait = [&](uint64_t& bar, uint32_t index) -> bool {
-    const uint32_t a = smem_u32(&bar);
-    int done = 0;
+    int done = 1;
     if (lane == 0) {
+      const uint32_t a = smem_u32(&bar);
       done = mbar_try_wait(a, index & 1u);
       for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
         done = mbar_try_wait_for(a, index & 1u, 1000000u);
@@ -153,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         flag(kp, OSCAR_FLAG_TIMEOUT);
       }
     }
-    return __shfl_sync(0xffffffffu, done, 0);
+    return __all_sync(0xffffffffu, done);
   };
 
   if (warp == 0) {
@@ -208,21 +226,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- S = Q K^T
     constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
     const uint64_t qd = tmem::sdesc_sw128(sq, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
-    uint32_t cnt = 0, qn[kBlocks] = {0, 0}, sn[kBlocks] = {0, 0};  // pages; items and pages of each block
+    uint32_t st = 0, lap = 0;                      // stage, and laps of the stages
+    uint32_t q0 = 0, q1 = 0, n0 = 0, n1 = 0;       // items and pages of each block
     bool ok = true;
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
-      for (int b = 0; ok && b < w.blocks; ++b) ok = wait(ctl->q_full[b], qn[b]++);
+      ok = wait(ctl->q_full[0], q0++);
+      if (ok && w.blocks > 1) ok = wait(ctl->q_full[1], q1++);
+      int l0 = 0, l1 = 0;  // this item's pages of each block so far
       for (int i = 0; ok && i < w.pages; ++i) {
-        const uint32_t st = (cnt + i) % kStages;
-        ok = wait(ctl->k_full[st], (cnt + i) / kStages);
         const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
         for (int b = b0; ok && b < b1; ++b) {
-          const int local = w.it.split ? i >> 1 : i;
-          const uint32_t n = sn[b] + local;
+          const uint32_t n = b ? n1++ : n0++;
           // the buffer's last P (page n - 2) has been read; that of an earlier item was before
           // the softmax handed over this item's queries
-          if (local >= 2) ok = wait(ctl->o_done[b][n & 1], (n >> 1) - 1);
+          const bool reused = (b ? l1++ : l0++) >= 2;
+          uint64_t& last = ctl->o_done[b][n & 1];
+          if (b == b0) ok = reused ? wait2(ctl->k_full[st], lap, last, (n >> 1) - 1) : wait(ctl->k_full[st], lap);
+          else if (reused) ok = wait(last, (n >> 1) - 1);
           if (!ok) break;
           tmem::fence_after();
           if (elect_one()) {
@@ -237,9 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
+        if (++st == kStages) {
+          st = 0;
+          ++lap;
+        }
       }
-      cnt += w.pages;
-      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages_of(b);
     }
     if (!ok) {  // MMAs in flight end before the tensor memory is freed
       if (elect_one()) tmem::commit(smem_u32(&ctl->drain[0]));
@@ -250,18 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
     const uint64_t vd = tmem::sdesc_sw128(sst + 16384, 8192, 1024);
-    uint32_t cnt = 0, sn[kBlocks] = {0, 0};
+    uint32_t st = 0, lap = 0, n0 = 0, n1 = 0;
     bool ok = true;
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
+      int l0 = 0, l1 = 0;
       for (int i = 0; ok && i < w.pages; ++i) {
-        const uint32_t st = (cnt + i) % kStages;
-        ok = wait(ctl->v_full[st], (cnt + i) / kStages);
         const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
         for (int b = b0; ok && b < b1; ++b) {
-          const int local = w.it.split ? i >> 1 : i;
-          const uint32_t n = sn[b] + local;
-          ok = wait(ctl->p_full[b][n & 1], n >> 1);
+          const uint32_t n = b ? n1++ : n0++;
+          const bool first = (b ? l1++ : l0++) == 0;
+          uint64_t& p = ctl->p_full[b][n & 1];
+          ok = b == b0 ? wait2(ctl->v_full[st], lap, p, n >> 1) : wait(p, n >> 1);
           if (!ok) break;
           tmem::fence_after();
           if (elect_one()) {
@@ -269,15 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vb = vd + st * (kPageKv >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)  // hi then lo
-              tmem::mma_ts(d, a + 8 * k, vb + (k & 3) * (2048 / 16), kIdO, local > 0 || k > 0);
+              tmem::mma_ts(d, a + 8 * k, vb + (k & 3) * (2048 / 16), kIdO, !first || k > 0);
             tmem::commit(smem_u32(&ctl->o_done[b][n & 1]));
             if (b == b1 - 1) tmem::commit(smem_u32(&ctl->v_empty[st]));
           }
           __syncwarp();
         }
+        if (++st == kStages) {
+          st = 0;
+          ++lap;
+        }
       }
-      cnt += w.pages;
-      for (int b = 0; b < w.blocks; ++b) sn[b] += w.pages_of(b);
     }
     if (!ok) {
       if (elect_one()) tmem::commit(smem_u32(&ctl->drain[1]));
@@ -296,14 +321,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work w = load_work(ix);
       if (b >= w.blocks) continue;
       // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
-      for (int k = 0; k < 16; ++k) {
-        const int row = 32 * wq + 2 * k + (lane >> 4), c = lane & 15, m = w.row0(b) + row;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (m < w.rows) {
-          const int req = order[w.it.lo + m / G];
-          v = reinterpret_cast<const uint4*>(q + (size_t(req) * kp.n_q_heads + size_t(w.it.kvh) * G + m % G) * kHeadDim)[c];
+      {
+        // lane: the member of its row; then all loads before the first store
+        const int m = w.row0(b) + r;
+        const int req = m < w.rows ? order[w.it.lo + m / G] : -1;
+        const int head = w.it.kvh * G + m % G;
+        const int row_of_q = req >= 0 ? req * kp.n_q_heads + head : -1;
+        uint4 v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int src = __shfl_sync(0xffffffffu, row_of_q, 2 * k + (lane >> 4));
+          v[k] = src >= 0 ? reinterpret_cast<const uint4*>(q + size_t(src) * kHeadDim)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
         }
-        *reinterpret_cast<uint4*>(smem + b * kQBlock + (c >> 3) * (kQBlock / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int row = 32 * wq + 2 * k + (lane >> 4), c = lane & 15;
+          *reinterpret_cast<uint4*>(smem + b * kQBlock + (c >> 3) * (kQBlock / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[k];
+        }
       }
       fence_proxy_async();
       mbar_arrive(smem_u32(&ctl->q_full[b]));
