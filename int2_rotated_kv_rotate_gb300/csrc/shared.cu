@@ -78,6 +78,30 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Two floats in one register pair, and sums and products of both at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -342,11 +366,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async();
       mbar_arrive(smem_u32(&ctl->q_full[b]));
       float m_ref = -INFINITY, l = 0.f;
+      const bool idle = w.row0(b) + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
       const int pages = w.pages_of(b);
       for (int i = 0; i < pages; ++i, ++n) {
         const uint32_t buf = tl + (n & 1) * kPage;
         ok = wait(ctl->s_full[b][n & 1], n >> 1);
         if (!ok) break;
+        if (idle) {
+          mbar_arrive(smem_u32(&ctl->p_full[b][n & 1]));
+          continue;
+        }
         tmem::fence_after();
         uint32_t s0[32], s1[32];
         tmem::ld_x32(buf, s0);
@@ -354,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem::wait_ld();
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        for (int j = 0; j < 32; ++j) mx = max3(mx, __uint_as_float(s0[j]), __uint_as_float(s1[j]));
         mx *= scale;
         const bool raise = mx > m_ref + kRaise;  // also from -inf
         if (i == 0) {
@@ -377,15 +406,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t scale2 = pack2(scale, scale), minus_ref = pack2(-ref, -ref), minus_one = pack2(-1.f, -1.f);
+        uint64_t l2 = pack2(0.f, 0.f);
         uint32_t hi[32], lo[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
-          const float pa = ex2(fmaf(__uint_as_float(s[0]), scale, -ref)), pb = ex2(fmaf(__uint_as_float(s[1]), scale, -ref));
-          l += pa + pb;
+          float pa, pb;
+          unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), scale2, minus_ref), pa, pb);
+          pa = ex2(pa);
+          pb = ex2(pb);
+          const uint64_t p = pack2(pa, pb);
+          l2 = add2(l2, p);
           hi[j] = pack_bf16(pa, pb);
-          lo[j] = pack_bf16(pa - bf16_lo(hi[j]), pb - bf16_hi(hi[j]));
+          unpack2(fma2(pack2(bf16_lo(hi[j]), bf16_hi(hi[j])), minus_one, p), pa, pb);
+          lo[j] = pack_bf16(pa, pb);
         }
+        float la, lb;
+        unpack2(l2, la, lb);
+        l += la + lb;
         tmem::st_x32(buf, hi);
         tmem::st_x32(buf + 32, lo);
         tmem::wait_st();
