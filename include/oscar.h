@@ -189,10 +189,12 @@ oscar_status oscar_plan_decode(oscar_cache* cache, const int* slots, int n_req, 
  * several longer ones) have those pages attended once for all of them, as one more launch
  * of oscar_bf16_decode_attention before the decode's own; each request's further pages and
  * the merge are as without the flag.  Results are those of the plan without it, up to the
- * rounding of the sums.  A captured decode may be replayed under later plans that have the
- * flag (or, without shared pages, do not); one captured without it may not be replayed
- * under a plan with shared runs. */
+ * rounding of the sums.  Where sharing would save too few reads to pay for the launch, the
+ * plan goes without it; with OSCAR_PLAN_SHARED_ALWAYS (only together with it) it never does.
+ * A decode captured under a plan with the flag may be replayed under any later plan; one
+ * captured without it may not be replayed under a plan with shared runs. */
 #define OSCAR_PLAN_SHARED_PREFIX 0x4u
+#define OSCAR_PLAN_SHARED_ALWAYS 0x8u
 oscar_status oscar_plan_decode_ex(oscar_cache* cache, const int* slots, int n_req, int max_split_pages, uint32_t flags,
                                   void* stream);
 
@@ -209,7 +211,7 @@ size_t oscar_decode_workspace_max_bytes(const oscar_cache* cache);
 oscar_status oscar_plan_info(const oscar_cache* cache, int* n_items, int* n_bf16_items, int* max_item_pages);
 
 /* Of a plan with OSCAR_PLAN_SHARED_PREFIX: the shared launch's work items, and the pages of
- * a kv-head that it attends once for several requests (0 and 0 without sharing). */
+ * a kv-head that it attends once for several requests (0 and 0 where it goes without). */
 oscar_status oscar_plan_shared_info(const oscar_cache* cache, int* n_items, int* n_pages);
 
 /* Decode, step 2 (device, per layer): fused decode attention over the mixed-precision

@@ -257,6 +257,7 @@ def oscar_plan_decode(handle: int, slots, max_split_pages: int = 0, stream=None)
 OSCAR_PLAN_NARROW = 0x1
 OSCAR_PLAN_FOLDED_ROTATIONS = 0x2  # q arrives rotated (R_K folded into W_q), the output stays rotated
 OSCAR_PLAN_SHARED_PREFIX = 0x4  # BF16 format: pages that requests share are attended once for all of them
+OSCAR_PLAN_SHARED_ALWAYS = 0x8  # ... also where too few are shared for it to pay
 
 
 def oscar_plan_decode_ex(handle: int, slots, max_split_pages: int = 0, flags: int = 0, stream=None) -> None:

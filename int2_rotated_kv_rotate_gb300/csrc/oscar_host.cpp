@@ -54,7 +54,13 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 constexpr int kAppendChunk = 16;     // tokens (or ring slots) per append work item
 constexpr int kMaxAppendTokenItems = 65536;
 constexpr int kSharedItemPages = 16;  // an item's fixed time in the shared launch, in pages
-constexpr int kSharedMinPages = 1;    // shorter shared runs stay with their requests' private items
+// A plan uses the shared launch where sharing saves that many bytes of reads: below, the
+// launch and the longer merges cost more than the reads, which L2 largely serves.  Measured
+// with / without it, 32 query heads on 8 kv-heads: 8 requests on 8 pages (15 MB saved) 11.8 /
+// 11.5 us, 4 on 32 (25 MB) 13.1 / 13.4, 2 on 128 (34 MB) 19.8 / 17.7, 4 on 64 (50 MB) 14.9 /
+// 18.6, 32 on 8 (65 MB) 21.5 / 20.6, 8 on 64 (117 MB) 20.6 / 29.2, 32 on 128 (1 GB) 29.5 / 134.
+constexpr long long kSharedPaysBytes = 32LL << 20;
+constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages stays with its requests' private items
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
 bool config_ok(const oscar_config* c, std::string* why) {
@@ -313,7 +319,7 @@ struct SharedRuns {
   int pages = 0;                   // pages attended once for several requests
 };
 
-SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::vector<int>& Ls) {
+SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::vector<int>& Ls, bool always) {
   SharedRuns out;
   const int n = int(Ls.size()), Hkv = c->cfg.n_kv_heads, G = c->cfg.n_q_heads / Hkv;
   out.order.resize(n);
@@ -345,7 +351,7 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
       if (!same) break;
     }
     if (end > g.begin) {
-      if (end - g.begin < kSharedMinPages) continue;
+      if (!always && (end - g.begin) * (long long)(g.hi - g.lo - 1) < kSharedMinSaved) continue;
       runs.push_back({g.lo, g.hi, g.begin, end, g.parent});
       parent = int(runs.size()) - 1;
       for (int k = g.lo; k < g.hi; ++k) out.first_private[out.order[k]] = end;
@@ -360,10 +366,17 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
       lo = hi;
     }
   }
+  long long saved = 0;  // pages
+  for (const Run& r : runs) saved += (long long)(r.end - r.begin) * (r.hi - r.lo - 1);
+  if (!always && saved * Hkv * (2LL * kPage * kHeadDim * 2) < kSharedPaysBytes) {
+    out.first_private.assign(n, 0);
+    return out;
+  }
   // Pages of an item: the CTAs, one an SM, take the items in turn, so the launch lasts as
   // long as its rounds of items, each about kSharedItemPages pages' time longer than its
-  // pages (the queries, the pipeline's fill, the partials).  The row blocks of a run's pages
-  // are items of their own.
+  // pages (the queries, the pipeline's fill, the partials); and every partial slot of a head
+  // is merged, an eighth of a page's time each.  The row blocks of a run's pages are items of
+  // their own.
   const int per_item = kSharedRows / G;  // members of an item at most
   long long best = -1;
   int chunk = 1, longest = 0;
@@ -372,7 +385,7 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
     const int ch = ceil_div(longest, parts);
     long long items = 0;
     for (const Run& r : runs) items += (long long)Hkv * ceil_div(r.hi - r.lo, per_item) * ceil_div(r.end - r.begin, ch);
-    const long long cost = (items + c->n_sm - 1) / c->n_sm * (ch + kSharedItemPages);
+    const long long cost = 8 * ((items + c->n_sm - 1) / c->n_sm) * (ch + kSharedItemPages) + 2 * parts;
     if (best < 0 || cost < best) {
       best = cost;
       chunk = ch;
@@ -795,11 +808,14 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
                                   void* stream) {
   if (!c || !slots || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad plan arguments");
-  if (flags & ~(OSCAR_PLAN_NARROW | OSCAR_PLAN_FOLDED_ROTATIONS | OSCAR_PLAN_SHARED_PREFIX))
+  if (flags & ~(OSCAR_PLAN_NARROW | OSCAR_PLAN_FOLDED_ROTATIONS | OSCAR_PLAN_SHARED_PREFIX |
+                OSCAR_PLAN_SHARED_ALWAYS))
     return fail(OSCAR_ERR_INVALID_ARG, "unknown plan flags %#x", flags);
   if ((flags & OSCAR_PLAN_FOLDED_ROTATIONS) && !is_int2(c))
     return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_FOLDED_ROTATIONS applies to the INT2 formats");
   const bool shared = (flags & OSCAR_PLAN_SHARED_PREFIX) != 0;
+  if ((flags & OSCAR_PLAN_SHARED_ALWAYS) && !shared)
+    return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_SHARED_ALWAYS goes with OSCAR_PLAN_SHARED_PREFIX");
   if (shared && is_int2(c))
     return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_SHARED_PREFIX applies to the BF16 format");
   if (max_split_pages < 0) return fail(OSCAR_ERR_INVALID_ARG, "max_split_pages < 0");
@@ -842,7 +858,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       if (e) return fail(OSCAR_ERR_CUDA, "tensor map of the page pool: %s", cudaGetErrorString(cudaError_t(e)));
       c->map_ready = true;
     }
-    runs = find_shared_runs(c, slots, Ls);
+    runs = find_shared_runs(c, slots, Ls, (flags & OSCAR_PLAN_SHARED_ALWAYS) != 0);
     if (runs.items.size() > c->lay.max_shared_items)
       return fail(OSCAR_ERR_INVALID_ARG, "plan of %zu shared items exceeds %zu", runs.items.size(), c->lay.max_shared_items);
   } else {
@@ -1135,7 +1151,14 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   if (st) return st;
   if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_attention needs the BF16 format");
   int e = 0;
-  if (c->dec_shared) {
+  // A captured decode is replayed under later plans, which may share.
+  bool with_shared = c->dec_shared && c->dec_shared_items > 0;
+  if (c->dec_shared && !with_shared) {
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    CUDA_TRY(cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capturing));
+    with_shared = capturing != cudaStreamCaptureStatusNone;
+  }
+  if (with_shared) {
     st = check_device(c);
     if (st) return st;
     e = launch_shared(kernel_params(c), layer, c->page_map, q, static_cast<uint8_t*>(workspace) + c->ws.partials, c->n_sm,
@@ -1143,7 +1166,7 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   }
   if (!e)
     e = launch_bf16_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws, c->dec_wide,
-                           c->dec_shared, c->n_sm, stream, &g_launches);
+                           with_shared, c->n_sm, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "bf16 decode launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from int2_rotated_kv_rotate_gb300 import KVCache, OSCAR_PLAN_SHARED_PREFIX as SHARED, workloads as wl
+from int2_rotated_kv_rotate_gb300 import KVCache, OSCAR_PLAN_SHARED_PREFIX, workloads as wl
 from int2_rotated_kv_rotate_gb300 import _native as N
 
 from helpers import compare_decode
@@ -17,6 +17,7 @@ from helpers import compare_decode
 pytestmark = pytest.mark.gpu
 
 SEED = 515
+SHARED = OSCAR_PLAN_SHARED_PREFIX | N.OSCAR_PLAN_SHARED_ALWAYS  # the small cases here would go without
 
 
 def tokens(hkv, stream, n):
@@ -143,7 +144,7 @@ def test_long_prefix_and_many_heads():
 @pytest.mark.parametrize("gqa,members,pages", [(4, 2, 9), (8, 17, 4)])
 def test_more_items_than_multiprocessors(gqa, members, pages):
     """Every CTA of the shared launch takes several items, of one row block and of two, with even
-    and odd numbers of pages."""
+    and odd numbers of pages (its warps pass barriers of one item to the next)."""
     groups, hkv = 41, 8
     b = Batch(hkv, gqa, groups * members, groups * (pages + 2) + groups * members, pages + 4)
     slots = []
@@ -153,6 +154,37 @@ def test_more_items_than_multiprocessors(gqa, members, pages):
     b.check(slots, label="many")
     items, shared = b.cache.shared_info()
     assert items > 2 * 152 and shared == sum(pages - g % 3 for g in range(groups))
+
+
+def test_sharing_only_where_it_pays():
+    """A short prefix goes without the shared launch unless told otherwise, a long one has it; a
+    decode captured under the first is right under the second."""
+    b = Batch(8, 4, 16, 300, 80)
+    short = b.new(64 * 4)
+    few = [short, b.new(9, short, 4)]
+    q = torch.randn(16, b.hq, 128, device="cuda").bfloat16()
+    _, launches = b.check(few, flags=OSCAR_PLAN_SHARED_PREFIX, label="short")
+    assert launches == 1 and b.cache.shared_info() == (0, 0)
+    _, launches = b.check(few, label="short, always")
+    assert launches == 2 and b.cache.shared_info()[1] == 4
+    first = b.new(64 * 64)
+    many = [first] + [b.new(5 * i, first, 64) for i in range(1, 12)]
+    _, launches = b.check(many, flags=OSCAR_PLAN_SHARED_PREFIX, label="long")
+    assert launches == 2 and b.cache.shared_info()[1] == 64
+    b.cache.plan(few, flags=OSCAR_PLAN_SHARED_PREFIX)
+    out, out32 = torch.empty_like(q), torch.empty(q.shape, device="cuda")
+    call = lambda: N.oscar_bf16_decode_attention(b.cache.handle, 0, q, out, b.cache.workspace, out32)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    b.cache.plan(many, flags=OSCAR_PLAN_SHARED_PREFIX)
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, s in enumerate(many):
+        want, tol = b.reference(s, q[i])
+        assert ((out32[i].cpu().double() - want).abs() <= tol).all(), f"request {i}"
 
 
 def test_peaked_scores_move_the_reference():
@@ -276,9 +308,10 @@ def test_refusals():
     b = Batch(1, 4, 2, 20, 8)
     first = b.new(64 * 4)
     slots = [first, b.new(5, first, 4)]
-    with pytest.raises(N.OscarError) as e:
-        b.cache.plan(slots, flags=0x8)
-    assert e.value.status == 1
+    for flags in (0x10, N.OSCAR_PLAN_SHARED_ALWAYS):
+        with pytest.raises(N.OscarError) as e:
+            b.cache.plan(slots, flags=flags)
+        assert e.value.status == 1
     with pytest.raises(N.OscarError) as e:
         b.cache.plan([slots[0], slots[0]], flags=SHARED)
     assert e.value.status == 1
