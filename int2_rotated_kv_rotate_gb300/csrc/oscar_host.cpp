@@ -1293,7 +1293,9 @@ oscar_status oscar_evict(oscar_cache* c, int layer, const float* weights, float*
         return fail(OSCAR_ERR_INVALID_ARG, "weights, weights_out and kept must not overlap");
   oscar_status st = check_device(c);
   if (st) return st;
-  const int e = launch_evict(kernel_params(c), layer, weights, weights_out, kept, int(c->ev_reqs.size()), c->ev_max_pages,
+  int max_len = 0;
+  for (const EvictReq& r : c->ev_reqs) max_len = std::max(max_len, r.L);
+  const int e = launch_evict(kernel_params(c), layer, weights, weights_out, kept, int(c->ev_reqs.size()), max_len, c->ev_max_pages,
                              c->n_sm, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "evict launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;

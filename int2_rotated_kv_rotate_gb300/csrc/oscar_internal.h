@@ -196,10 +196,10 @@ int encode_page_map(const KernelParams& kp, void* map);
 int launch_shared(const KernelParams& kp, int layer, const void* map, const void* q, uint8_t* partials, int n_sm,
                   void* stream, int* launches);
 
-// Eviction of one layer (evict.cu): kept int32 as the weights' shape.  max_keep_pages: the
-// most new pages of a request of the plan.
+// Eviction of one layer (evict.cu): kept int32 as the weights' shape.  max_len and
+// max_keep_pages: the longest request of the plan, and the most new pages of one.
 int launch_evict(const KernelParams& kp, int layer, const float* weights, float* weights_out, int* kept, int n_req,
-                 int max_keep_pages, int n_sm, void* stream, int* launches);
+                 int max_len, int max_keep_pages, int n_sm, void* stream, int* launches);
 
 // CTAs of the decode kernel of this shape that fit on the GPU at once (occupancy x SMs);
 // the planner sizes work items so that one wave holds them all.

@@ -253,6 +253,24 @@ def test_evict_a_long_row_and_many_heads():
         cache.evict_cancel()
 
 
+@pytest.mark.parametrize("lens", [[30000] * 3 + [9000, 20481, 100], [90000] + [33000] * 4 + [5], [25000] * 2 + [3000] * 8])
+def test_evict_rows_of_one_and_of_several_ctas(lens):
+    """Row counts and lengths on either side of the CTAs a row gets and of what they hold."""
+    hkv = 8
+    cache, slots = make(32, hkv, lens, spare=sum(-(-L // 64) for L in lens))
+    kv = fill(cache, slots, lens)[0]
+    g = torch.Generator(device="cuda").manual_seed(17)
+    for kind, share in (("heavy", 0.3), ("few", 0.62)):
+        keep = [max(1, int(L * share)) for L in lens]
+        W = draw_weights(kind, cache.new_weights().shape, g)
+        cache.evict_begin(slots, keep, n_sink=1)
+        w_out, kept = cache.evict(0, W)
+        for i, s in enumerate(slots):
+            pages = cache.bf16_pages(0)[torch.tensor(cache.evict_pages(s), dtype=torch.long, device="cuda")]
+            check_evicted(cache, i, s, kv[i], pages, W, w_out, kept, keep[i], 1, 0, lens[i], kind)
+        cache.evict_cancel()
+
+
 def test_evict_leaves_shared_pages_and_other_slots_alone():
     lens = [640, 0, 200]
     cache, slots = make(4, 1, [640, 640, 200], spare=20)
