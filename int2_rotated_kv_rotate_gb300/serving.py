@@ -10,6 +10,12 @@ step through the library's calls, and frees a request's pages when it finishes. 
 loop runs the INT2 cache and the uncompressed BF16 cache, each sized to the same byte
 budget; the number of requests that fit at once is what differs.
 
+Around the attention the loop can run what a model's serving step runs: rotary positions on
+the queries and the new keys (`rotary`); the BF16 cache's decode with shared prefixes attended
+once (`share_decode`); and, on the BF16 cache, eviction of the tokens with the least
+accumulated attention weight once a request holds more than `evict_above` of them, down to
+`evict_to`, so that a long request stays within a bounded number of pages.
+
 Scheduling: first come, first served.  A request is admitted when a slot is free and the
 free pages cover its final length on top of what the running requests will still need
 (so a running request never runs out of pages).  A prefix holder is a slot that holds
@@ -43,7 +49,8 @@ class Request:
     gen: int  # tokens generated (decode steps)
     group: int = -1  # shared-prefix group, -1 = none
     slot: int = -1
-    length: int = 0
+    length: int = 0  # tokens held in the cache
+    position: int = 0  # tokens seen: the next token's position (= length unless some were evicted)
     generated: int = 0
     shared: int = 0  # prompt tokens mapped from the group's prefix holder
 
@@ -123,7 +130,14 @@ class ServingLoop:
 
     def __init__(self, w: wl.Workload, fmt: int, budget_bytes: int, tokens: TokenSource, layer_params=None,
                  max_requests: int = 128, max_len: int = 1 << 16, prefix_tokens: int = 0,
-                 prefill_chunk: int = 16384, device="cuda"):
+                 prefill_chunk: int = 16384, device="cuda", rotary=None, share_decode: bool = False,
+                 evict_above: int = 0, evict_to: int = 0, n_sink: int = 4, n_recent: int = 64):
+        if (share_decode or evict_above) and fmt in _INT2:
+            raise ValueError("share_decode and eviction need the BF16 format")
+        if share_decode and evict_above:
+            raise ValueError("share_decode and eviction exclude each other (the weights' decode does not share)")
+        if evict_above and not (0 < evict_to <= evict_above and n_sink >= 0 and n_recent >= 0 and n_sink + n_recent <= evict_to):
+            raise ValueError("eviction needs n_sink + n_recent <= evict_to <= evict_above")
         self.w, self.fmt, self.tokens = w, fmt, tokens
         self.S = w.n_sink if fmt in _INT2 else 0
         self.W = w.window if fmt in _INT2 else 0
@@ -134,9 +148,15 @@ class ServingLoop:
             RK, RV, cK, cV = layer_params
             for layer in range(w.n_layers):
                 self.cache.set_layer_params(layer, RK[layer], RV[layer], cK[layer], cV[layer])
+        self.rotary, self.share_decode = rotary, share_decode
+        self.evict_above, self.evict_to, self.protect = evict_above, evict_to, (n_sink, n_recent)
+        if evict_above:
+            self.weights = [self.cache.new_weights() for _ in range(w.n_layers)]
+            self._weights_out, self._kept = self.cache.new_weights(), torch.empty(
+                self.weights[0].shape, dtype=torch.int32, device=device)
         self.holders = {}  # group -> holder slot
         self.stats = dict(steps=0, generated=0, completed=0, prefill_tokens=0, shared_tokens=0, prefix_hits=0,
-                          max_batch=0, batch_sum=0, decode_s=0.0, wall_s=0.0, max_pages_used=0)
+                          max_batch=0, batch_sum=0, decode_s=0.0, wall_s=0.0, max_pages_used=0, evictions=0)
 
     # ------------------------------------------------------------------ pages
     def _need(self, L: int) -> int:
@@ -163,6 +183,11 @@ class ServingLoop:
             idx = self.tokens.index(layer, pieces)
             K = self.tokens.K.index_select(0, idx)
             V = self.tokens.V.index_select(0, idx)
+            if self.rotary is not None:
+                if layer == 0:
+                    positions = torch.cat([torch.arange(a, a + n, dtype=torch.int32, device=K.device)
+                                           for a, n in zip(starts, counts)])
+                self.rotary.apply(positions, K, q_out=K)
             c.append(layer, K, V)
         c.commit()
 
@@ -193,8 +218,14 @@ class ServingLoop:
 
     def _future_pages(self) -> int:
         """Pages the running requests will still take before they finish."""
-        return sum(max(0, self._need(r.prompt + r.gen) - max(self._need(r.length), r.shared // 64))
-                   for r in self.running)
+        return sum(max(0, self._peak_pages(r) - max(self._need(r.length), r.shared // 64)) for r in self.running)
+
+    def _peak_pages(self, r: Request) -> int:
+        """The most pages a request holds at once: with eviction, its own up to the step that
+        crosses the limit and the new ones it then moves to."""
+        if not self.evict_above or r.prompt + r.gen <= self.evict_above:
+            return self._need(r.prompt + r.gen)
+        return self._need(max(r.prompt, self.evict_above) + 1) + self._need(self.evict_to)
 
     def _admit(self, waiting) -> list:
         admitted = []
@@ -209,7 +240,7 @@ class ServingLoop:
             if sh and self._holder(r.group) is None:
                 sh = 0
             free_pages, free_slots = self.cache.stats()
-            own = self._need(r.prompt + r.gen) - sh // 64
+            own = self._peak_pages(r) - sh // 64
             if free_slots == 0 or free_pages - self._future_pages() < own:
                 break
             waiting.pop(0)
@@ -219,7 +250,10 @@ class ServingLoop:
                 r.shared = sh
                 self.stats["shared_tokens"] += sh
                 self.stats["prefix_hits"] += 1
-            r.length = sh
+            r.length = r.position = sh
+            if self.evict_above:
+                for wt in self.weights:
+                    wt[r.slot].zero_()
             admitted.append(r)
             self.running.append(r)
         # prefill the admitted prompts, in chunks
@@ -240,6 +274,7 @@ class ServingLoop:
             self._append(batch, starts, counts)
             for r, n in zip(batch, counts):
                 r.length += n
+                r.position += n
                 self.stats["prefill_tokens"] += n
             admitted = [r for r in admitted if r.length < r.prompt]
         return admitted
@@ -250,12 +285,14 @@ class ServingLoop:
         reqs = self.running
         slots = [r.slot for r in reqs]
         c.reserve(slots, [1] * len(reqs))
-        c.plan(slots)
+        c.plan(slots, flags=N.OSCAR_PLAN_SHARED_PREFIX if self.share_decode else 0)
         # pool rows of every request's new token and query, all layers: row = (A * stream +
         # B * layer + position) mod P, one device tensor per step
         tk = self.tokens
-        base = torch.tensor([[TokenSource.A * TokenSource.stream(r, r.length, self.prefix) + r.length,
-                              TokenSource.A * (r.rid + 17) + r.length] for r in reqs], dtype=torch.long)
+        base = torch.tensor([[TokenSource.A * TokenSource.stream(r, r.position, self.prefix) + r.position,
+                              TokenSource.A * (r.rid + 17) + r.position] for r in reqs], dtype=torch.long)
+        if self.rotary is not None:
+            positions = torch.tensor([r.position for r in reqs], dtype=torch.int32).to(tk.device)
         rows = ((base.to(tk.device)[None] + TokenSource.B * torch.arange(self.w.n_layers, device=tk.device)[:, None, None])
                 % tk.P)  # [layer, request, (token, query)]
         for layer in range(self.w.n_layers):
@@ -263,18 +300,42 @@ class ServingLoop:
             K = tk.K.index_select(0, idx)
             V = tk.V.index_select(0, idx)
             q = tk.Q.index_select(0, qi)
+            if self.rotary is not None:
+                self.rotary.apply(positions, q, K, q_out=q, k_out=K)
             o32 = torch.empty(q.shape, dtype=torch.float32, device=q.device) if on_output else None
             if self.fmt in _INT2:
                 out = c.append_decode(layer, K, V, q, out_f32=o32)
             else:
                 c.bf16_append(layer, K, V)
-                out = c.decode(layer, q, out_f32=o32)
+                if self.evict_above:
+                    out, _ = c.decode_weights(layer, q, self.weights[layer], out_f32=o32)
+                else:
+                    out = c.decode(layer, q, out_f32=o32)
             if on_output:
                 on_output(self.stats["steps"], layer, list(reqs), K, V, q, out, o32)
         c.commit()
         for r in reqs:
             r.length += 1
+            r.position += 1
             r.generated += 1
+
+    def _evict_long(self, on_evict: Optional[Callable]):
+        """Evict from the requests that hold more tokens than the limit and still generate."""
+        reqs = [r for r in self.running if r.length > self.evict_above and r.generated < r.gen]
+        if not reqs:
+            return
+        c, slots = self.cache, [r.slot for r in reqs]
+        c.evict_begin(slots, [self.evict_to] * len(reqs), *self.protect)
+        idx = torch.tensor(slots, dtype=torch.long).to(self.tokens.device)
+        for layer in range(self.w.n_layers):
+            c.evict(layer, self.weights[layer], self._weights_out, self._kept)
+            if on_evict:
+                on_evict(layer, reqs, self.weights[layer], self._kept)
+            self.weights[layer].index_copy_(0, idx, self._weights_out.index_select(0, idx))
+        c.evict_commit()
+        for r in reqs:
+            r.length, r.shared = self.evict_to, 0
+        self.stats["evictions"] += len(reqs)
 
     def _warm_gathers(self, n_max: int) -> None:
         """Run the step's gathers once for every batch size (set-up, untimed): the first use
@@ -289,7 +350,8 @@ class ServingLoop:
              % tk.P)
         torch.cuda.synchronize(tk.device)
 
-    def run(self, requests, on_output: Optional[Callable] = None, on_step: Optional[Callable] = None):
+    def run(self, requests, on_output: Optional[Callable] = None, on_step: Optional[Callable] = None,
+            on_evict: Optional[Callable] = None):
         """Serve every request to completion; returns the statistics."""
         waiting = list(requests)
         self._warm_gathers(min(len(requests), self.cache.cfg.max_requests))
@@ -315,6 +377,8 @@ class ServingLoop:
             st["batch_sum"] += n
             st["max_batch"] = max(st["max_batch"], n)
             st["max_pages_used"] = max(st["max_pages_used"], free0 - self.cache.stats()[0])
+            if self.evict_above:
+                self._evict_long(on_evict)
             done = [r for r in self.running if r.generated >= r.gen]
             for r in done:
                 self.cache.free(r.slot)
