@@ -189,7 +189,7 @@ oscar_status oscar_plan_decode(oscar_cache* cache, const int* slots, int n_req, 
  * several longer ones) have those pages attended once for all of them, as one more launch
  * of oscar_bf16_decode_attention before the decode's own; each request's further pages and
  * the merge are as without the flag.  Results are those of the plan without it, up to the
- * rounding of the sums.  Where sharing would save too few reads to pay for the launch, the
+ * rounding of the sums (and values below 2^78: the shared sums carry factors up to 2^32).  Where sharing would save too few reads to pay for the launch, the
  * plan goes without it; with OSCAR_PLAN_SHARED_ALWAYS (only together with it) it never does.
  * A decode captured under a plan with the flag may be replayed under any later plan; one
  * captured without it may not be replayed under a plan with shared runs. */
@@ -285,7 +285,7 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* cache, int layer, const void
  * 16-byte aligned; weights_out, same shape: the rows of the listed slots become the kept
  * tokens' weights, then zeros to the end of the row; kept int32, same shape: the positions
  * (before the eviction) of the kept tokens, entries from keep on stay as they are.  The
- * three must not overlap.
+ * three must not overlap.  Every layer goes before the commit, in any order.
  * Step 3 (host): oscar_evict_commit makes the new pages the requests' (uploads their
  * page-table rows on `stream`) and frees the old ones; plan again before decoding.
  * oscar_evict_cancel gives the new pages back instead.

@@ -305,8 +305,8 @@ int launch_evict(const KernelParams& kp, int layer, const float* weights, float*
                                         : launch_select<8>(kp, weights, weights_out, kept, n_req, max_len, n_sm, stream);
   if (e) return e;
   *launches += 1;
-  if (max_keep_pages <= 0) return 0;  // no request gives tokens up and keeps any
-  const dim3 grid(unsigned(max_keep_pages), unsigned(kp.n_kv_heads), unsigned(n_req < 65535 ? n_req : 65535));
+  // (also where no request gives tokens up: a captured launch serves later plans)
+  const dim3 grid(unsigned(max_keep_pages > 0 ? max_keep_pages : 1), unsigned(kp.n_kv_heads), unsigned(n_req < 65535 ? n_req : 65535));
   e = launch_ex(evict_gather_kernel, grid, dim3(kGatherThreads), 0, stream, kp, layer, static_cast<const int*>(kept));
   if (!e) *launches += 1;
   return e;

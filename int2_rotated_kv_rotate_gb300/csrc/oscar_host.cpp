@@ -379,17 +379,27 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
   // their own.
   const int per_item = kSharedRows / G;  // members of an item at most
   long long best = -1;
-  int chunk = 1, longest = 0;
+  int chunk = 0, longest = 0;
   for (const Run& r : runs) longest = std::max(longest, r.end - r.begin);
   for (int parts = 1; parts <= std::min(longest, 64); ++parts) {
     const int ch = ceil_div(longest, parts);
-    long long items = 0;
-    for (const Run& r : runs) items += (long long)Hkv * ceil_div(r.hi - r.lo, per_item) * ceil_div(r.end - r.begin, ch);
+    long long items = 0, n_slots = 0;
+    for (const Run& r : runs) {
+      const long long segs = (long long)Hkv * ceil_div(r.end - r.begin, ch);
+      items += segs * ceil_div(r.hi - r.lo, per_item);
+      n_slots += segs * (r.hi - r.lo) * ((r.hi - r.lo) * G <= kSharedRows / 2 ? 2 : 1);
+    }
+    // (the other half of the partial slots is the private items')
+    if (items > (long long)c->lay.max_shared_items || n_slots > (long long)c->lay.max_decode_items / 2) continue;
     const long long cost = 8 * ((items + c->n_sm - 1) / c->n_sm) * (ch + kSharedItemPages) + 2 * parts;
     if (best < 0 || cost < best) {
       best = cost;
       chunk = ch;
     }
+  }
+  if (chunk == 0) {  // nothing shared, or no room for the runs' partials
+    out.first_private.assign(n, 0);
+    return out;
   }
   std::vector<int> seg_end(runs.size());
   for (size_t k = 0; k < runs.size(); ++k) {  // parents come before their children
@@ -859,8 +869,6 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       c->map_ready = true;
     }
     runs = find_shared_runs(c, slots, Ls, (flags & OSCAR_PLAN_SHARED_ALWAYS) != 0);
-    if (runs.items.size() > c->lay.max_shared_items)
-      return fail(OSCAR_ERR_INVALID_ARG, "plan of %zu shared items exceeds %zu", runs.items.size(), c->lay.max_shared_items);
   } else {
     runs.first_private.assign(n_req, 0);
     runs.n_segs.assign(n_req, 0);
@@ -920,7 +928,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
         break;
       }
   auto split_count = [](int a, int b, int step) { return (a > 0 ? ceil_div(a, step) : 0) + (b > a ? ceil_div(b - a, step) : 0); };
-  long long n_bf_items = 0;
+  long long n_bf_items = 0, n_shared_slots = 0;
+  for (int i = 0; i < n_req; ++i) n_shared_slots += (long long)Hkv * runs.n_segs[i];
   // BF16 items of one CTA chunk: 16 tokens per warp
   const int bf_item = is_int2(c) ? 16 * nw : kBf16ItemTokens;
   for (int i = 0; i < n_req; ++i) n_bf_items += (long long)Hkv * split_count(bfnew_of[i], nbf_of[i], bf_item);
@@ -950,7 +959,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       chunk = int(std::max<long long>(4, item_bytes / page_bytes));
     }
     // the plan must fit the item buffers
-    while (chunk < max_np && count_items(chunk) > (long long)c->lay.max_decode_items)
+    while (chunk < max_np && count_items(chunk) + n_shared_slots > (long long)c->lay.max_decode_items)
       chunk = std::min(max_np, chunk + chunk / 4 + 1);
   }
   std::vector<DecodeReq> reqs(n_req);
@@ -1198,6 +1207,10 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q,
     return fail(OSCAR_ERR_INVALID_ARG, "NULL q, out, weights_out or workspace");
   if ((reinterpret_cast<uintptr_t>(weights_in) | reinterpret_cast<uintptr_t>(weights_out)) % 4)
     return fail(OSCAR_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  const uintptr_t wi = reinterpret_cast<uintptr_t>(weights_in), wo = reinterpret_cast<uintptr_t>(weights_out);
+  const uintptr_t w_bytes = uintptr_t(c->cfg.max_requests) * c->cfg.n_kv_heads * uintptr_t(oscar_weights_stride(c)) * 4;
+  if (wi && wi != wo && wi < wo + w_bytes && wo < wi + w_bytes)
+    return fail(OSCAR_ERR_INVALID_ARG, "weights_in and weights_out overlap");
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(OSCAR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const WeightsWorkspace w = weights_workspace(c, c->dec_n_req);
   if (ws_bytes < w.total) return fail(OSCAR_ERR_INVALID_ARG, "workspace %zu < %zu bytes", ws_bytes, w.total);

@@ -50,14 +50,15 @@ class RotaryEmbedding:
         self.steps = torch.tensor(signed, dtype=torch.int64).to(device)
         self.device = self.steps.device
 
-    def _check(self, name: str, x, rows: Optional[int], like=None):
-        if x.dim() != 3 or x.shape[2] != self.head_dim or (self.head_dim > 1 and x.stride(2) != 1):
+    def _check(self, name: str, x, rows: int, like=None):
+        shape = x.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or x.stride()[2] != 1:
             raise ValueError(f"{name} must be [rows, heads, {self.head_dim}] with contiguous channels")
         if x.dtype not in _DTYPES or x.device != self.device:
             raise ValueError(f"{name} must be bf16, fp16 or fp32 on {self.device}")
-        if rows is not None and x.shape[0] != rows:
+        if shape[0] != rows:
             raise ValueError(f"{name} must have {rows} rows")
-        if like is not None and (x.shape != like.shape or x.dtype != like.dtype):
+        if like is not None and (shape != like.shape or x.dtype != like.dtype):
             raise ValueError(f"{name} must have the shape and dtype of its input")
 
     def apply(self, positions, q, k=None, *, q_out=None, k_out=None, transpose: bool = False, stream=None):
@@ -70,14 +71,20 @@ class RotaryEmbedding:
             raise ValueError(f"positions must be contiguous int32 or int64 [rows] on {self.device}")
         rows = positions.shape[0]
         self._check("q", q, rows)
-        pairs = [(q, torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out)]
-        self._check("q_out", pairs[0][1], rows, q)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out is not q:
+            self._check("q_out", q_out, rows, q)
+        pairs = [(q, q_out)]
         if k is not None:
             self._check("k", k, rows)
             if k.dtype != q.dtype:
                 raise ValueError("q and k must have one dtype")
-            pairs.append((k, torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out))
-            self._check("k_out", pairs[1][1], rows, k)
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            elif k_out is not k:
+                self._check("k_out", k_out, rows, k)
+            pairs.append((k, k_out))
         elif k_out is not None:
             raise ValueError("k_out without k")
         flags = ((N.OSCAR_ROPE_INTERLEAVED if self.interleaved else 0) | (N.OSCAR_ROPE_TRANSPOSE if transpose else 0)
@@ -89,4 +96,4 @@ class RotaryEmbedding:
         else:
             with torch.cuda.device(self.device):
                 N.oscar_rope(*args)
-        return (pairs[0][1], pairs[1][1]) if k is not None else pairs[0][1]
+        return (q_out, k_out) if k is not None else q_out

@@ -300,6 +300,30 @@ def test_evict_leaves_shared_pages_and_other_slots_alone():
     assert cache.stats()[0] == cache.cfg.max_pages
 
 
+def test_a_captured_eviction_serves_later_plans():
+    """Captured where nothing moves, replayed where it does, for more requests and longer rows."""
+    lens = [100, 700, 300]
+    cache, slots = make(4, 1, lens, spare=30)
+    kv = fill(cache, slots, lens)[0]
+    W = draw_weights("heavy", cache.new_weights().shape, torch.Generator(device="cuda").manual_seed(5))
+    w_out, kept = torch.zeros_like(W), torch.zeros(W.shape, dtype=torch.int32, device="cuda")
+    cache.evict_begin([slots[0]], [100])
+    cache.evict(0, W, weights_out=w_out, kept=kept)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.evict(0, W, weights_out=w_out, kept=kept)
+    cache.evict_cancel()
+    keeps = [64, 333, 300]
+    cache.evict_begin(slots, keeps)
+    graph.replay()
+    for i, s in enumerate(slots):
+        pages = cache.bf16_pages(0)[torch.tensor(cache.evict_pages(s), dtype=torch.long, device="cuda")]
+        check_evicted(cache, i, s, kv[i], pages, W, w_out, kept, keeps[i], 0, 0, lens[i], "replay")
+    cache.evict_commit()
+    assert cache.status() == (0, 0)
+
+
 def test_cancel_and_state_rules():
     lens = [500, 300]
     cache, slots = make(4, 1, lens, spare=8, max_requests=3)
@@ -386,6 +410,10 @@ def test_decode_weights_refusals():
             N.oscar_bf16_decode_weights(cache.handle, a["layer"], a["q"], a["out"], a["weights_in"], a["weights_out"],
                                         a["workspace"])
         assert e.value.status == 1 and N.oscar_last_launch_count() == 0
+    two = torch.zeros(2 * w.numel(), device="cuda")
+    half = two[w.numel() // 2:].data_ptr()
+    assert N.lib().oscar_bf16_decode_weights(cache.handle, 0, q.data_ptr(), out.data_ptr(), two.data_ptr(), half,
+                                             ws.data_ptr(), ws.numel(), None, None) == 1
     for bad in (w[..., :-1], w.double(), w.cpu()):
         with pytest.raises(ValueError):
             cache.decode_weights(0, q, bad)

@@ -304,6 +304,18 @@ def test_a_bad_page_is_flagged_and_skipped():
     b.check(slots, label="mended")
 
 
+def test_more_runs_than_the_plan_has_room_for():
+    """A plan whose runs would fill the partial slots goes without some or all of the sharing."""
+    b = Batch(1, 4, 96, 400, 100)
+    first = b.new(64 * 90)
+    slots = [first]
+    for i in range(95):  # every request leaves the prefix one page further on
+        slots.append(b.new(1 + i % 40, first, 90 - i % 85))
+    b.check(slots, label="comb")
+    assert b.cache.shared_info()[1] > 0
+    b.check(slots, msp=1, label="comb, one page an item")
+
+
 def test_refusals():
     b = Batch(1, 4, 2, 20, 8)
     first = b.new(64 * 4)
