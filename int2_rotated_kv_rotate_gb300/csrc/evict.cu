@@ -3,8 +3,8 @@
 // the order of their positions, and are copied into the request's new pages.
 //
 // evict_select_kernel, one cluster of CTAs per (request, kv-head): a radix select.  Each CTA
-// keeps its slice of the row's weights in shared memory (rows too long for that are read
-// again from L2).
+// keeps its slice of the row's keys in shared memory (what does not fit is read again from
+// L2).
 // A weight's key is its bits mapped so that unsigned order is numeric order; protected
 // tokens (the sinks and the most recent ones) take the greatest key.  Three passes (11, 11
 // and 10 bits) narrow down the key of the keep-th token: each CTA counts its slice of the
@@ -97,7 +97,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const int tiles = (rq.L + kTile - 1) / kTile, per = (tiles + kCluster - 1) / kCluster;
     const int t0 = min(tiles, rank * per), t1 = min(tiles, t0 + per);
     const bool all = rq.keep >= rq.L, choose = !all && rq.keep > 0;
-    const bool cached = t1 - t0 <= slice_tiles;
+    const int t_cached = min(t1, t0 + slice_tiles);
     auto token = [&](int tile) { return tile * kTile + 4 * int(threadIdx.x); };
     auto make_keys = [&](int tile) {  // (rows are whole pages long)
       const int t = token(tile), protect_from = rq.L - rq.n_recent;
@@ -111,7 +111,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       }
       return k;
     };
-    auto keys = [&](int tile) { return cached ? slice[(tile - t0) * kThreads + int(threadIdx.x)] : make_keys(tile); };
+    auto keys = [&](int tile) { return tile < t_cached ? slice[(tile - t0) * kThreads + int(threadIdx.x)] : make_keys(tile); };
     // f(token, key) for each of the thread's tokens of a tile
     auto each = [&](int tile, auto f) {
       const int t = token(tile);
@@ -125,11 +125,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     uint32_t edge = 0, ties = 0;  // the keep-th key; tokens equal to it that stay
     uint32_t above_before = 0, equal_before = 0;
     if (choose) {
-      if (cached) {
 #pragma unroll 4
-        for (int tile = t0; tile < t1; ++tile)
-          if (token(tile) < rq.L) slice[(tile - t0) * kThreads + int(threadIdx.x)] = make_keys(tile);
-      }
+      for (int tile = t0; tile < t_cached; ++tile)
+        if (token(tile) < rq.L) slice[(tile - t0) * kThreads + int(threadIdx.x)] = make_keys(tile);
       for (int e = threadIdx.x; e < 3 * kBins / 4; e += kThreads) reinterpret_cast<uint4*>(hist[0])[e] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       uint32_t need = uint32_t(rq.keep);
@@ -226,8 +224,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 constexpr int kGatherThreads = 256;
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(KernelParams kp, int layer,
                                                                       const int* __restrict__ kept) {
-  pdl_wait();
-  pdl_trigger();
   const int n_req = reinterpret_cast<const int*>(kp.base + kp.lay.evict_plan)[0];
   const EvictReq* reqs = reinterpret_cast<const EvictReq*>(kp.base + kp.lay.evict_plan + 256);
   const int kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -286,7 +282,7 @@ int launch_select(const KernelParams& kp, const float* weights, float* weights_o
     attr = true;
   }
   const int tiles = (max_len + kTile - 1) / kTile, per = (tiles + kCluster - 1) / kCluster;
-  const int slice_tiles = per <= kMost ? per : 0;
+  const int slice_tiles = per < kMost ? per : kMost;
   const int rows = n_req * kp.n_kv_heads, clusters = rows < 8 * n_sm ? rows : 8 * n_sm;
   return launch_ex(evict_select_kernel<kCluster>, dim3(kCluster * clusters), dim3(kThreads),
                    size_t(slice_tiles) * kTileBytes, stream, kp, weights, weights_out, kept, slice_tiles);
@@ -296,8 +292,8 @@ int launch_select(const KernelParams& kp, const float* weights, float* weights_o
 int launch_evict(const KernelParams& kp, int layer, const float* weights, float* weights_out, int* kept, int n_req,
                  int max_len, int max_keep_pages, int n_sm, void* stream, int* launches) {
   // CTAs of a row: as many as leave the launch one wave (two CTAs an SM), since a CTA's scans
-  // and barriers take as long as some five tiles.  64 rows of 100000 tokens: 62 us with four,
-  // 85 us with eight; 224 rows of up to 32768: 49 us with one, 57 us with four.
+  // and barriers take as long as some five tiles.  64 rows of 100000 tokens: 51 us with four,
+  // 85 us with eight; 224 rows of up to 32768: 42 us with one, 57 us with four.
   const long long rows = (long long)n_req * kp.n_kv_heads, wave = 2LL * n_sm;
   const int tiles = (max_len + kTile - 1) / kTile;
   int e = rows * 4 > wave || tiles <= 2 ? launch_select<1>(kp, weights, weights_out, kept, n_req, max_len, n_sm, stream)
@@ -307,7 +303,10 @@ int launch_evict(const KernelParams& kp, int layer, const float* weights, float*
   *launches += 1;
   // (also where no request gives tokens up: a captured launch serves later plans)
   const dim3 grid(unsigned(max_keep_pages > 0 ? max_keep_pages : 1), unsigned(kp.n_kv_heads), unsigned(n_req < 65535 ? n_req : 65535));
-  e = launch_ex(evict_gather_kernel, grid, dim3(kGatherThreads), 0, stream, kp, layer, static_cast<const int*>(kept));
+  // Not as a dependent launch: the selection's large shared memory would leave the copy, resident
+  // before the SM is empty, little L1 for its loads in flight (361 against 300 us on 8 x 100000).
+  evict_gather_kernel<<<grid, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(kp, layer, kept);
+  e = int(cudaGetLastError());
   if (!e) *launches += 1;
   return e;
 }
