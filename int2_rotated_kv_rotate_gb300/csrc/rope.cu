@@ -193,11 +193,13 @@ int launch_t(RopeParams p, bool aligned, int n_sm, void* stream, int* launches) 
   p.chunks = (H + most - 1) / most;
   p.head_lanes = (H + p.chunks - 1) / p.chunks;
   const int threads = (p.units * p.head_lanes + 31) / 32 * 32;
-  // Rows of a CTA: what one wave of CTAs needs, at most 16.  4099 rows of 40 bf16 heads: 16.9 us in one wave, 18.9 and 21.5 us with 4 and 8 rows
-  // a CTA (a ragged second wave); 16384 rows of 72 heads: 112, 107 and 109 us with 4, 8, 16.
+  // Rows of a CTA: full waves of CTAs of at most 16 rows.  4099 rows of 40 bf16 heads: 16.9 us
+  // in one wave of 9 rows a CTA, 18.9 and 21.5 us with 4 and 8 (a ragged second wave); 16384
+  // rows of 72 heads: 112, 107 and 109 us with 4, 8 and 16.
   const int per_sm = p.interleaved ? kPerSMInterleaved : kPerSMHalf;
   const long long wave = std::max<long long>(1, (long long)n_sm * (512 * per_sm / threads) / p.chunks);
-  p.rows_per_cta = int(std::min<long long>(16, (p.n_rows + wave - 1) / wave));
+  const long long waves = (p.n_rows + 16 * wave - 1) / (16 * wave);
+  p.rows_per_cta = int((p.n_rows + waves * wave - 1) / (waves * wave));
   const size_t smem = size_t(p.rows_per_cta) * pairs * sizeof(float2);
   const long long grid = (p.n_rows + p.rows_per_cta - 1) / p.rows_per_cta * p.chunks;
   if (grid > 0x7fffffffLL) return int(cudaErrorInvalidConfiguration);
