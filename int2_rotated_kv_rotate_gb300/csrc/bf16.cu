@@ -21,6 +21,8 @@ namespace {
 // attended.  Plans of one wave (small steps, latency-bound) run the deeper pipeline
 // (NBUF 3, two CTAs per SM); larger plans NBUF 2 (three CTAs per SM, more CTAs to overlap
 // one another's prologues and merges).
+template <int NBUF>
+constexpr int kBf16PerSM = NBUF == 3 ? 2 : 3;  // (told to the compiler, which else keeps to fewer registers and spills)
 template <int G, int NBUF>
 constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::kBytes;
 
@@ -31,7 +33,7 @@ constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::k
 // merge, which reads the shared runs' partials, waits for its end: the private items of the
 // SMs that it leaves free run beside it.
 template <int G, int NBUF, bool WEIGHTS>
-__global__ void __launch_bounds__(128) bf16_split_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q,
+__global__ void __launch_bounds__(128, kBf16PerSM<NBUF>) bf16_split_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q,
                                                          uint8_t* __restrict__ partials, uint16_t* __restrict__ out,
                                                          float* __restrict__ out_f32, float* __restrict__ scores,
                                                          float2* __restrict__ ml, bool after_shared) {
