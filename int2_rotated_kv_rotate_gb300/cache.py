@@ -5,6 +5,8 @@ of the C ABI (see include/oscar.h for semantics and layouts).
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _native as N
@@ -144,6 +146,13 @@ class KVCache:
         """A layer's accumulated attention weights, zeros: fp32 [request slots, H_kv, weights_stride]."""
         return torch.zeros(self._weights_shape(), device=self.device)
 
+    @staticmethod
+    def _on(stream):
+        """Context in which torch works on `stream` (None: the current one)."""
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
     def _weights_shape(self):
         if not self.weights_stride:
             raise ValueError("accumulated weights need the BF16 format")
@@ -181,10 +190,11 @@ class KVCache:
         them when this call makes the tensor).  Rows of other slots stay as they are (those of a
         weights_out that this call makes: as in weights)."""
         self._check_weights("weights", weights)
-        if weights_out is None:
-            weights_out = weights.clone()
-        if kept is None:
-            kept = torch.full(weights.shape, -1, dtype=torch.int32, device=self.device)
+        with self._on(stream):  # what this call makes is made in the launch's order
+            if weights_out is None:
+                weights_out = weights.clone()
+            if kept is None:
+                kept = torch.full(weights.shape, -1, dtype=torch.int32, device=self.device)
         self._check_weights("weights_out", weights_out)
         self._check_weights("kept", kept, torch.int32)
         N.oscar_evict(self.handle, layer, weights, weights_out, kept, stream)

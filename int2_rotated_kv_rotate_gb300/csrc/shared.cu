@@ -240,7 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         nv = cnt + 1;
       }
     }
-    if (!ok) {  // copies still in flight land before the CTA leaves
+    // the last arrivals on the stages' barriers come before the CTA leaves
+    for (uint32_t k = cnt > kStages ? cnt - kStages : 0; ok && k < cnt; ++k)
+      ok = wait2(ctl->k_empty[k % kStages], k / kStages, ctl->v_empty[k % kStages], k / kStages);
+    if (!ok) {  // copies still in flight land first, too
       for (uint32_t k = nk > kStages ? nk - kStages : 0; k < nk; ++k)
         mbar_wait(smem_u32(&ctl->k_full[k % kStages]), (k / kStages) & 1u);
       for (uint32_t k = nv > kStages ? nv - kStages : 0; k < nv; ++k)

@@ -300,6 +300,38 @@ def test_evict_leaves_shared_pages_and_other_slots_alone():
     assert cache.stats()[0] == cache.cfg.max_pages
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_another_stream(handle):
+    """Weights' decode and eviction on a stream that is not the current one, which is kept busy:
+    what the calls make is made in their stream's order."""
+    lens = [3000, 700]
+    cache, slots = make(4, 1, lens, spare=40)
+    kv = fill(cache, slots, lens)[0]
+    q = queries(2, 4, 3)
+    cache.plan(slots)
+    want = cache.decode_weights(0, q, cache.new_weights())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    w = cache.new_weights()
+    out = torch.empty_like(q)
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    cache.decode_weights(0, q, w, out=out, stream=stream)
+    cache.evict_begin(slots, [1000, 699], stream=stream)
+    w_out, kept = cache.evict(0, w, stream=stream)
+    side.synchronize()
+    assert torch.equal(w.cpu(), want[1].cpu()) and torch.equal(out.cpu(), want[0].cpu())
+    torch.cuda.synchronize()
+    for i, s in enumerate(slots):
+        pages = cache.bf16_pages(0)[torch.tensor(cache.evict_pages(s), dtype=torch.long, device="cuda")]
+        check_evicted(cache, i, s, kv[i], pages, w, w_out, kept, [1000, 699][i], 0, 0, lens[i], "side stream")
+    cache.evict_commit(stream=stream)
+    side.synchronize()
+
+
 def test_a_captured_eviction_serves_later_plans():
     """Captured where nothing moves, replayed where it does, for more requests and longer rows."""
     lens = [100, 700, 300]
