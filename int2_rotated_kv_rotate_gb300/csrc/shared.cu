@@ -8,8 +8,8 @@
 //   S = Q K^T      M = 128 rows, N = 64 tokens, K = 128 channels: Q and the page's keys in
 //                  shared memory, 128-byte swizzle, S in tensor memory;
 //   P = 2^(S - m)  one thread a row: the whole row of the page in registers, so its maximum
-//                  and sum need no other thread; P goes back over S as bf16 hi and lo halves
-//                  (16 bits, as the private items keep);
+//                  and sum need no other thread; P goes back as bf16 hi and lo halves (16
+//                  bits, as the private items keep);
 //   O += P V       M = 128, N = 128 channels, K = 64 tokens, hi then lo: P from tensor memory,
 //                  the page's values in shared memory as they are stored (channels contiguous).
 // The reference m of a row moves only when a score exceeds it by more than 32 (base 2), so O is
@@ -22,8 +22,10 @@
 // or, for runs of at most 128 rows, the even and the odd pages of one row block, each with a
 // partial slot of its own (one block's chain of S, softmax and O took 2400 cycles a page, more
 // than the 1470 of an SM's share of the copy rate for its 32 KB).  S of a block's next page is
-// computed while its softmax works on this one: two S / P buffers a block, 512 tensor-memory
-// columns in all.
+// computed as soon as its softmax has read this one's, beside O of the page before: a buffer of
+// S and one of P a block, 512 tensor-memory columns in all.  (With P over S in two buffers, S of
+// page n + 1 waited for O of page n - 1 and the softmax for S: 117.5 against
+// 114.8 us on 64 requests of 33000 shared tokens at GQA 8.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,11 +49,10 @@ static_assert(kBlocks == 2, "warps 4-7 and 8-11");
 struct Control {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[kBlocks];
-  uint64_t s_full[kBlocks][2], p_full[kBlocks][2];
-  // O holds the pages up to n and P n is read: barrier n & 1, completion n >> 1.  (A parity tells
-  // a completion from its neighbours only.  The warp that issues S n waits for page n - 2 when
-  // page n - 1 may be done already, but never page n.)
-  uint64_t o_done[kBlocks][2];
+  // Completion n of each is page n of the block: S is written, S is read, P is written, P is
+  // read and O holds the pages up to n.  Whoever waits for one of them waits for every page in
+  // order, and none gets two ahead (a parity tells a completion from its neighbours only).
+  uint64_t s_full[kBlocks], s_empty[kBlocks], p_full[kBlocks], o_done[kBlocks];
   uint64_t drain[2];
   uint32_t tmem;
   int abort;
@@ -61,8 +62,8 @@ constexpr int kOffControl = kOffStages + kStages * kPageKv;
 constexpr int kSmemBytes = kOffControl + int(sizeof(Control)) + 1024;  // + alignment to 1024
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-// Tensor-memory columns of block b: two S / P buffers of 64, then O of 128.
-constexpr uint32_t kBlockCols = 256, kColO = 128;
+// Tensor-memory columns of block b: S of 64, P of 64 (hi, lo), O of 128.
+constexpr uint32_t kBlockCols = 256, kColP = 64, kColO = 128;
 
 // A row's reference moves when a score exceeds it by this much (base 2).
 constexpr float kRaise = 32.f;
@@ -132,11 +133,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < kBlocks; ++b) {
       mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(smem_u32(&ctl->s_full[b][k]), 1);
-        mbar_init(smem_u32(&ctl->p_full[b][k]), kBlockRows);
-        mbar_init(smem_u32(&ctl->o_done[b][k]), 1);
-      }
+      mbar_init(smem_u32(&ctl->s_full[b]), 1);
+      mbar_init(smem_u32(&ctl->s_empty[b]), kBlockRows);
+      mbar_init(smem_u32(&ctl->p_full[b]), kBlockRows);
+      mbar_init(smem_u32(&ctl->o_done[b]), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->drain[i]), 1);
     ctl->abort = 0;
@@ -260,27 +260,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work w = load_work(ix);
       ok = wait(ctl->q_full[0], q0++);
       if (ok && w.blocks > 1) ok = wait(ctl->q_full[1], q1++);
-      int l0 = 0, l1 = 0;  // this item's pages of each block so far
       for (int i = 0; ok && i < w.pages; ++i) {
         const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
         for (int b = b0; ok && b < b1; ++b) {
           const uint32_t n = b ? n1++ : n0++;
-          // the buffer's last P (page n - 2) has been read; that of an earlier item was before
-          // the softmax handed over this item's queries
-          const bool reused = (b ? l1++ : l0++) >= 2;
-          uint64_t& last = ctl->o_done[b][n & 1];
-          if (b == b0) ok = reused ? wait2(ctl->k_full[st], lap, last, (n >> 1) - 1) : wait(ctl->k_full[st], lap);
-          else if (reused) ok = wait(last, (n >> 1) - 1);
+          if (b == b0) ok = n ? wait2(ctl->k_full[st], lap, ctl->s_empty[b], n - 1) : wait(ctl->k_full[st], lap);
+          else if (n) ok = wait(ctl->s_empty[b], n - 1);
           if (!ok) break;
           tmem::fence_after();
           if (elect_one()) {
-            const uint32_t d = tm + b * kBlockCols + (n & 1) * kPage;
+            const uint32_t d = tm + b * kBlockCols;
             const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kPageKv >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               tmem::mma_ss(d, qb + ((k >> 2) * (kQBlock / 2) + (k & 3) * 32) / 16, kb + ((k >> 2) * 8192 + (k & 3) * 32) / 16,
                            kIdS, k > 0);
-            tmem::commit(smem_u32(&ctl->s_full[b][n & 1]));
+            tmem::commit(smem_u32(&ctl->s_full[b]));
             if (b == b1 - 1) tmem::commit(smem_u32(&ctl->k_empty[st]));
           }
           __syncwarp();
@@ -310,17 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = b0; ok && b < b1; ++b) {
           const uint32_t n = b ? n1++ : n0++;
           const bool first = (b ? l1++ : l0++) == 0;
-          uint64_t& p = ctl->p_full[b][n & 1];
-          ok = b == b0 ? wait2(ctl->v_full[st], lap, p, n >> 1) : wait(p, n >> 1);
+          ok = b == b0 ? wait2(ctl->v_full[st], lap, ctl->p_full[b], n) : wait(ctl->p_full[b], n);
           if (!ok) break;
           tmem::fence_after();
           if (elect_one()) {
-            const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + (n & 1) * kPage;
+            const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + kColP;
             const uint64_t vb = vd + st * (kPageKv >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)  // hi then lo
               tmem::mma_ts(d, a + 8 * k, vb + (k & 3) * (2048 / 16), kIdO, !first || k > 0);
-            tmem::commit(smem_u32(&ctl->o_done[b][n & 1]));
+            tmem::commit(smem_u32(&ctl->o_done[b]));
             if (b == b1 - 1) tmem::commit(smem_u32(&ctl->v_empty[st]));
           }
           __syncwarp();
@@ -372,28 +366,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool idle = w.row0(b) + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
       const int pages = w.pages_of(b);
       for (int i = 0; i < pages; ++i, ++n) {
-        const uint32_t buf = tl + (n & 1) * kPage;
-        ok = wait(ctl->s_full[b][n & 1], n >> 1);
+        ok = wait(ctl->s_full[b], n);
         if (!ok) break;
+        // P and O of the page before (the item's first page: of an earlier item, long done)
+        auto last_done = [&] { return i == 0 || wait(ctl->o_done[b], n - 1); };
         if (idle) {
-          mbar_arrive(smem_u32(&ctl->p_full[b][n & 1]));
+          mbar_arrive(smem_u32(&ctl->s_empty[b]));
+          ok = last_done();
+          if (!ok) break;
+          mbar_arrive(smem_u32(&ctl->p_full[b]));
           continue;
         }
         tmem::fence_after();
         uint32_t s0[32], s1[32];
-        tmem::ld_x32(buf, s0);
-        tmem::ld_x32(buf + 32, s1);
+        tmem::ld_x32(tl, s0);
+        tmem::ld_x32(tl + 32, s1);
         tmem::wait_ld();
+        tmem::fence_before();
+        mbar_arrive(smem_u32(&ctl->s_empty[b]));
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 32; ++j) mx = max3(mx, __uint_as_float(s0[j]), __uint_as_float(s1[j]));
         mx *= scale;
         const bool raise = mx > m_ref + kRaise;  // also from -inf
+        bool waited = false;
         if (i == 0) {
           m_ref = mx;
         } else if (__any_sync(0xffffffffu, raise)) {
-          ok = wait(ctl->o_done[b][(n - 1) & 1], (n - 1) >> 1);
+          ok = last_done();
           if (!ok) break;
+          waited = true;
           tmem::fence_after();
           const float f = raise ? ex2(m_ref - mx) : 1.f;
           if (raise) m_ref = mx;
@@ -428,15 +430,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         float la, lb;
         unpack2(l2, la, lb);
         l += la + lb;
-        tmem::st_x32(buf, hi);
-        tmem::st_x32(buf + 32, lo);
+        if (!waited) {
+          ok = last_done();
+          if (!ok) break;
+          tmem::fence_after();
+        }
+        tmem::st_x32(tl + kColP, hi);
+        tmem::st_x32(tl + kColP + 32, lo);
         tmem::wait_st();
         tmem::fence_before();
-        mbar_arrive(smem_u32(&ctl->p_full[b][n & 1]));
+        mbar_arrive(smem_u32(&ctl->p_full[b]));
       }
       if (!ok) break;
       // ---- the rows' partials
-      if (pages > 0) ok = wait(ctl->o_done[b][(n - 1) & 1], (n - 1) >> 1);
+      if (pages > 0) ok = wait(ctl->o_done[b], n - 1);
       if (!ok) break;
       tmem::fence_after();
       const int m = w.row0(b) + r;
