@@ -16,6 +16,7 @@
 // evict_gather_kernel, one page of new tokens a CTA at a time: warp w copies eight tokens,
 // half a warp the 256 bytes of a row of K, the other half those of V, all eight loaded
 // before the first is stored.  HBM-bound: 1 KB a kept token and kv-head.
+// 8 x 100000 tokens of 8 kv-heads to a quarter: selection 51 us, copy 238 us (1.64 GB, 6.9 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -300,6 +300,45 @@ def test_evict_leaves_shared_pages_and_other_slots_alone():
     assert cache.stats()[0] == cache.cfg.max_pages
 
 
+def test_pages_past_four_gib():
+    """Every operator on pages whose byte offsets in the pool pass 32 bits."""
+    hkv, far = 8, 17000  # 256 KB a page
+    cache = KVCache(fmt=N.OSCAR_FORMAT_BF16, n_q_heads=32, n_kv_heads=hkv, n_layers=1, max_requests=4, max_pages=far + 60,
+                    max_pages_per_request=far)
+    below = cache.alloc()  # holds the pages below
+    for _ in range(2):
+        cache.reserve([below], [32 * far])
+        cache.commit()
+    w = wl.scaled(wl.WORKLOADS["tiny"], name="far", n_kv_heads=hkv)
+    first = cache.alloc()
+    K, V = wl.gen_kv(w, SEED, 0, 1, 0, 700, device="cuda")
+    cache.reserve([first], [700])
+    cache.append(0, K, V)
+    cache.commit()
+    assert min(cache.pages(first)) * cache.cfg.n_kv_heads * cache.layout.bf16_page_bytes > 1 << 32
+    second = cache.alloc()
+    cache.share_prefix(second, first, 640)
+    q = queries(2, 32, 8)
+    for flags in (0, N.OSCAR_PLAN_SHARED_PREFIX | N.OSCAR_PLAN_SHARED_ALWAYS):
+        cache.plan([first, second], flags=flags)
+        out32 = torch.empty(2, 32, 128, device="cuda")
+        out = cache.decode(0, q, out_f32=out32)
+        for i, n in ((0, 700), (1, 640)):
+            ref = torch.cat([attention(q[i, 4 * h:4 * h + 4], K[:n, h], V[:n, h])[0] for h in range(hkv)])
+            compare_decode(out32[i], out[i], ref.cpu().numpy(), f"flags {flags} request {i}")
+    cache.plan([first, second])
+    weights = cache.new_weights()
+    before = weights.clone()
+    cache.decode_weights(0, q, weights)
+    check_weights(weights[second], before[second], q[1], (K[:640], V[:640]), hkv, "far")
+    cache.evict_begin([first], [130])
+    w_out, kept = cache.evict(0, weights)
+    pages = cache.bf16_pages(0)[torch.tensor(cache.evict_pages(first), dtype=torch.long, device="cuda")]
+    check_evicted(cache, 0, first, (K, V), pages, weights, w_out, kept, 130, 0, 0, 700, "far")
+    cache.evict_commit()
+    assert cache.status() == (0, 0)
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_another_stream(handle):
     """Weights' decode and eviction on a stream that is not the current one, which is kept busy:
