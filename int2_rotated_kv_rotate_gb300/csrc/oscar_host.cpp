@@ -815,7 +815,7 @@ oscar_status oscar_plan_decode(oscar_cache* c, const int* slots, int n_req, int 
 }
 
 oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, int max_split_pages, uint32_t flags,
-                                  void* stream) {
+                                  void* stream) try {
   if (!c || !slots || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad plan arguments");
   if (flags & ~(OSCAR_PLAN_NARROW | OSCAR_PLAN_FOLDED_ROTATIONS | OSCAR_PLAN_SHARED_PREFIX |
@@ -1075,6 +1075,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   c->dec_shared_pages = runs.pages;
   c->plan_covers_reservation = c->reserved && n_reserved_planned == int(c->app_reqs.size());
   return OSCAR_OK;
+} catch (const std::bad_alloc&) {
+  return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed");
 }
 
 size_t oscar_decode_workspace_bytes(const oscar_cache* c) { return (c && c->planned) ? c->ws.total : 0; }
@@ -1223,7 +1225,7 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q,
 }
 
 oscar_status oscar_evict_begin(oscar_cache* c, const int* slots, const int* keep, int n_req, int n_sink, int n_recent,
-                               void* stream) {
+                               void* stream) try {
   if (!c || !slots || !keep || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad evict arguments");
   if (is_int2(c)) return fail(OSCAR_ERR_STATE, "eviction needs the BF16 format");
@@ -1286,6 +1288,8 @@ oscar_status oscar_evict_begin(oscar_cache* c, const int* slots, const int* keep
   c->ev_max_pages = max_pages;
   c->evicting = true;
   return OSCAR_OK;
+} catch (const std::bad_alloc&) {
+  return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed");
 }
 
 oscar_status oscar_evict(oscar_cache* c, int layer, const float* weights, float* weights_out, int* kept, void* stream) {
@@ -1327,20 +1331,21 @@ oscar_status oscar_evict_pages(const oscar_cache* c, int slot, int* pages, int n
   return OSCAR_OK;
 }
 
-oscar_status oscar_evict_commit(oscar_cache* c, void* stream) {
+oscar_status oscar_evict_commit(oscar_cache* c, void* stream) try {
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
   if (!c->evicting) return fail(OSCAR_ERR_STATE, "no eviction begun");
   Upload u;
   oscar_status st = begin_upload(c, &u);
   if (st) return st;
   std::vector<int> changed;
+  changed.reserve(c->ev_reqs.size());  // nothing below allocates
   for (size_t i = 0; i < c->ev_reqs.size(); ++i) {
     const EvictReq& e = c->ev_reqs[i];
     if (e.keep >= e.L) continue;
     Request& r = c->reqs[e.slot];
     for (int p : r.pages)
       if (--c->refcount[p] == 0) c->free_pages.push_back(p);
-    r.pages = c->ev_pages[i];
+    r.pages.swap(c->ev_pages[i]);
     r.L = r.H = e.keep;
     int32_t* row = c->h_page_table + size_t(e.slot) * c->cfg.max_pages_per_request;
     std::fill(row, row + c->cfg.max_pages_per_request, -1);
@@ -1354,6 +1359,8 @@ oscar_status oscar_evict_commit(oscar_cache* c, void* stream) {
   st = upload_rows(c, u, changed, static_cast<cudaStream_t>(stream));
   if (st) return st;
   return end_upload(c, u, static_cast<cudaStream_t>(stream));
+} catch (const std::bad_alloc&) {
+  return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed");
 }
 
 oscar_status oscar_evict_cancel(oscar_cache* c) {
