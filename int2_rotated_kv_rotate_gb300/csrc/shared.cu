@@ -52,6 +52,9 @@ static_assert(kBlocks == 2, "warps 4-7 and 8-11");
 
 struct Control {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  // Completion n is item n of those in which the block has a page.  (A split item of one page
+  // leaves block 1 none.  Arriving for it all the same, block 1 would run ahead over such items:
+  // nothing there waits for the warp of S, which waits for each of them in order.)
   uint64_t q_full[kBlocks];
   // Completion n of each is page n of the block: S is written, S is read, P is written, P is
   // read and O holds the pages up to n.  Whoever waits for one of them waits for every page in
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
       ok = wait(ctl->q_full[0], q0++);
-      if (ok && w.blocks > 1) ok = wait(ctl->q_full[1], q1++);
+      if (ok && w.blocks > 1 && w.pages_of(1) > 0) ok = wait(ctl->q_full[1], q1++);
       for (int i = 0; ok && i < w.pages; ++i) {
         const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
         for (int b = b0; ok && b < b1; ++b) {
@@ -345,6 +348,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
       if (b >= w.blocks) continue;
+      const int pages = w.pages_of(b);
+      // the partial slot of row m's member
+      auto slot_of = [&](int m) {
+        const DecodeReq& dr = reqs[order[w.it.lo + m / G]];
+        return partials + (size_t(dr.first_item) + size_t(w.it.kvh) * dr.items_per_head + w.it.seg + (w.it.split ? b : 0)) *
+                              size_t(G) * (8 + 4 * kHeadDim);
+      };
+      if (pages == 0) {  // nothing attended: the merge reads no more than this of the slot
+        const int m = w.row0(b) + r;
+        if (m < w.rows) reinterpret_cast<float2*>(slot_of(m))[m % G] = make_float2(-INFINITY, 0.f);
+        continue;
+      }
       // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
       {
         // lane: the member of its row; then all loads before the first store
@@ -368,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&ctl->q_full[b]));
       float m_ref = -INFINITY, l = 0.f;
       const bool idle = w.row0(b) + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
-      const int pages = w.pages_of(b);
       for (int i = 0; i < pages; ++i, ++n) {
         ok = wait(ctl->s_full[b], n);
         if (!ok) break;
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the rows' partials
-      if (pages > 0) ok = wait(ctl->o_done[b], n - 1);
+      ok = wait(ctl->o_done[b], n - 1);
       if (!ok) break;
       tmem::fence_after();
       const int m = w.row0(b) + r;
@@ -455,8 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* slot = partials;
       const int h = m % G;
       if (mine) {
-        const DecodeReq& dr = reqs[order[w.it.lo + m / G]];
-        slot += (size_t(dr.first_item) + size_t(w.it.kvh) * dr.items_per_head + w.it.seg + (w.it.split ? b : 0)) * size_t(G) * (8 + 4 * kHeadDim);
+        slot = slot_of(m);
         reinterpret_cast<float2*>(slot)[h] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
       }
       float4* dst = reinterpret_cast<float4*>(slot + G * 8) + h * (kHeadDim / 4);
