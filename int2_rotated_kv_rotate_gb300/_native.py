@@ -7,6 +7,7 @@ missing the import of this module's functions fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -159,6 +160,16 @@ def _stream(stream) -> int | None:
         # (the raw handle: a Stream object a call costs 4 us of the host's time)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def on_stream(stream):
+    """Context in which torch works on `stream` (None: the current one).  What a call makes for
+    its launch is made there: the allocator hands blocks out again in one stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _ints(values):

@@ -61,10 +61,18 @@ class RotaryEmbedding:
         if like is not None and (shape != like.shape or x.dtype != like.dtype):
             raise ValueError(f"{name} must have the shape and dtype of its input")
 
+    @staticmethod
+    def _new(x, stream):
+        if stream is None:
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        with N.on_stream(stream):  # in the launch's order
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
     def apply(self, positions, q, k=None, *, q_out=None, k_out=None, transpose: bool = False, stream=None):
         """(q', k') of rows at `positions` (int32 or int64 [rows], any order): q [rows, H_q,
         head_dim] and optionally k [rows, H_kv, head_dim], any row and head strides.  Outputs
-        are new contiguous tensors unless given; q_out = q (k_out = k) works in place.
+        are new contiguous tensors unless given, made on the stream of the launch; q_out = q
+        (k_out = k) works in place.
         transpose=True applies the transposed map: gradients of q', k' to those of q, k."""
         if (positions.dim() != 1 or positions.dtype not in (torch.int32, torch.int64)
                 or positions.device != self.device or (positions.shape[0] > 1 and positions.stride(0) != 1)):
@@ -72,7 +80,7 @@ class RotaryEmbedding:
         rows = positions.shape[0]
         self._check("q", q, rows)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = self._new(q, stream)
         elif q_out is not q:
             self._check("q_out", q_out, rows, q)
         pairs = [(q, q_out)]
@@ -81,7 +89,7 @@ class RotaryEmbedding:
             if k.dtype != q.dtype:
                 raise ValueError("q and k must have one dtype")
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+                k_out = self._new(k, stream)
             elif k_out is not k:
                 self._check("k_out", k_out, rows, k)
             pairs.append((k, k_out))

@@ -1,0 +1,48 @@
+"""What the operators' calls make themselves is made on the stream of their launch: the caching
+allocator hands a block out again in the order of the stream it belongs to."""
+import pytest
+import torch
+
+from int2_rotated_kv_rotate_gb300 import RotaryEmbedding
+
+pytestmark = pytest.mark.gpu
+
+
+def pool_stream(t):
+    """The stream whose pool the tensor's memory belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the caching allocator's")
+
+
+def keep_busy():
+    x = torch.randn(4096, 4096, device="cuda")
+    for _ in range(40):
+        x = x @ x * 1e-3
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_rotary_outputs_on_another_stream(handle):
+    """A block that pending work of the current stream still reads is not the output's."""
+    rot = RotaryEmbedding(base=1e6)
+    q = torch.randn(2048, 16, 128, device="cuda").bfloat16()
+    k = torch.randn(2048, 4, 128, device="cuda").bfloat16()
+    positions = torch.arange(2048, device="cuda")
+    want = rot.apply(positions, q, k)
+    side = torch.cuda.Stream()
+    keep_busy()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    read = torch.zeros_like(q)  # (q_out's size: the block that its allocation would get)
+    kept = torch.empty_like(q)
+    torch.cuda.synchronize()
+    keep_busy()
+    kept.copy_(read)
+    del read
+    got = rot.apply(positions, q, k, stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    torch.cuda.synchronize()
+    assert bool((kept == 0).all())
+    assert pool_stream(got[0]) == pool_stream(got[1]) == side.cuda_stream
