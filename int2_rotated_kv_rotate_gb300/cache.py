@@ -5,8 +5,6 @@ of the C ABI (see include/oscar.h for semantics and layouts).
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _native as N
@@ -110,7 +108,8 @@ class KVCache:
             # sized for every plan of the cache, once: launches captured into a graph keep
             # this pointer across later plans
             full = N.oscar_decode_workspace_max_bytes(self.handle)
-            self.workspace = torch.empty(max(need, full, 256), dtype=torch.uint8, device=self.device)
+            with N.on_stream(stream):
+                self.workspace = torch.empty(max(need, full, 256), dtype=torch.uint8, device=self.device)
         return need
 
     def plan_info(self):
@@ -120,12 +119,13 @@ class KVCache:
         """(work items, pages) that the plan attends once for several requests."""
         return N.oscar_plan_shared_info(self.handle)
 
-    def _check_decode(self, q, out, out_f32):
+    def _check_decode(self, q, out, out_f32, stream):
         shape = (self._n_plan, self.cfg.n_q_heads, self.cfg.head_dim)
         if tuple(q.shape) != shape or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != self.mem.device:
             raise ValueError(f"q must be contiguous bf16 {shape} on {self.mem.device}")
         if out is None:
-            out = torch.empty_like(q)
+            with N.on_stream(stream):
+                out = torch.empty_like(q)
         if tuple(out.shape) != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 like q")
         if out_f32 is not None and (tuple(out_f32.shape) != shape or out_f32.dtype != torch.float32
@@ -134,7 +134,7 @@ class KVCache:
         return out
 
     def decode(self, layer: int, q, out=None, out_f32=None, stream=None):
-        out = self._check_decode(q, out, out_f32)
+        out = self._check_decode(q, out, out_f32, stream)
         if self.is_int2:
             N.oscar_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
         else:
@@ -145,13 +145,6 @@ class KVCache:
     def new_weights(self) -> torch.Tensor:
         """A layer's accumulated attention weights, zeros: fp32 [request slots, H_kv, weights_stride]."""
         return torch.zeros(self._weights_shape(), device=self.device)
-
-    @staticmethod
-    def _on(stream):
-        """Context in which torch works on `stream` (None: the current one)."""
-        if stream is None:
-            return contextlib.nullcontext()
-        return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
     def _weights_shape(self):
         if not self.weights_stride:
@@ -170,10 +163,11 @@ class KVCache:
         weights_out = weights if weights_out is None else weights_out
         self._check_weights("weights", weights)
         self._check_weights("weights_out", weights_out)
-        out = self._check_decode(q, out, out_f32)
+        out = self._check_decode(q, out, out_f32, stream)
         if self.weights_workspace is None:  # sized for every plan, once: captured launches keep this pointer
-            self.weights_workspace = torch.empty(N.oscar_decode_weights_workspace_max_bytes(self.handle),
-                                                 dtype=torch.uint8, device=self.device)
+            with N.on_stream(stream):
+                self.weights_workspace = torch.empty(N.oscar_decode_weights_workspace_max_bytes(self.handle),
+                                                     dtype=torch.uint8, device=self.device)
         N.oscar_bf16_decode_weights(self.handle, layer, q, out, weights, weights_out, self.weights_workspace, out_f32,
                                     stream)
         return out, weights_out
@@ -190,7 +184,7 @@ class KVCache:
         them when this call makes the tensor).  Rows of other slots stay as they are (those of a
         weights_out that this call makes: as in weights)."""
         self._check_weights("weights", weights)
-        with self._on(stream):  # what this call makes is made in the launch's order
+        with N.on_stream(stream):  # what this call makes is made in the launch's order
             if weights_out is None:
                 weights_out = weights.clone()
             if kept is None:
@@ -215,7 +209,7 @@ class KVCache:
         """quantize_append then decode of `layer` in one launch (INT2 format; plan made
         during the reservation over every reserved slot)."""
         self._check_tokens(k_new, v_new)
-        out = self._check_decode(q, out, out_f32)
+        out = self._check_decode(q, out, out_f32, stream)
         N.oscar_append_decode_attention(self.handle, layer, k_new, v_new, q, out, self.workspace, out_f32, stream)
         return out
 

@@ -3,7 +3,7 @@ allocator hands a block out again in the order of the stream it belongs to."""
 import pytest
 import torch
 
-from int2_rotated_kv_rotate_gb300 import RotaryEmbedding
+from int2_rotated_kv_rotate_gb300 import OSCAR_FORMAT_BF16, KVCache, RotaryEmbedding
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,30 @@ def test_rotary_outputs_on_another_stream(handle):
     torch.cuda.synchronize()
     assert bool((kept == 0).all())
     assert pool_stream(got[0]) == pool_stream(got[1]) == side.cuda_stream
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("call", ["decode", "decode_weights"])
+def test_decode_outputs_and_workspaces_on_another_stream(call, handle):
+    cache = KVCache(fmt=OSCAR_FORMAT_BF16, n_q_heads=4, n_kv_heads=1, n_layers=1, max_requests=2, max_pages=64,
+                    max_pages_per_request=32)
+    slots = [cache.alloc(), cache.alloc()]
+    cache.reserve(slots, [100, 1500])
+    cache.append(0, torch.randn(1600, 1, 128, device="cuda").bfloat16(), torch.randn(1600, 1, 128, device="cuda").bfloat16())
+    cache.commit()
+    q = torch.randn(2, 4, 128, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    w = cache.new_weights()
+    torch.cuda.synchronize()
+    cache.plan(slots, stream=stream)
+    if call == "decode":
+        out = cache.decode(0, q, stream=stream)
+    else:
+        out, _ = cache.decode_weights(0, q, w, stream=stream)
+        assert pool_stream(cache.weights_workspace) == side.cuda_stream
+    assert pool_stream(out) == pool_stream(cache.workspace) == side.cuda_stream
+    side.synchronize()
+    cache.plan(slots)
+    assert torch.equal(out, cache.decode(0, q))
+    assert pool_stream(cache.decode(0, q)) == torch.cuda.current_stream().cuda_stream
