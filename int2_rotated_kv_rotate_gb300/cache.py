@@ -126,10 +126,11 @@ class KVCache:
         if out is None:
             with N.on_stream(stream):
                 out = torch.empty_like(q)
-        if tuple(out.shape) != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        if (tuple(out.shape) != shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
+                or out.device != self.mem.device):
             raise ValueError("out must be contiguous bf16 like q")
         if out_f32 is not None and (tuple(out_f32.shape) != shape or out_f32.dtype != torch.float32
-                                    or not out_f32.is_contiguous()):
+                                    or not out_f32.is_contiguous() or out_f32.device != self.mem.device):
             raise ValueError("out_f32 must be contiguous fp32 like q")
         return out
 

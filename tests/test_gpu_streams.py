@@ -73,3 +73,19 @@ def test_decode_outputs_and_workspaces_on_another_stream(call, handle):
     cache.plan(slots)
     assert torch.equal(out, cache.decode(0, q))
     assert pool_stream(cache.decode(0, q)) == torch.cuda.current_stream().cuda_stream
+
+
+def test_outputs_on_another_device_are_refused():
+    cache = KVCache(fmt=OSCAR_FORMAT_BF16, n_q_heads=4, n_kv_heads=1, n_layers=1, max_requests=1, max_pages=2,
+                    max_pages_per_request=2)
+    slot = cache.alloc()
+    cache.reserve([slot], [3])
+    cache.append(0, *(torch.zeros(3, 1, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    cache.commit()
+    cache.plan([slot])
+    q, host = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 4, 128)
+    for kw in (dict(out=host.bfloat16()), dict(out_f32=host)):
+        with pytest.raises(ValueError):
+            cache.decode_weights(0, q, cache.new_weights(), **kw)
+        with pytest.raises(ValueError):
+            cache.decode(0, q, **kw)
