@@ -218,14 +218,28 @@ class ServingLoop:
 
     def _future_pages(self) -> int:
         """Pages the running requests will still take before they finish."""
-        return sum(max(0, self._peak_pages(r) - max(self._need(r.length), r.shared // 64)) for r in self.running)
+        return sum(max(0, self._peak_pages(r, r.shared) - max(0, self._need(r.length) - r.shared // 64))
+                   for r in self.running)
 
-    def _peak_pages(self, r: Request) -> int:
-        """The most pages a request holds at once: with eviction, its own up to the step that
-        crosses the limit and the new ones it then moves to."""
-        if not self.evict_above or r.prompt + r.gen <= self.evict_above:
-            return self._need(r.prompt + r.gen)
-        return self._need(max(r.prompt, self.evict_above) + 1) + self._need(self.evict_to)
+    def _peak_pages(self, r: Request, shared: int) -> int:
+        """The most pages of its own a request will hold at once, with `shared` prefix tokens in its
+        holder's.  An eviction needs those up to the step that crosses the limit and the new ones;
+        what stays is all its own, also of a prefix that it shared before."""
+        left, length = r.prompt + r.gen - r.position, r.length
+        if r.position < r.prompt:  # not prefilled yet
+            left, length = r.gen, r.prompt
+        evicted = r.position > r.length
+        if not self.evict_above:
+            return self._need(length + left) - shared // 64
+        peak = 0
+        if not evicted:
+            at = max(length, self.evict_above) + 1  # where the first eviction comes, if the request gets so far
+            if length + left <= at:
+                return self._need(length + left) - shared // 64
+            peak = self._need(at) - shared // 64 + self._need(self.evict_to)
+            length, left = self.evict_to, length + left - at
+        at = self.evict_above + 1
+        return max(peak, self._need(length + left) if length + left <= at else self._need(at) + self._need(self.evict_to))
 
     def _admit(self, waiting) -> list:
         admitted = []
@@ -240,7 +254,7 @@ class ServingLoop:
             if sh and self._holder(r.group) is None:
                 sh = 0
             free_pages, free_slots = self.cache.stats()
-            own = self._peak_pages(r) - sh // 64
+            own = self._peak_pages(r, sh)
             if free_slots == 0 or free_pages - self._future_pages() < own:
                 break
             waiting.pop(0)
