@@ -60,7 +60,7 @@ constexpr int kSharedItemPages = 16;  // an item's fixed time in the shared laun
 // 11.5 us, 4 on 32 (25 MB) 13.1 / 13.4, 2 on 128 (34 MB) 19.8 / 17.7, 4 on 64 (50 MB) 14.9 /
 // 18.6, 32 on 8 (65 MB) 21.5 / 20.6, 8 on 64 (117 MB) 20.6 / 29.2, 32 on 128 (1 GB) 29.5 / 134.
 constexpr long long kSharedPaysBytes = 32LL << 20;
-constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages stays with its requests' private items
+constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages is none by itself: its members attend them, or their own runs do
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
 bool config_ok(const oscar_config* c, std::string* why) {
@@ -344,25 +344,26 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
     const Group g = todo.back();
     todo.pop_back();
     if (g.hi - g.lo < 2) continue;
-    int end = g.begin, parent = g.parent;
+    int end = g.begin, parent = g.parent, begin = g.begin;
     for (int first; (first = page(out.order[g.lo], end)) >= 0; ++end) {
       bool same = true;
       for (int k = g.lo + 1; same && k < g.hi; ++k) same = page(out.order[k], end) == first;
       if (!same) break;
     }
-    if (end > g.begin) {
-      if (!always && (end - g.begin) * (long long)(g.hi - g.lo - 1) < kSharedMinSaved) continue;
+    if (end > g.begin && (always || (end - g.begin) * (long long)(g.hi - g.lo - 1) >= kSharedMinSaved)) {
       runs.push_back({g.lo, g.hi, g.begin, end, g.parent});
       parent = int(runs.size()) - 1;
+      begin = end;
       for (int k = g.lo; k < g.hi; ++k) out.first_private[out.order[k]] = end;
     }
+    // (a run too short to pay by itself goes with those of its members that share on)
     std::stable_sort(out.order.begin() + g.lo, out.order.begin() + g.hi,
                      [&](int a, int b) { return page(a, end) < page(b, end); });
     for (int lo = g.lo; lo < g.hi;) {
       const int p = page(out.order[lo], end);
       int hi = lo + 1;
       while (hi < g.hi && page(out.order[hi], end) == p) ++hi;
-      if (p >= 0 && hi - lo > 1) todo.push_back({lo, hi, end, parent});
+      if (p >= 0 && hi - lo > 1) todo.push_back({lo, hi, begin, parent});
       lo = hi;
     }
   }

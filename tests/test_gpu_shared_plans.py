@@ -51,3 +51,18 @@ def test_items_of_one_page_between_longer_ones(seed):
     b.check([slots[i] for i in order], seed=seed, label="mixed")
     assert b.cache.shared_info()[0] > 2 * 152
     same_again(b, len(slots))
+
+
+@pytest.mark.parametrize("common", [1, 2])
+def test_long_runs_under_a_short_one(common):
+    """Two pairs of requests on 512 pages of their own behind one or two common pages, which by
+    themselves would save too little: the pairs' pages are attended once for each pair."""
+    b = Batch(8, 4, 4, 2 * 512 + common + 8, 520)
+    first = b.new(64 * common)
+    other = b.new(0, first, common)
+    b.append(first, 64 * 512)
+    b.append(other, 64 * 512)
+    slots = [first, other, b.new(7, first, 512 + common), b.new(70, other, 512 + common)]
+    _, launches = b.check(slots, flags=OSCAR_PLAN_SHARED_PREFIX, label="pairs")
+    items, pages = b.cache.shared_info()
+    assert launches == 2 and items > 0 and 2 * 512 <= pages <= 2 * (512 + common)
