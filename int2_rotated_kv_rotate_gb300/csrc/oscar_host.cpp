@@ -54,12 +54,19 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 constexpr int kAppendChunk = 16;     // tokens (or ring slots) per append work item
 constexpr int kMaxAppendTokenItems = 65536;
 constexpr int kSharedItemPages = 16;  // an item's fixed time in the shared launch, in pages
-// A plan uses the shared launch where sharing saves that many bytes of reads: below, the
-// launch and the longer merges cost more than the reads, which L2 largely serves.  Measured
-// with / without it, 32 query heads on 8 kv-heads: 8 requests on 8 pages (15 MB saved) 11.8 /
-// 11.5 us, 4 on 32 (25 MB) 13.1 / 13.4, 2 on 128 (34 MB) 19.8 / 17.7, 4 on 64 (50 MB) 14.9 /
-// 18.6, 32 on 8 (65 MB) 21.5 / 20.6, 8 on 64 (117 MB) 20.6 / 29.2, 32 on 128 (1 GB) 29.5 / 134.
-constexpr long long kSharedPaysBytes = 32LL << 20;
+// A plan uses the shared launch where the reads that it saves take longer than what it adds, in
+// bytes read: itself (8 MB), a merge's turns over the shared slots of a head (1 MB each), the
+// rows of an item (40 MB for a block of 128), and the private tokens that wait for the SMs it
+// holds (2.5 times their bytes, up to 30 MB of them).  Fitted to 634 plans of 6 to 260 MB saved,
+// 4 to 64 query heads on 1 to 8 kv-heads, 2 to 128 requests, tails of 1 to 2000 tokens.  On 240
+// others: 1.2 % over the better of the two on average, 23 over it by more than 5 % (4.2 % and 59
+// with the saved bytes alone, from 32 MB on).
+// With / without it, 32 query heads on 8 kv-heads, tails of 40 tokens: 8 requests on 8 pages
+// (15 MB saved) 11.2 / 10.5 us, 4 on 32 (25 MB) 12.9 / 12.3, 2 on 128 (34 MB) 21.1 / 17.3, 4 on
+// 64 (50 MB) 14.9 / 17.5, 32 on 8 (65 MB) 22.0 / 19.5, 8 on 64 (117 MB) 20.5 / 27.8, 32 on 32
+// (260 MB) 25.3 / 54.0; tails of 2000 tokens, 5 on 96 (101 MB) 31.4 / 27.3.
+constexpr double kSharedLaunchBytes = 8e6, kSharedSlotBytes = 1e6, kSharedRowBytes = 40e6 / 128;
+constexpr double kSharedPrivateBytes = 30e6, kSharedPrivateWeight = 2.5;
 constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages is none by itself: its members attend them, or their own runs do
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
@@ -367,19 +374,13 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
       lo = hi;
     }
   }
-  long long saved = 0;  // pages
-  for (const Run& r : runs) saved += (long long)(r.end - r.begin) * (r.hi - r.lo - 1);
-  if (!always && saved * Hkv * (2LL * kPage * kHeadDim * 2) < kSharedPaysBytes) {
-    out.first_private.assign(n, 0);
-    return out;
-  }
   // Pages of an item: the CTAs, one an SM, take the items in turn, so the launch lasts as
   // long as its rounds of items, each about kSharedItemPages pages' time longer than its
   // pages (the queries, the pipeline's fill, the partials); and every partial slot of a head
   // is merged, an eighth of a page's time each.  The row blocks of a run's pages are items of
   // their own.
   const int per_item = kSharedRows / G;  // members of an item at most
-  long long best = -1;
+  long long best = -1, best_items = 0, best_slots = 0;
   int chunk = 0, longest = 0;
   for (const Run& r : runs) longest = std::max(longest, r.end - r.begin);
   for (int parts = 1; parts <= std::min(longest, 64); ++parts) {
@@ -395,10 +396,29 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
     const long long cost = 8 * ((items + c->n_sm - 1) / c->n_sm) * (ch + kSharedItemPages) + 2 * parts;
     if (best < 0 || cost < best) {
       best = cost;
+      best_items = items;
+      best_slots = n_slots;
       chunk = ch;
     }
   }
-  if (chunk == 0) {  // nothing shared, or no room for the runs' partials
+  bool pays = chunk > 0;  // else nothing shared, or no room for the runs' partials
+  if (pays && !always) {
+    long long saved = 0, rows = 0, sharers = 0, tokens = 0;  // pages; query rows of all items; requests; private tokens
+    for (const Run& r : runs) {
+      saved += (long long)(r.end - r.begin) * (r.hi - r.lo - 1);
+      rows += (long long)Hkv * ceil_div(r.end - r.begin, chunk) * (r.hi - r.lo) * G;
+    }
+    for (int i = 0; i < n; ++i) {
+      sharers += out.first_private[i] > 0;
+      tokens += Ls[i] - kPage * out.first_private[i];
+    }
+    const double token_bytes = double(Hkv) * (2 * kHeadDim * 2);
+    pays = double(saved) * kPage * token_bytes >=
+           kSharedLaunchBytes + kSharedSlotBytes * double(best_slots) / double(Hkv * sharers) +
+               kSharedRowBytes * std::min(double(rows) / double(best_items), kSharedRows / 2.0) +
+               kSharedPrivateWeight * std::min(double(tokens) * token_bytes, kSharedPrivateBytes);
+  }
+  if (!pays) {
     out.first_private.assign(n, 0);
     return out;
   }

@@ -66,3 +66,20 @@ def test_long_runs_under_a_short_one(common):
     _, launches = b.check(slots, flags=OSCAR_PLAN_SHARED_PREFIX, label="pairs")
     items, pages = b.cache.shared_info()
     assert launches == 2 and items > 0 and 2 * 512 <= pages <= 2 * (512 + common)
+
+
+@pytest.mark.parametrize("members,pages,tail,shares", [
+    (8, 8, 40, False), (4, 32, 40, False), (2, 128, 40, False), (4, 64, 40, True), (32, 8, 40, False), (8, 64, 40, True),
+    (32, 32, 40, True), (5, 96, 2000, False), (16, 4, 500, False), (16, 200, 2000, True)])
+def test_plans_share_where_it_was_measured_to_pay(members, pages, tail, shares):
+    b = Batch(8, 4, members, pages + members * (2 + tail // 64), pages + 2 + tail // 64)
+    first = b.cache.alloc()
+    b.cache.reserve([first], [64 * pages])
+    b.cache.commit()
+    slots = [first] + [b.cache.alloc() for _ in range(members - 1)]
+    for s in slots[1:]:
+        b.cache.share_prefix(s, first, 64 * pages)
+    b.cache.reserve(slots, [tail] * members)
+    b.cache.commit()
+    b.cache.plan(slots, flags=OSCAR_PLAN_SHARED_PREFIX)
+    assert (b.cache.shared_info()[0] > 0) == shares
