@@ -16,6 +16,32 @@ _DTYPES = {torch.bfloat16: N.OSCAR_DTYPE_BF16, torch.float16: N.OSCAR_DTYPE_F16,
 _SCALINGS = {"linear": N.OSCAR_ROPE_LINEAR, "bands": N.OSCAR_ROPE_BANDS, "yarn": N.OSCAR_ROPE_YARN}
 
 
+_count_as_written = torch.autograd.graph.increment_version  # (a graph that saved the tensor is told)
+
+
+class _Apply(torch.autograd.Function):
+    """RotaryEmbedding.apply on inputs that need gradients: the transposed map on theirs."""
+
+    @staticmethod
+    def forward(ctx, rotary, transpose, positions, *tensors):
+        ctx.rotary, ctx.transpose = rotary, transpose
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        return rotary.apply(positions, *tensors, transpose=transpose)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        out = [None] * len(grads)
+        live = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[3 + i]]
+        if live:
+            (positions,) = ctx.saved_tensors
+            rows = [grads[i] if grads[i].stride(-1) == 1 else grads[i].contiguous() for i in live]
+            turned = ctx.rotary.apply(positions, *rows, transpose=not ctx.transpose)
+            for i, g in zip(live, turned if len(live) > 1 else (turned,)):
+                out[i] = g
+        return (None, None, None, *out)
+
+
 class RotaryEmbedding:
     """Rotary positions of one configuration.
 
@@ -73,16 +99,27 @@ class RotaryEmbedding:
         head_dim] and optionally k [rows, H_kv, head_dim], any row and head strides.  Outputs
         are new contiguous tensors unless given, made on the stream of the launch; q_out = q
         (k_out = k) works in place.
-        transpose=True applies the transposed map: gradients of q', k' to those of q, k."""
+        transpose=True applies the transposed map: gradients of q', k' to those of q, k.  Inputs
+        that require gradients get them through autograd, on new outputs only."""
         if (positions.dim() != 1 or positions.dtype not in (torch.int32, torch.int64)
                 or positions.device != self.device or (positions.shape[0] > 1 and positions.stride(0) != 1)):
             raise ValueError(f"positions must be contiguous int32 or int64 [rows] on {self.device}")
         rows = positions.shape[0]
+        if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)
+                                        or (q_out is not None and q_out.requires_grad)
+                                        or (k_out is not None and k_out.requires_grad)):
+            if q_out is not None or k_out is not None:
+                raise ValueError("tensors that require grad are turned into new outputs only")
+            with N.on_stream(stream):
+                return _Apply.apply(self, transpose, positions, q) if k is None else _Apply.apply(self, transpose, positions, q, k)
         self._check("q", q, rows)
+        written = []
         if q_out is None:
             q_out = self._new(q, stream)
-        elif q_out is not q:
-            self._check("q_out", q_out, rows, q)
+        else:
+            if q_out is not q:
+                self._check("q_out", q_out, rows, q)
+            written.append(q_out)
         pairs = [(q, q_out)]
         if k is not None:
             self._check("k", k, rows)
@@ -90,8 +127,10 @@ class RotaryEmbedding:
                 raise ValueError("q and k must have one dtype")
             if k_out is None:
                 k_out = self._new(k, stream)
-            elif k_out is not k:
-                self._check("k_out", k_out, rows, k)
+            else:
+                if k_out is not k:
+                    self._check("k_out", k_out, rows, k)
+                written.append(k_out)
             pairs.append((k, k_out))
         elif k_out is not None:
             raise ValueError("k_out without k")
@@ -104,4 +143,6 @@ class RotaryEmbedding:
         else:
             with torch.cuda.device(self.device):
                 N.oscar_rope(*args)
+        if written:
+            _count_as_written(written)
         return (q_out, k_out) if k is not None else q_out
