@@ -129,9 +129,10 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
       }
   };
   const bool copies = mine && !turns && static_cast<const void*>(in) != static_cast<const void*>(out);
+  const bool works = copies || (mine && turns);  // (nothing to read past rotary_dim in place)
   pdl_wait();
   pdl_trigger();
-  if (mine && (kVec || turns)) fetch(0);  // in flight while the table is made
+  if (works && (kVec || turns)) fetch(0);  // in flight while the table is made
   for (int e = threadIdx.x; e < n_rows * pairs; e += blockDim.x) {
     const int r = e / pairs, i = e - r * pairs;
     const long long pos = p.positions64 ? reinterpret_cast<const long long*>(p.positions)[row0 + r]
@@ -141,10 +142,9 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
         make_float2(cs.x * p.magnitude, (p.transpose ? -cs.y : cs.y) * p.magnitude);
   }
   __syncthreads();
-  if (!mine) return;
+  if (!works) return;
   if constexpr (!kVec) {
     if (!turns) {  // single channels and 16-byte vectors past rotary_dim
-      if (!copies) return;
       for (int r = 0; r < n_rows; ++r, in += x.in_row, out += x.out_row) {
         if (single) *out = *in;
         else store<T, kWide, true>(out, load<T, kWide, true>(in));
