@@ -170,9 +170,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Bounded wait of a whole warp for completions of one or two barriers (index: parity of the
   // completion).  Lane 0 polls the first, lane 1 the second: each polling lane costs the
-  // barrier's bank a turn, and two waits one after the other twice a wait's 200 cycles.  Once
-  // one runs out, every role leaves its loop.
-  auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> bool {
+  // barrier's bank a turn, and two waits one after the other twice a wait's 200 cycles.  The
+  // __syncwarp orders what they saw before what the others do next; a vote would not.  Each lane
+  // has its own poll's result: the roles vote once a page, where the warp meets anyway, so after
+  // a wait that ran out MMAs and stores of that page still go out, on memory of this CTA, and
+  // every role then leaves its loop.
+  auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> int {
     int done = 1;
     if (lane < 2) {
       const uint32_t a = lane ? smem_u32(&bar1) : smem_u32(&bar0), par = (lane ? index1 : index0) & 1u;
@@ -186,9 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         flag(kp, OSCAR_FLAG_TIMEOUT);
       }
     }
-    return __all_sync(0xffffffffu, done);
+    __syncwarp();
+    return done;
   };
-  auto wait = [&](uint64_t& bar, uint32_t index) -> bool {
+  auto wait = [&](uint64_t& bar, uint32_t index) -> int {
     int done = 1;
     if (lane == 0) {
       const uint32_t a = smem_u32(&bar);
@@ -202,8 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         flag(kp, OSCAR_FLAG_TIMEOUT);
       }
     }
-    return __all_sync(0xffffffffu, done);
+    __syncwarp();
+    return done;
   };
+
+  auto all = [](int done) -> bool { return __all_sync(0xffffffffu, done); };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- pages
@@ -227,29 +234,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int y = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
         const uint32_t dst = sst + st * kPageKv;
-        if (cnt >= kStages && !(ok = wait(ctl->k_empty[st], cnt / kStages - 1))) break;
-        if (elect_one()) {
+        int done = cnt >= kStages ? wait(ctl->k_empty[st], cnt / kStages - 1) : 1;
+        if (lane == 0 && done) {  // (lane 0 polled: no copy into a stage that was not left)
           const uint32_t bar = smem_u32(&ctl->k_full[st]);
           mbar_expect_tx(bar, kPageKv / 2);
           tma_load(dst, &map, 0, y, bar);
           tma_load(dst + 8192, &map, 64, y, bar);
         }
-        __syncwarp();
+        if (!(ok = all(done))) break;
         nk = cnt + 1;
-        if (cnt >= kStages && !(ok = wait(ctl->v_empty[st], cnt / kStages - 1))) break;
-        if (elect_one()) {
+        done = cnt >= kStages ? wait(ctl->v_empty[st], cnt / kStages - 1) : 1;
+        if (lane == 0 && done) {
           const uint32_t bar = smem_u32(&ctl->v_full[st]);
           mbar_expect_tx(bar, kPageKv / 2);
           tma_load(dst + 16384, &map, 0, y + kPage, bar);
           tma_load(dst + 24576, &map, 64, y + kPage, bar);
         }
-        __syncwarp();
+        if (!(ok = all(done))) break;
         nv = cnt + 1;
       }
     }
     // the last arrivals on the stages' barriers come before the CTA leaves
     for (uint32_t k = cnt > kStages ? cnt - kStages : 0; ok && k < cnt; ++k)
-      ok = wait2(ctl->k_empty[k % kStages], k / kStages, ctl->v_empty[k % kStages], k / kStages);
+      ok = all(wait2(ctl->k_empty[k % kStages], k / kStages, ctl->v_empty[k % kStages], k / kStages));
     if (!ok) {  // copies still in flight land first, too
       for (uint32_t k = nk > kStages ? nk - kStages : 0; k < nk; ++k)
         mbar_wait(smem_u32(&ctl->k_full[k % kStages]), (k / kStages) & 1u);
@@ -265,15 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
       const Work w = load_work(ix);
-      ok = wait(ctl->q_full[0], q0++);
-      if (ok && w.blocks > 1 && w.pages_of(1) > 0) ok = wait(ctl->q_full[1], q1++);
+      ok = all(wait(ctl->q_full[0], q0++));
+      if (ok && w.blocks > 1 && w.pages_of(1) > 0) ok = all(wait(ctl->q_full[1], q1++));
       for (int i = 0; ok && i < w.pages; ++i) {
         const int b0 = w.it.split ? i & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
         for (int b = b0; ok && b < b1; ++b) {
           const uint32_t n = b ? n1++ : n0++;
-          if (b == b0) ok = n ? wait2(ctl->k_full[st], lap, ctl->s_empty[b], n - 1) : wait(ctl->k_full[st], lap);
-          else if (n) ok = wait(ctl->s_empty[b], n - 1);
-          if (!ok) break;
+          int done = 1;
+          if (b == b0) done = n ? wait2(ctl->k_full[st], lap, ctl->s_empty[b], n - 1) : wait(ctl->k_full[st], lap);
+          else if (n) done = wait(ctl->s_empty[b], n - 1);
           tmem::fence_after();
           if (elect_one()) {
             const uint32_t d = tm + b * kBlockCols;
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem::commit(smem_u32(&ctl->s_full[b]));
             if (b == b1 - 1) tmem::commit(smem_u32(&ctl->k_empty[st]));
           }
-          __syncwarp();
+          ok = all(done);
         }
         if (++st == kStages) {
           st = 0;
@@ -312,8 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = b0; ok && b < b1; ++b) {
           const uint32_t n = b ? n1++ : n0++;
           const bool first = (b ? l1++ : l0++) == 0;
-          ok = b == b0 ? wait2(ctl->v_full[st], lap, ctl->p_full[b], n) : wait(ctl->p_full[b], n);
-          if (!ok) break;
+          const int done = b == b0 ? wait2(ctl->v_full[st], lap, ctl->p_full[b], n) : wait(ctl->p_full[b], n);
           tmem::fence_after();
           if (elect_one()) {
             const uint32_t d = tm + b * kBlockCols + kColO, a = tm + b * kBlockCols + kColP;
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem::commit(smem_u32(&ctl->o_done[b]));
             if (b == b1 - 1) tmem::commit(smem_u32(&ctl->v_empty[st]));
           }
-          __syncwarp();
+          ok = all(done);
         }
         if (++st == kStages) {
           st = 0;
@@ -384,15 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       const bool idle = w.row0(b) + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
       for (int i = 0; i < pages; ++i, ++n) {
-        ok = wait(ctl->s_full[b], n);
-        if (!ok) break;
+        int done = wait(ctl->s_full[b], n);
         // P and O of the page before (the item's first page: of an earlier item, long done)
-        auto last_done = [&] { return i == 0 || wait(ctl->o_done[b], n - 1); };
+        auto last_done = [&] {
+          if (i > 0) done &= wait(ctl->o_done[b], n - 1);
+        };
         if (idle) {
           mbar_arrive(smem_u32(&ctl->s_empty[b]));
-          ok = last_done();
-          if (!ok) break;
+          last_done();
           mbar_arrive(smem_u32(&ctl->p_full[b]));
+          if (!(ok = all(done))) break;
           continue;
         }
         tmem::fence_after();
@@ -411,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 0) {
           m_ref = mx;
         } else if (__any_sync(0xffffffffu, raise)) {
-          ok = last_done();
-          if (!ok) break;
+          last_done();
           waited = true;
           tmem::fence_after();
           const float f = raise ? ex2(m_ref - mx) : 1.f;
@@ -449,8 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack2(l2, la, lb);
         l += la + lb;
         if (!waited) {
-          ok = last_done();
-          if (!ok) break;
+          last_done();
           tmem::fence_after();
         }
         tmem::st_x32(tl + kColP, hi);
@@ -458,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem::wait_st();
         tmem::fence_before();
         mbar_arrive(smem_u32(&ctl->p_full[b]));
+        if (!(ok = all(done))) break;
       }
       if (!ok) break;
       // ---- the rows' partials
-      ok = wait(ctl->o_done[b], n - 1);
-      if (!ok) break;
+      if (!(ok = all(wait(ctl->o_done[b], n - 1)))) break;
       tmem::fence_after();
       const int m = w.row0(b) + r;
       const bool mine = m < w.rows;
