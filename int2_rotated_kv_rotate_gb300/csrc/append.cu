@@ -387,8 +387,8 @@ int launch_append(const KernelParams& kp, int layer, const void* k_new, const vo
   dim3 grid(passes < per_head ? passes : per_head, kp.n_kv_heads, 2);
   const uint16_t* k = static_cast<const uint16_t*>(k_new);
   const uint16_t* v = static_cast<const uint16_t*>(v_new);
-  static bool attr = false;
-  if (!attr) {
+  static PerDevice attr;
+  const int ready = attr.get([] {
     int e = int(cudaFuncSetAttribute(append_kernel<32, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem));
     if (!e)
       e = int(cudaFuncSetAttribute(append_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem));
@@ -396,9 +396,9 @@ int launch_append(const KernelParams& kp, int layer, const void* k_new, const vo
       e = int(cudaFuncSetAttribute(append_kernel<32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmemCm));
     if (!e)
       e = int(cudaFuncSetAttribute(append_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmemCm));
-    if (e) return e;
-    attr = true;
-  }
+    return e ? -e : 1;
+  });
+  if (ready < 0) return -ready;
   const size_t smem = size_t(kp.v_cm ? kAppendSmemCm : kAppendSmem);
   int e;
   if (kp.v_cm)

@@ -191,18 +191,16 @@ constexpr int kBf16KernelSmem(int G, int nbuf) {
 
 template <int G, int NBUF, bool WEIGHTS = false>
 int resident_ctas(int n_sm) {
-  static int resident = 0;
-  if (resident == 0) {
+  static PerDevice resident;
+  return resident.get([=] {
     int e = int(cudaFuncSetAttribute(bf16_split_kernel<G, NBUF, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kBf16KernelSmem(G, NBUF)));
     int per_sm = 0;
     if (!e)
       e = int(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, bf16_split_kernel<G, NBUF, WEIGHTS>,
                                                             128, kBf16KernelSmem(G, NBUF)));
-    if (e) return -e;
-    resident = (per_sm > 0 ? per_sm : 1) * n_sm;
-  }
-  return resident;
+    return e ? -e : (per_sm > 0 ? per_sm : 1) * n_sm;
+  });
 }
 
 template <int G, int NBUF>

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "oscar_internal.h"
@@ -559,6 +560,22 @@ __device__ __forceinline__ bool wait_counter(const unsigned* ctr, unsigned expec
 // Generic-proxy writes made visible to this thread (e.g. by an acquire) are ordered before
 // its later async-proxy (bulk copy) reads of global memory.
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// What `make` gives (positive, or a negative error) for the current device, made at its first
+// call there: a kernel's attributes and occupancy belong to a device.
+struct PerDevice {
+  std::atomic<int> value[64] = {};
+  template <typename Make>
+  int get(Make make) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return -int(e);
+    if (dev >= 64) return make();
+    int v = value[dev].load(std::memory_order_acquire);
+    if (v == 0 && (v = make()) > 0) value[dev].store(v, std::memory_order_release);
+    return v;
+  }
+};
 
 // Launch with programmatic stream serialization (PDL) allowed.
 template <typename Kern, typename... Args>

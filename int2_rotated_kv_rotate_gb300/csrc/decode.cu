@@ -1457,8 +1457,8 @@ __global__ void __launch_bounds__(Shape<NW>::NTH, Cfg<G, GROUP, NW, CM>::kPerSM)
 template <int G, int GROUP, bool FUSED, int NW, bool CM>
 int resident_ctas_t(int n_sm) {
   using C = Cfg<G, GROUP, NW, CM>;
-  static int resident = 0;  // CTAs of split_kernel that fit on the GPU at once
-  if (resident == 0) {
+  static PerDevice resident;  // CTAs of split_kernel that fit on the GPU at once
+  return resident.get([=] {
     int e = int(cudaFuncSetAttribute(split_kernel<G, GROUP, FUSED, NW, CM>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
     if (!e)
@@ -1481,12 +1481,12 @@ int resident_ctas_t(int n_sm) {
       if (per_sm * C::kTmemCols > 512) per_sm = 512 / C::kTmemCols;
     }
     if (e) return -e;
-    resident = (per_sm > 0 ? per_sm : 1) * n_sm;
+    int n = (per_sm > 0 ? per_sm : 1) * n_sm;
     // One CTA per SM (16-warp shape): leave a few SMs to the preceding launch's last CTAs
     // (its final merges), so that no CTA of this launch waits for an SM to drain.
-    if (NW == 16 && resident > 4 * kSpareSMs) resident -= kSpareSMs;
-  }
-  return resident;
+    if (NW == 16 && n > 4 * kSpareSMs) n -= kSpareSMs;
+    return n;
+  });
 }
 
 // The decode and the fused append + decode kernels of a shape get one plan: the smaller

@@ -275,13 +275,13 @@ template <int kCluster>
 int launch_select(const KernelParams& kp, const float* weights, float* weights_out, int* kept, int n_req, int max_len,
                   int n_sm, void* stream) {
   constexpr int kTileBytes = kTile * 4, kMost = 10;  // of 8 KB: two CTAs an SM
-  static bool attr = false;
-  if (!attr) {
+  static PerDevice attr;
+  const int ready = attr.get([] {
     const int e = int(cudaFuncSetAttribute(evict_select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kMost * kTileBytes));
-    if (e) return e;
-    attr = true;
-  }
+    return e ? -e : 1;
+  });
+  if (ready < 0) return -ready;
   const int tiles = (max_len + kTile - 1) / kTile, per = (tiles + kCluster - 1) / kCluster;
   const int slice_tiles = per < kMost ? per : kMost;
   const int rows = n_req * kp.n_kv_heads, clusters = rows < 8 * n_sm ? rows : 8 * n_sm;

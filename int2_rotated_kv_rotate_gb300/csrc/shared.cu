@@ -524,12 +524,12 @@ int encode_page_map(const KernelParams& kp, void* map) {
 
 int launch_shared(const KernelParams& kp, int layer, const void* map, const void* q, uint8_t* partials, int n_sm,
                   void* stream, int* launches) {
-  static bool attr = false;
-  if (!attr) {
+  static PerDevice attr;
+  const int ready = attr.get([] {
     const int e = int(cudaFuncSetAttribute(shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
-    if (e) return e;
-    attr = true;
-  }
+    return e ? -e : 1;
+  });
+  if (ready < 0) return -ready;
   const int e = launch_ex(shared_kernel, dim3(n_sm), dim3(kThreads), size_t(kSmemBytes), stream, kp, layer,
                           *static_cast<const CUtensorMap*>(map), static_cast<const uint16_t*>(q), partials);
   if (!e) *launches += 1;
