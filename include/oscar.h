@@ -259,9 +259,10 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const vo
  * the kv-head's query heads of softmax(q K^T / sqrt(d))[t] for every token t < L of the
  * planned requests; weights_in NULL counts as zeros and may be weights_out (it must not
  * overlap it otherwise).  Other entries of weights_out stay as they are.  The workspace
- * (oscar_decode_weights_workspace_bytes for the current plan, _max_bytes for every plan)
- * also holds the scores, 4 bytes a query head and token of a row.  Two launches.  Not with
- * a plan of OSCAR_PLAN_SHARED_PREFIX (OSCAR_ERR_STATE). */
+ * (oscar_decode_weights_workspace_bytes for the current plan, _max_bytes for every plan, as a
+ * captured launch needs it) also holds the scores, 4 bytes a query head and token of the
+ * plan's requests.  Two launches.  Not with a plan of OSCAR_PLAN_SHARED_PREFIX
+ * (OSCAR_ERR_STATE). */
 int oscar_weights_stride(const oscar_cache* cache);
 size_t oscar_decode_weights_workspace_bytes(const oscar_cache* cache);
 size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* cache);

@@ -26,6 +26,9 @@ class KVCache:
         self.layout = N.oscar_cache_layout(self.handle)
         self.workspace = None
         self.weights_workspace = None
+        self._weights_full = N.oscar_decode_weights_workspace_max_bytes(self.handle)  # bytes of it for every plan
+        self._weights_need = 0  # and for the current one
+        self._weights_streams = []  # streams that launched on it, its own first
         self.weights_stride = N.oscar_weights_stride(self.handle)  # 0: no weights in this format
         self.fmt = fmt
         self.is_int2 = fmt in (N.OSCAR_FORMAT_INT2, N.OSCAR_FORMAT_INT2_CM)
@@ -110,6 +113,7 @@ class KVCache:
             full = N.oscar_decode_workspace_max_bytes(self.handle)
             with N.on_stream(stream):
                 self.workspace = torch.empty(max(need, full, 256), dtype=torch.uint8, device=self.device)
+        self._weights_need = N.oscar_decode_weights_workspace_bytes(self.handle)
         return need
 
     def plan_info(self):
@@ -157,6 +161,27 @@ class KVCache:
         if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.mem.device:
             raise ValueError(f"{name} must be contiguous {dtype} {shape} on {self.mem.device}")
 
+    def _score_space(self, stream):
+        """The weights' workspace: the plan's size and some to grow, or every plan's size from the
+        first captured launch on, since a graph keeps the pointer across later plans."""
+        ws = self.weights_workspace
+        full = self._weights_full
+        if ws is not None and ws.numel() >= full:
+            return ws
+        with N.on_stream(stream):
+            captured = torch.cuda.is_current_stream_capturing()
+            if ws is None or ws.numel() < (full if captured else self._weights_need):
+                for handle in self._weights_streams:  # launches of any of them may still use the old one
+                    ws.record_stream(torch.cuda.ExternalStream(handle))
+                scores = self._weights_need - full + 4 * self.cfg.max_requests * self.cfg.n_q_heads * self.weights_stride
+                size = full if captured else min(full, self._weights_need + scores // 4)
+                self.weights_workspace = ws = torch.empty(max(size, 256), dtype=torch.uint8, device=self.device)
+                self._weights_streams = []
+            handle = N._stream(None)
+        if handle not in self._weights_streams:
+            self._weights_streams.append(handle)
+        return ws
+
     def decode_weights(self, layer: int, q, weights, weights_out=None, out=None, out_f32=None, stream=None):
         """decode that also adds every attended token's softmax probability, summed over its
         kv-head's query heads, to `weights`: (out, weights_out).  In place without weights_out;
@@ -165,11 +190,7 @@ class KVCache:
         self._check_weights("weights", weights)
         self._check_weights("weights_out", weights_out)
         out = self._check_decode(q, out, out_f32, stream)
-        if self.weights_workspace is None:  # sized for every plan, once: captured launches keep this pointer
-            with N.on_stream(stream):
-                self.weights_workspace = torch.empty(N.oscar_decode_weights_workspace_max_bytes(self.handle),
-                                                     dtype=torch.uint8, device=self.device)
-        N.oscar_bf16_decode_weights(self.handle, layer, q, out, weights, weights_out, self.weights_workspace, out_f32,
+        N.oscar_bf16_decode_weights(self.handle, layer, q, out, weights, weights_out, self._score_space(stream), out_f32,
                                     stream)
         return out, weights_out
 

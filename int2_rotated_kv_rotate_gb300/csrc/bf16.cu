@@ -26,7 +26,7 @@ constexpr int kBf16PerSM = NBUF == 3 ? 2 : 3;  // (told to the compiler, which e
 template <int G, int NBUF>
 constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::kBytes;
 
-// WEIGHTS: the scores (log2 units) go to scores, fp32 [plan request][kv-head][stride][G], and
+// WEIGHTS: the scores (log2 units) go to scores, fp32 [kv-head][L][G] of each plan request, and
 // each head's (maximum, 1 / denominator) to ml, for bf16_weights_kernel.
 // after_shared: the preceding launch attends the plan's shared runs.  It waited for its own
 // predecessors before it let this one start, so q and the pages are final here, and only a
@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(128, kBf16PerSM<NBUF>) bf16_split_kernel(Kerne
     }
     for (int e = threadIdx.x; e < G * kHeadDim; e += 128) qs[(e / kHeadDim) * kQRow + e % kHeadDim] = bf16_f32(q[head0 * kHeadDim + e]);
     __syncthreads();
+    float* sc = WEIGHTS ? scores + (size_t(dr.score0) + size_t(it.kvh) * size_t(dr.L)) * G : nullptr;
     auto keep = [=](int h, int u, float s) {
-      if constexpr (WEIGHTS)
-        scores[((size_t(it.req) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride) + size_t(u)) * G + h] = s;
+      if constexpr (WEIGHTS) sc[size_t(u) * G + h] = s;
     };
     auto nothing = [] {};
     bf16_rows_mma<G, 4, NBUF, decltype(rowK), decltype(rowV), decltype(nothing), decltype(keep), true>(
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWeightsThreads) bf16_weights_kernel(KernelPar
     float2 head[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) head[h] = ml[size_t(it.req) * kp.n_q_heads + size_t(it.kvh) * G + h];
-    const float* sc = scores + (size_t(it.req) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride) * G;
+    const float* sc = scores + (size_t(dr.score0) + size_t(it.kvh) * size_t(dr.L)) * G;
     const size_t row = (size_t(dr.slot) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride);
     for (int p = t0 + int(blockIdx.y) * kPiece; p < t1; p += int(gridDim.y) * kPiece) {
       float4 s[4][G / 4];

@@ -209,6 +209,7 @@ struct oscar_cache {
   bool map_ready = false;
   alignas(64) unsigned char page_map[128];  // tensor map of the BF16 page pool
   int dec_n_req = 0, dec_items = 0, dec_bf16_items = 0, dec_max_pages = 0;
+  long long dec_tokens = 0;  // of all kv-heads
   DecodeWorkspace ws{};
   int device = 0;              // the device current at creation (the device of `base`)
   uint32_t counter_polls = 0;  // oscar_set_wait_limit (0 = kDefaultCounterPolls)
@@ -440,15 +441,15 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
   return out;
 }
 
-// Workspace of a decode with weights over n_req requests.  Only the total depends on the
-// plan: a captured launch keeps its offsets.
-WeightsWorkspace weights_workspace(const oscar_cache* c, int n_req) {
+// Workspace of a decode with weights over `tokens` tokens of all kv-heads.  Only the total
+// depends on the plan: a captured launch keeps its offsets.
+WeightsWorkspace weights_workspace(const oscar_cache* c, size_t tokens) {
   const size_t Hq = c->cfg.n_q_heads, G = Hq / c->cfg.n_kv_heads;
   WeightsWorkspace w;
   w.ml = 0;
   w.partials = align256(size_t(c->cfg.max_requests) * Hq * 8);
   w.scores = w.partials + align256(c->lay.max_decode_items * G * (8 + 4 * kHeadDim));
-  w.total = w.scores + size_t(n_req) * Hq * size_t(oscar_weights_stride(c)) * 4;
+  w.total = w.scores + tokens * G * 4;
   return w;
 }
 
@@ -986,6 +987,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   std::vector<DecodeReq> reqs(n_req);
   std::vector<DecodeItem> items;
   int n_bf16 = 0, max_pages = 0, n_slots = 0;
+  long long tokens = 0;  // of all kv-heads
   for (int i = 0; i < n_req; ++i) {
     DecodeReq& q = reqs[i];
     q.slot = slots[i];
@@ -1001,6 +1003,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       const int n_s = std::min(q.L, S);
       u_new = std::min(n_bf, Lpre[i] < n_s ? Lpre[i] : n_s + std::max(0, Lpre[i] - q.H));
     }
+    q.score0 = tokens;
+    tokens += (long long)Hkv * q.L;
     q.first_item = n_slots;
     q.n_shared = runs.n_segs[i];
     for (int h = 0; h < Hkv; ++h) {
@@ -1084,6 +1088,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   w.total = off;
   c->ws = w;
   c->dec_n_req = n_req;
+  c->dec_tokens = tokens;
   c->dec_items = int(items.size());
   c->dec_bf16_items = n_bf16;
   c->dec_max_pages = max_pages;
@@ -1209,11 +1214,12 @@ int oscar_weights_stride(const oscar_cache* c) {
 }
 
 size_t oscar_decode_weights_workspace_bytes(const oscar_cache* c) {
-  return c && c->planned && !is_int2(c) ? weights_workspace(c, c->dec_n_req).total : 0;
+  return c && c->planned && !is_int2(c) ? weights_workspace(c, size_t(c->dec_tokens)).total : 0;
 }
 
 size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* c) {
-  return c && !is_int2(c) ? weights_workspace(c, c->cfg.max_requests).total : 0;
+  if (!c || is_int2(c)) return 0;
+  return weights_workspace(c, size_t(c->cfg.max_requests) * c->cfg.n_kv_heads * size_t(oscar_weights_stride(c))).total;
 }
 
 oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q, void* out, const float* weights_in,
@@ -1235,7 +1241,7 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q,
   if (wi && wi != wo && wi < wo + w_bytes && wo < wi + w_bytes)
     return fail(OSCAR_ERR_INVALID_ARG, "weights_in and weights_out overlap");
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(OSCAR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const WeightsWorkspace w = weights_workspace(c, c->dec_n_req);
+  const WeightsWorkspace w = weights_workspace(c, size_t(c->dec_tokens));
   if (ws_bytes < w.total) return fail(OSCAR_ERR_INVALID_ARG, "workspace %zu < %zu bytes", ws_bytes, w.total);
   oscar_status st = check_device(c);
   if (st) return st;

@@ -45,6 +45,7 @@ struct DecodeReq {
   int first_item;    // items of this request, kv-head-major: first_item + kvh*items_per_head ..
   int items_per_head;
   int n_shared;      // of each head's partial slots, the first n_shared are the shared launch's
+  long long score0;  // decode with weights: tokens of all heads of the requests before this one
 };
 
 // One work item of the launch that attends shared runs (BF16 format): pages [begin, end) of
@@ -183,7 +184,7 @@ int launch_bf16_decode(const KernelParams& kp, int layer, const void* q, void* o
 struct WeightsWorkspace {
   size_t ml;        // float2 [plan request][H_q]: maximum (log2 units), 1 / denominator
   size_t partials;  // as DecodeWorkspace, room for every plan
-  size_t scores;    // fp32 [plan request][kv-head][weights_stride][G]
+  size_t scores;    // fp32 [kv-head][L][G] of each plan request, at its score0
   size_t total;
 };
 int launch_bf16_decode_weights(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32,
