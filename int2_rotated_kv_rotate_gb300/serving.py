@@ -14,7 +14,9 @@ Around the attention the loop can run what a model's serving step runs: rotary p
 the queries and the new keys (`rotary`); the BF16 cache's decode with shared prefixes attended
 once (`share_decode`); and, on the BF16 cache, eviction of the tokens with the least
 accumulated attention weight once a request holds more than `evict_above` of them, down to
-`evict_to`, so that a long request stays within a bounded number of pages.
+`evict_to`, so that a long request stays within a bounded number of pages (the weights that
+this keeps count against the budget: a row of the longest request for every slot and layer,
+so `max_requests` and `max_len` decide what they take).
 
 Scheduling: first come, first served.  A request is admitted when a slot is free and the
 free pages cover its final length on top of what the running requests will still need
@@ -103,20 +105,32 @@ def pages_needed(fmt: int, L: int, S: int, W: int) -> int:
     return -(-L // 64)
 
 
-def cache_for_budget(w: wl.Workload, fmt: int, budget_bytes: int, max_requests: int, max_len: int, device):
-    """The cache with the most pages whose device block fits the budget."""
+def eviction_bytes(w: wl.Workload, max_requests: int, pages: int, pages_per_request: int) -> int:
+    """Device bytes that a loop with eviction keeps beside a cache of so many pages: the layers'
+    weights, a layer's kept weights and positions, and the scores of the pool's tokens."""
+    row = 64 * min(pages, pages_per_request)
+    return 4 * ((w.n_layers + 2) * max_requests * w.n_kv_heads * row + 64 * pages * w.n_q_heads)
+
+
+def cache_for_budget(w: wl.Workload, fmt: int, budget_bytes: int, max_requests: int, max_len: int, device,
+                     evicts: bool = False):
+    """The cache with the most pages whose device block, with what eviction keeps beside it, fits
+    the budget."""
     ppr = -(-max_len // 64) + 2
 
     def cfg(pages):
         return N.oscar_config(fmt, w.head_dim, w.n_q_heads, w.n_kv_heads, w.group, 64, w.n_sink, w.window, w.n_layers,
                               max_requests, pages, ppr)
 
+    def total(pages):
+        return N.oscar_cache_device_bytes(cfg(pages)) + (eviction_bytes(w, max_requests, pages, ppr) if evicts else 0)
+
     lo, hi = 1, 1 << 24
-    if N.oscar_cache_device_bytes(cfg(lo)) > budget_bytes:
+    if total(lo) > budget_bytes:
         raise ValueError(f"a budget of {budget_bytes} bytes holds no page")
     while lo < hi:
         mid = (lo + hi + 1) // 2
-        if N.oscar_cache_device_bytes(cfg(mid)) <= budget_bytes:
+        if total(mid) <= budget_bytes:
             lo = mid
         else:
             hi = mid - 1
@@ -143,7 +157,7 @@ class ServingLoop:
         self.W = w.window if fmt in _INT2 else 0
         self.prefix = prefix_tokens
         self.prefill_chunk = prefill_chunk
-        self.cache = cache_for_budget(w, fmt, budget_bytes, max_requests, max_len, device)
+        self.cache = cache_for_budget(w, fmt, budget_bytes, max_requests, max_len, device, evicts=evict_above > 0)
         if fmt in _INT2:
             RK, RV, cK, cV = layer_params
             for layer in range(w.n_layers):

@@ -50,3 +50,23 @@ def test_sharers_that_evict_twice_fit(pages):
     assert st["completed"] == 3 and st["prefix_hits"] == 3 and st["evictions"] >= 6
     assert loop.cache.status() == (0, 0)
     loop.close()
+
+
+def test_eviction_keeps_within_the_budget():
+    """The default slots and lengths in 1 GiB: cache, weights and what a run allocates besides (the
+    decode's partial sums aside, which every format's loop has) stay within it."""
+    w = shape(n_layers=4, n_q_heads=32, n_kv_heads=8)
+    tokens = serving.TokenSource(w, SEED, pool_tokens=2048)
+    budget = 1 << 30
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    loop = serving.ServingLoop(w, OSCAR_FORMAT_BF16, budget, tokens, evict_above=700, evict_to=300)
+    assert torch.cuda.memory_allocated() - before <= budget
+    assert loop.cache.nbytes > budget // 4  # and most of it is not given away
+    st = loop.run([serving.Request(rid=i, prompt=600 + 50 * i, gen=150) for i in range(6)])
+    assert st["completed"] == 6 and st["evictions"] >= 6
+    scores = loop.cache.weights_workspace.numel() - (N.oscar_decode_weights_workspace_max_bytes(loop.cache.handle)
+                                                     - 4 * 128 * 32 * loop.cache.weights_stride)
+    kept = sum(t.numel() * 4 for t in [*loop.weights, loop._weights_out, loop._kept])
+    assert loop.cache.nbytes + kept + scores <= budget
+    loop.close()
