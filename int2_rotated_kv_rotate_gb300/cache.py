@@ -113,7 +113,8 @@ class KVCache:
             full = N.oscar_decode_workspace_max_bytes(self.handle)
             with N.on_stream(stream):
                 self.workspace = torch.empty(max(need, full, 256), dtype=torch.uint8, device=self.device)
-        self._weights_need = N.oscar_decode_weights_workspace_bytes(self.handle)
+        if not self.is_int2:
+            self._weights_need = N.oscar_decode_weights_workspace_bytes(self.handle)
         return need
 
     def plan_info(self):
@@ -172,7 +173,7 @@ class KVCache:
             captured = torch.cuda.is_current_stream_capturing()
             if ws is None or ws.numel() < (full if captured else self._weights_need):
                 for handle in self._weights_streams:  # launches of any of them may still use the old one
-                    ws.record_stream(torch.cuda.ExternalStream(handle))
+                    ws.record_stream(torch.cuda.ExternalStream(handle, device=self.mem.device))
                 scores = self._weights_need - full + 4 * self.cfg.max_requests * self.cfg.n_q_heads * self.weights_stride
                 size = full if captured else min(full, self._weights_need + scores // 4)
                 self.weights_workspace = ws = torch.empty(max(size, 256), dtype=torch.uint8, device=self.device)
