@@ -5,7 +5,7 @@
 // fixed-point fraction of a turn, so p t_i modulo one turn is one wrapping integer product:
 // exact for every position, with no fp64 and no range reduction of a large angle.  The top
 // two bits (rounded) are the quadrant, and what is left is at most an eighth of a turn and
-// converts to fp32 with a relative error of 2^-24.
+// converts to fp32, all of its bits at once, with a relative error of 2^-24.
 //
 // Elementwise and HBM-bound: every channel is read once and written once.  A CTA takes the
 // rows of `rows_per_cta` positions and some 320 threads' worth of heads.  It computes its
@@ -15,8 +15,9 @@
 // pairs (interleaved).  Two rows are loaded before the first is stored.  Walking the rows
 // with a fixed head costs one pointer step a row; walking the heads of a row, and holding
 // the sines in registers, spent more on addresses than it saved (8192 rows of 40 heads with
-// 96 turning channels: 54 against 41 us).  Measured: 5.65 TB/s on 16384 rows of 72 bf16
-// heads (107 us), 5.6 TB/s on 4099 rows of 40 fp32 heads (30 us); one row 1.7 us in a graph.
+// 96 turning channels: 54 against 41 us).  Measured: 5.8 TB/s on 16384 rows of 72 bf16
+// heads (104 us), 5.9 TB/s on 4099 rows of 40 fp32 heads (28.5 us); one row 1.6 us in a graph;
+// without vectors, 8192 rows of 40 bf16 heads with 18 turning channels 50 us (31 with 128).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -28,8 +28,9 @@
 // shared tokens at GQA 8.)
 //
 // Measured (one launch, cold): 8 requests at GQA 4 on 65536 tokens of 8 kv-heads, 268 MB, 51.6 us
-// (5.2 TB/s); 32 requests at GQA 8, 87.9 us, where a page and block takes 768 cycles of the
-// tensor pipe and about as many of shared memory for the MMAs' operands and the copies.
+// (5.2 TB/s); 32 requests at GQA 8, 87.9 us, where a page and block takes 1500 cycles, 768 of the
+// tensor pipe and about as many of shared memory for the MMAs' operands and the copies: neither
+// is the bound; what is left is the chain of a block's S, softmax, P and O.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
