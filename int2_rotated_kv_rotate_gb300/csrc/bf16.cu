@@ -26,6 +26,13 @@ constexpr int kBf16PerSM = NBUF == 3 ? 2 : 3;  // (told to the compiler, which e
 template <int G, int NBUF>
 constexpr int kBf16SlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::kBytes;
 
+// Where the scores of an item's (request, kv-head) begin.
+template <int G>
+__device__ __forceinline__ size_t score_offset(const KernelParams& kp, const DecodeItem& it, const DecodeReq& dr) {
+  const long long base = reinterpret_cast<const long long*>(kp.base + kp.lay.score_base)[it.req];
+  return (size_t(base) + size_t(it.kvh) * size_t(dr.L)) * G;
+}
+
 // WEIGHTS: the scores (log2 units) go to scores, fp32 [kv-head][L][G] of each plan request, and
 // each head's (maximum, 1 / denominator) to ml, for bf16_weights_kernel.
 // after_shared: the preceding launch attends the plan's shared runs.  It waited for its own
@@ -96,7 +103,8 @@ __global__ void __launch_bounds__(128, kBf16PerSM<NBUF>) bf16_split_kernel(Kerne
     }
     for (int e = threadIdx.x; e < G * kHeadDim; e += 128) qs[(e / kHeadDim) * kQRow + e % kHeadDim] = bf16_f32(q[head0 * kHeadDim + e]);
     __syncthreads();
-    float* sc = WEIGHTS ? scores + (size_t(dr.score0) + size_t(it.kvh) * size_t(dr.L)) * G : nullptr;
+    float* sc = nullptr;
+    if constexpr (WEIGHTS) sc = scores + score_offset<G>(kp, it, dr);
     auto keep = [=](int h, int u, float s) {
       if constexpr (WEIGHTS) sc[size_t(u) * G + h] = s;
     };
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(kWeightsThreads) bf16_weights_kernel(KernelPar
     float2 head[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) head[h] = ml[size_t(it.req) * kp.n_q_heads + size_t(it.kvh) * G + h];
-    const float* sc = scores + (size_t(dr.score0) + size_t(it.kvh) * size_t(dr.L)) * G;
+    const float* sc = scores + score_offset<G>(kp, it, dr);
     const size_t row = (size_t(dr.slot) * kp.n_kv_heads + it.kvh) * size_t(kp.weights_stride);
     for (int p = t0 + int(blockIdx.y) * kPiece; p < t1; p += int(gridDim.y) * kPiece) {
       float4 s[4][G / 4];

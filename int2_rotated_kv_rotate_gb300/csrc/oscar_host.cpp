@@ -46,7 +46,8 @@ oscar_status fail(oscar_status st, const char* fmt, ...) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // offsets of the items inside a plan block (counts at 0, requests at 256)
 size_t append_items_offset(size_t reqs) { return 256 + align256(reqs * sizeof(AppendReq)); }
-size_t decode_items_offset(size_t reqs) { return 256 + align256(reqs * sizeof(DecodeReq)); }
+size_t score_base_offset(size_t reqs) { return 256 + align256(reqs * sizeof(DecodeReq)); }
+size_t decode_items_offset(size_t reqs) { return score_base_offset(reqs) + align256(reqs * 8); }
 // offset of the items behind the order of a plan's shared runs
 size_t shared_items_offset(size_t reqs) { return align256(reqs * 4); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -150,6 +151,7 @@ DeviceLayout compute_layout(const oscar_config& c) {
   L.decode_plan = take(decode_items_offset(reqs) + L.max_decode_items * sizeof(DecodeItem));
   L.decode_counts = L.decode_plan;
   L.decode_reqs = L.decode_plan + 256;
+  L.score_base = L.decode_plan + score_base_offset(reqs);
   L.decode_items = L.decode_plan + decode_items_offset(reqs);
   if (c.format == OSCAR_FORMAT_BF16) {
     L.max_shared_items = 16384;
@@ -988,6 +990,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   std::vector<DecodeItem> items;
   int n_bf16 = 0, max_pages = 0, n_slots = 0;
   long long tokens = 0;  // of all kv-heads
+  std::vector<long long> score_base(n_req);
   for (int i = 0; i < n_req; ++i) {
     DecodeReq& q = reqs[i];
     q.slot = slots[i];
@@ -1003,7 +1006,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
       const int n_s = std::min(q.L, S);
       u_new = std::min(n_bf, Lpre[i] < n_s ? Lpre[i] : n_s + std::max(0, Lpre[i] - q.H));
     }
-    q.score0 = tokens;
+    score_base[i] = tokens;
     tokens += (long long)Hkv * q.L;
     q.first_item = n_slots;
     q.n_shared = runs.n_segs[i];
@@ -1067,6 +1070,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   counts[2] = n_front;
   counts[3] = int(runs.items.size());
   std::memcpy(u.staging + 256, reqs.data(), reqs.size() * sizeof(DecodeReq));
+  std::memcpy(u.staging + score_base_offset(c->cfg.max_requests), score_base.data(), score_base.size() * 8);
   DecodeItem* staged = reinterpret_cast<DecodeItem*>(u.staging + items_off);
   for (size_t k = 0; k < order.size(); ++k) staged[k] = items[order[k]];
   if (!runs.items.empty()) {
