@@ -129,9 +129,12 @@ class KVCache:
         if tuple(q.shape) != shape or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != self.mem.device:
             raise ValueError(f"q must be contiguous bf16 {shape} on {self.mem.device}")
         if out is None:
-            with N.on_stream(stream):
+            if stream is None:
                 out = torch.empty_like(q)
-        if (tuple(out.shape) != shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
+            else:
+                with N.on_stream(stream):
+                    out = torch.empty_like(q)
+        elif (tuple(out.shape) != shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
                 or out.device != self.mem.device):
             raise ValueError("out must be contiguous bf16 like q")
         if out_f32 is not None and (tuple(out_f32.shape) != shape or out_f32.dtype != torch.float32
