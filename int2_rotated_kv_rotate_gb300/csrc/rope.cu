@@ -16,7 +16,7 @@
 // with a fixed head costs one pointer step a row; walking the heads of a row, and holding
 // the sines in registers, spent more on addresses than it saved (8192 rows of 40 heads with
 // 96 turning channels: 54 against 41 us).  Measured: 5.8 TB/s on 16384 rows of 72 bf16
-// heads (104 us), 5.9 TB/s on 4099 rows of 40 fp32 heads (28.5 us); one row 1.6 us in a graph;
+// heads (104 us), 6.0 TB/s on 4099 rows of 40 fp32 heads (28.1 us); one row 1.6 us in a graph;
 // without vectors, 8192 rows of 40 bf16 heads with 18 turning channels 50 us (31 with 128).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
   const int z = head >= p.x[0].n_heads;
   const RopeTensor& x = p.x[z];
   const int h = z ? head - p.x[0].n_heads : head;
-  const bool mine = threadIdx.x / p.units < p.head_lanes && h < x.n_heads;
+  bool mine = threadIdx.x / p.units < p.head_lanes && h < x.n_heads;
   const bool turns = unit < p.turn_units;
   const bool single = !turns && unit - p.turn_units < p.pass_from - p.rotary_dim;
   const int c0 = turns    ? unit * kChannels
@@ -129,11 +129,10 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
           if (turns) b[k] = load<T, kChannels, kVec>(in + k * x.in_row + pairs);
       }
   };
-  const bool copies = mine && !turns && static_cast<const void*>(in) != static_cast<const void*>(out);
-  const bool works = copies || (mine && turns);  // (nothing to read past rotary_dim in place)
+  if (!turns && static_cast<const void*>(in) == static_cast<const void*>(out)) mine = false;  // in place: nothing to copy
   pdl_wait();
   pdl_trigger();
-  if (works && (kVec || turns)) fetch(0);  // in flight while the table is made
+  if (mine && (kVec || turns)) fetch(0);  // in flight while the table is made
   for (int e = threadIdx.x; e < n_rows * pairs; e += blockDim.x) {
     const int r = e / pairs, i = e - r * pairs;
     const long long pos = p.positions64 ? reinterpret_cast<const long long*>(p.positions)[row0 + r]
@@ -143,7 +142,7 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
         make_float2(cs.x * p.magnitude, (p.transpose ? -cs.y : cs.y) * p.magnitude);
   }
   __syncthreads();
-  if (!works) return;
+  if (!mine) return;
   if constexpr (!kVec) {
     if (!turns) {  // single channels and 16-byte vectors past rotary_dim
       for (int r = 0; r < n_rows; ++r, in += x.in_row, out += x.out_row) {
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(512, INTERLEAVED ? kPerSMInterleaved : kPerSMH
           tv = from_f32<T>(v * cs.x + u * cs.y);
         }
       }
-      if (turns || copies) store<T, kChannels, kVec>(o, a[k]);
+      store<T, kChannels, kVec>(o, a[k]);
       if constexpr (!INTERLEAVED)
         if (turns) store<T, kChannels, kVec>(o + pairs, b[k]);
     }
