@@ -86,17 +86,24 @@ typedef enum {
  * step's append can run inside the decode launch.  OSCAR_FORMAT_INT2_CM: the same stored
  * numbers with channel-major value pages, decoded on the tcgen05 tensor cores with the
  * code operands in tensor memory (GQA 4 or 8 at group 128, GQA 4 at group 32); the append
- * always runs as its own launch.  OSCAR_FORMAT_BF16: the uncompressed comparison cache. */
-typedef enum { OSCAR_FORMAT_INT2 = 0, OSCAR_FORMAT_BF16 = 1, OSCAR_FORMAT_INT2_CM = 2 } oscar_format;
+ * always runs as its own launch.  OSCAR_FORMAT_BF16: the uncompressed comparison cache.
+ * OSCAR_FORMAT_INT4: every token in 4-bit pages, with no rotation, sinks or recent window
+ * (oscar_int4_append below has its rows). */
+typedef enum {
+  OSCAR_FORMAT_INT2 = 0,
+  OSCAR_FORMAT_BF16 = 1,
+  OSCAR_FORMAT_INT2_CM = 2,
+  OSCAR_FORMAT_INT4 = 4
+} oscar_format;
 
 typedef struct {
   int format;                /* oscar_format */
   int head_dim;              /* must be 128 */
   int n_q_heads;             /* H_q */
   int n_kv_heads;            /* H_kv; H_q / H_kv must be 4 or 8 */
-  int group;                 /* INT2 quantisation group along head_dim: 32 or 128 */
+  int group;                 /* INT2 and INT4 quantisation group along head_dim: 32 or 128 */
   int page;                  /* tokens per page: must be 64 */
-  int n_sink;                /* S, 0..64 (INT2 format; BF16 format ignores it) */
+  int n_sink;                /* S, 0..64 (INT2 format; BF16 and INT4 ignore it) */
   int window;                /* W, 0..1024 and a multiple of 16 (INT2 format) */
   int n_layers;              /* >= 1 */
   int max_requests;          /* request slots */
@@ -249,6 +256,47 @@ oscar_status oscar_bf16_append(oscar_cache* cache, int layer, const void* k_new,
 oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const void* q, void* out, void* workspace,
                                          size_t ws_bytes, float* out_f32, void* stream);
 
+/* Appends with rotary positions (formats OSCAR_FORMAT_BF16 and OSCAR_FORMAT_INT4), in the place
+ * of oscar_rope and the format's append: the reservation's new keys are turned by their
+ * positions on the way into the pages, its values go in as they are, and the queries of the same
+ * tokens, if given, are turned into q->out; one launch.  What the cache holds and q->out are
+ * those of oscar_rope (keys rounded to bf16) and the append after it, bit for bit.
+ * k, v: the rows of the reservation [sum n_new][H_kv][d] bf16, any row and head strides >= 0 in
+ * elements, channels contiguous (a fused projection's slices go in as they are).  q NULL, or
+ * the queries of the same rows in bf16, as a tensor of oscar_rope (q->out may be q->in; no other
+ * overlap of q->out with an input is allowed).  steps, rotary_dim (<= 128), magnitude: as for
+ * oscar_rope; flags: OSCAR_ROPE_INTERLEAVED, OSCAR_ROPE_POSITIONS64.  positions [dev]: int32
+ * (int64 with the flag), one a row, or NULL: a token's place in its request.  The current device
+ * must be the cache's. */
+typedef struct {
+  const void* in;
+  long long row, head;
+} oscar_rows;
+struct oscar_rope_tensor_s;
+oscar_status oscar_append_rotated(oscar_cache* cache, int layer, const uint64_t* steps, int rotary_dim, float magnitude,
+                                  uint32_t flags, const void* positions, const struct oscar_rope_tensor_s* q,
+                                  const oscar_rows* k, const oscar_rows* v, void* stream);
+
+/* 4-bit pages (format OSCAR_FORMAT_INT4): every token of a request, quantised as it is appended.
+ * Per token, K or V, and group of `group` consecutive channels, all in fp32: s = bf16((max x -
+ * min x) / 15), z = bf16(min x); code = 0 if s == 0 else fminf(fmaxf(rintf((x - z) / s), 0), 15);
+ * value fmaf(code, s, z).  Values past +-2^126 and infinities count as +-2^126, NaN as 2^126.
+ * Pools: codes [layer][phys_page][kv_head][K|V][64 tokens][64 B], sz [layer][phys_page][kv_head]
+ * [K|V][64 tokens][d/group][scale, zero] bf16.  Channel c of a page's token t is bits 4 (c % 8)
+ * .. + 3 of the little-endian word at byte 64 t + 16 ((c / 8 % 4) ^ (t / 2 % 4)) + 4 (c / 32).
+ * Requests, reservations, plans and prefix sharing are as for the BF16 format.
+ * oscar_int4_append: step 2 of an append, arguments as oscar_quantize_append.
+ * oscar_int4_read: the values of tokens [begin, end) of a request (a pending reservation's among
+ * them once they are appended) into k_out, v_out [dev] [end - begin][H_kv][d], contiguous, in
+ * dtype OSCAR_DTYPE_BF16 (one more rounding) or OSCAR_DTYPE_F32, 16-byte aligned, not overlapping.
+ * oscar_int4_decode_attention: softmax(q K^T / sqrt(d)) V over the values of all L tokens, as
+ * oscar_bf16_decode_attention takes it. */
+oscar_status oscar_int4_append(oscar_cache* cache, int layer, const void* k_new, const void* v_new, void* stream);
+oscar_status oscar_int4_read(oscar_cache* cache, int layer, int slot, int begin, int end, void* k_out, void* v_out,
+                             int dtype, void* stream);
+oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const void* q, void* out, void* workspace,
+                                         size_t ws_bytes, float* out_f32, void* stream);
+
 /* Accumulated attention weights (format OSCAR_FORMAT_BF16).  A row of weights is
  * oscar_weights_stride tokens, 64 * min(max_pages_per_request, max_pages); a buffer of one
  * layer is fp32 [max_requests][H_kv][stride] [dev], indexed by request slot and position and
@@ -382,7 +430,7 @@ oscar_status oscar_rope_steps(const oscar_rope_config* cfg, uint64_t* steps, flo
  * strides in elements (inputs: any >= 0; outputs: rows and heads that do not overlap).
  * Elementwise: out may be in, with the same strides; any other overlap of a call's outputs
  * with its inputs or outputs is not allowed. */
-typedef struct {
+typedef struct oscar_rope_tensor_s {
   const void* in;
   void* out;
   int n_heads;

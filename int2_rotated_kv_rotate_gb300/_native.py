@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(HERE, "liboscar.so")
 OSCAR_FORMAT_INT2 = 0
 OSCAR_FORMAT_BF16 = 1
 OSCAR_FORMAT_INT2_CM = 2  # INT2, channel-major value pages (tcgen05 decode)
+OSCAR_FORMAT_INT4 = 4  # every token in 4-bit pages
 OSCAR_FLAG_BAD_PAGE = 0x1
 OSCAR_FLAG_TIMEOUT = 0x2
 OSCAR_FLAG_BAD_SLOT = 0x4
@@ -49,6 +50,10 @@ class oscar_rope_tensor(ctypes.Structure):
         (n, ctypes.c_longlong) for n in ("in_row", "in_head", "out_row", "out_head")]
 
 
+class oscar_rows(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
 class oscar_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("codes", "sz", "sink", "ring", "bf16_pages", "codes_page_bytes",
                                                "sz_page_bytes", "bf16_page_bytes", "sink_bytes_per_head",
@@ -67,6 +72,7 @@ EXPORTS = [
     "oscar_decode_weights_workspace_bytes",
     "oscar_decode_weights_workspace_max_bytes", "oscar_bf16_decode_weights", "oscar_evict_begin", "oscar_evict",
     "oscar_evict_pages", "oscar_evict_commit", "oscar_evict_cancel",
+    "oscar_append_rotated", "oscar_int4_append", "oscar_int4_read", "oscar_int4_decode_attention",
     "oscar_set_wait_limit", "oscar_inject_fault", "oscar_get_status",
     "oscar_last_error", "oscar_last_launch_count",
 ]
@@ -127,6 +133,11 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(ctypes.c_float)]),
                 "oscar_rope": (I, [ctypes.POINTER(oscar_rope_tensor), I, P, I, I, ctypes.c_float, I, ctypes.c_uint32, P,
                                    ctypes.c_longlong, P]),
+                "oscar_append_rotated": (I, [P, I, P, I, ctypes.c_float, ctypes.c_uint32, P, ctypes.POINTER(oscar_rope_tensor),
+                                             ctypes.POINTER(oscar_rows), ctypes.POINTER(oscar_rows), P]),
+                "oscar_int4_append": (I, [P, I, P, P, P]),
+                "oscar_int4_read": (I, [P, I, I, I, I, P, P, I, P]),
+                "oscar_int4_decode_attention": (I, [P, I, P, P, P, S, P, P]),
                 "oscar_set_wait_limit": (I, [P, ctypes.c_uint32]),
                 "oscar_inject_fault": (I, [P, ctypes.c_uint32]),
                 "oscar_get_status": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -439,3 +450,29 @@ def oscar_rope(tensors, steps, head_dim: int, rotary_dim: int, magnitude: float,
     arr = (oscar_rope_tensor * len(descs))(*descs)
     _check(lib().oscar_rope(arr, len(descs), steps.data_ptr(), head_dim, rotary_dim, magnitude, dtype, flags,
                             positions.data_ptr(), positions.shape[0], _stream(stream)))
+
+
+def oscar_append_rotated(handle: int, layer: int, steps, rotary_dim: int, magnitude: float, flags: int, positions, q, q_out,
+                         k, v, stream=None) -> None:
+    """k, v and (nullable) q, q_out: [rows, heads, 128] device tensors of any row and head strides."""
+    sk, sv = k.stride(), v.stride()
+    qd = None
+    if q is not None:
+        a, b = q.stride(), q_out.stride()
+        qd = oscar_rope_tensor(q.data_ptr(), q_out.data_ptr(), q.shape[1], a[0], a[1], b[0], b[1])
+    _check(lib().oscar_append_rotated(handle, layer, steps.data_ptr(), rotary_dim, magnitude, flags, _ptr(positions),
+                                      qd, oscar_rows(k.data_ptr(), sk[0], sk[1]), oscar_rows(v.data_ptr(), sv[0], sv[1]),
+                                      _stream(stream)))
+
+
+def oscar_int4_append(handle: int, layer: int, k_new, v_new, stream=None) -> None:
+    _check(lib().oscar_int4_append(handle, layer, _ptr(k_new), _ptr(v_new), _stream(stream)))
+
+
+def oscar_int4_read(handle: int, layer: int, slot: int, begin: int, end: int, k_out, v_out, dtype: int, stream=None) -> None:
+    _check(lib().oscar_int4_read(handle, layer, slot, begin, end, _ptr(k_out), _ptr(v_out), dtype, _stream(stream)))
+
+
+def oscar_int4_decode_attention(handle: int, layer: int, q, out, workspace, out_f32=None, stream=None) -> None:
+    _check(lib().oscar_int4_decode_attention(handle, layer, _ptr(q), _ptr(out), _ptr(workspace), workspace.numel(),
+                                             _ptr(out_f32), _stream(stream)))

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liboscar.so")
-SOURCES = ["oscar_host.cpp", "append.cu", "decode.cu", "bf16.cu", "calib.cu", "rope.cu", "evict.cu", "shared.cu"]
+SOURCES = ["oscar_host.cpp", "append.cu", "decode.cu", "bf16.cu", "calib.cu", "rope.cu", "evict.cu", "shared.cu",
+           "append_rows.cu", "int4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

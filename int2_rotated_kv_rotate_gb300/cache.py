@@ -12,7 +12,8 @@ from . import _native as N
 
 class KVCache:
     """One cache: INT2 mixed-precision (fmt=N.OSCAR_FORMAT_INT2, or N.OSCAR_FORMAT_INT2_CM with
-    channel-major value pages) or plain BF16 pages (N.OSCAR_FORMAT_BF16)."""
+    channel-major value pages), plain BF16 pages (N.OSCAR_FORMAT_BF16) or 4-bit pages
+    (N.OSCAR_FORMAT_INT4)."""
 
     def __init__(self, *, fmt: int = N.OSCAR_FORMAT_INT2, n_q_heads: int, n_kv_heads: int, group: int = 128,
                  n_sink: int = 4, window: int = 128, n_layers: int = 1, max_requests: int = 1, max_pages: int,
@@ -32,6 +33,7 @@ class KVCache:
         self.weights_stride = N.oscar_weights_stride(self.handle)  # 0: no weights in this format
         self.fmt = fmt
         self.is_int2 = fmt in (N.OSCAR_FORMAT_INT2, N.OSCAR_FORMAT_INT2_CM)
+        self.is_int4 = fmt == N.OSCAR_FORMAT_INT4
         self._rows = None  # rows of k_new / v_new the pending reservation expects
         self._n_plan = None  # requests of the current decode plan
 
@@ -91,11 +93,77 @@ class KVCache:
         self._check_tokens(k_new, v_new)
         N.oscar_bf16_append(self.handle, layer, k_new, v_new, stream)
 
+    def int4_append(self, layer: int, k_new, v_new, stream=None) -> None:
+        self._check_tokens(k_new, v_new)
+        N.oscar_int4_append(self.handle, layer, k_new, v_new, stream)
+
     def append(self, layer: int, k_new, v_new, stream=None) -> None:
         if self.is_int2:
             self.quantize_append(layer, k_new, v_new, stream)
+        elif self.is_int4:
+            self.int4_append(layer, k_new, v_new, stream)
         else:
             self.bf16_append(layer, k_new, v_new, stream)
+
+    def append_rotated(self, layer: int, rotary, k_new, v_new, q=None, *, positions=None, q_out=None, stream=None):
+        """append of k_new turned by its positions (`rotary`, a RotaryEmbedding of 128 channels), and
+        q' of the same tokens' queries, in one launch (BF16 and INT4 formats): what
+        rotary.apply(positions, q, k) and append would leave, bit for bit.  k_new, v_new bf16 [rows,
+        H_kv, 128] and q [rows, heads, 128], any row and head strides; positions int32 or int64
+        [rows], by default the tokens' places in their requests.  q' is a new contiguous tensor
+        unless q_out is given; q_out = q works in place."""
+        rows, dev = self._rows, self.mem.device
+        if rotary.head_dim != 128 or rotary.device != dev:
+            raise ValueError(f"rotary must have 128 channels a head, on {dev}")
+        for name, t, heads in (("k_new", k_new, self.cfg.n_kv_heads), ("v_new", v_new, self.cfg.n_kv_heads)):
+            if (tuple(t.shape) != (rows, heads, 128) or t.dtype != torch.bfloat16 or t.device != dev
+                    or t.stride()[2] != 1):
+                raise ValueError(f"{name} must be bf16 [{rows}, {heads}, 128] on {dev} with contiguous channels")
+        flags = N.OSCAR_ROPE_INTERLEAVED if rotary.interleaved else 0
+        if positions is not None:
+            if (tuple(positions.shape) != (rows,) or positions.dtype not in (torch.int32, torch.int64)
+                    or positions.device != dev or (rows > 1 and positions.stride(0) != 1)):
+                raise ValueError(f"positions must be contiguous int32 or int64 [{rows}] on {dev}")
+            if positions.dtype == torch.int64:
+                flags |= N.OSCAR_ROPE_POSITIONS64
+        given = q_out is not None
+        if q is not None:
+            shape = tuple(q.shape)
+            if (len(shape) != 3 or shape[0] != rows or shape[1] < 1 or shape[2] != 128 or q.dtype != torch.bfloat16
+                    or q.device != dev or q.stride()[2] != 1):
+                raise ValueError(f"q must be bf16 [{rows}, heads, 128] on {dev} with contiguous channels")
+            if torch.is_grad_enabled() and (q.requires_grad or (given and q_out.requires_grad)):
+                raise ValueError("queries that require grad are turned by RotaryEmbedding.apply")
+            if not given:
+                with N.on_stream(stream):  # in the launch's order
+                    q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            elif (tuple(q_out.shape) != shape or q_out.dtype != torch.bfloat16 or q_out.device != dev
+                    or q_out.stride()[2] != 1):
+                raise ValueError("q_out must be like q, with contiguous channels")
+        elif given:
+            raise ValueError("q_out without q")
+        N.oscar_append_rotated(self.handle, layer, rotary.steps, rotary.rotary_dim, rotary.magnitude, flags, positions, q, q_out,
+                               k_new, v_new, stream)
+        if given:
+            torch.autograd.graph.increment_version(q_out)
+        return q_out
+
+    def read(self, layer: int, slot: int, begin: int, end: int, k_out=None, v_out=None, *, dtype=torch.bfloat16, stream=None):
+        """The values (K, V) that 4-bit pages hold of a request's tokens [begin, end), [end - begin,
+        H_kv, 128] in bf16 or fp32 (dtype, unless the outputs are given)."""
+        shape = (max(0, end - begin), self.cfg.n_kv_heads, self.cfg.head_dim)
+        with N.on_stream(stream):  # what this call makes is made in the launch's order
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=self.mem.device)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=k_out.dtype, device=self.mem.device)
+        for t in (k_out, v_out):
+            if (tuple(t.shape) != shape or t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != k_out.dtype
+                    or not t.is_contiguous() or t.device != self.mem.device):
+                raise ValueError(f"k_out and v_out must be contiguous {shape} of one dtype, bf16 or fp32, on {self.mem.device}")
+        code = N.OSCAR_DTYPE_F32 if k_out.dtype == torch.float32 else N.OSCAR_DTYPE_BF16
+        N.oscar_int4_read(self.handle, layer, slot, begin, end, k_out, v_out, code, stream)
+        return k_out, v_out
 
     def commit(self) -> None:
         N.oscar_commit_append(self.handle)
@@ -113,7 +181,7 @@ class KVCache:
             full = N.oscar_decode_workspace_max_bytes(self.handle)
             with N.on_stream(stream):
                 self.workspace = torch.empty(max(need, full, 256), dtype=torch.uint8, device=self.device)
-        if not self.is_int2:
+        if self.weights_stride:
             self._weights_need = N.oscar_decode_weights_workspace_bytes(self.handle)
         return need
 
@@ -146,6 +214,8 @@ class KVCache:
         out = self._check_decode(q, out, out_f32, stream)
         if self.is_int2:
             N.oscar_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
+        elif self.is_int4:
+            N.oscar_int4_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
         else:
             N.oscar_bf16_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
         return out
@@ -248,7 +318,7 @@ class KVCache:
 
     def bf16_pages(self, layer: int) -> torch.Tensor:
         """The BF16 format's pages of one layer, a view: [pages, H_kv, K|V, 64, 128]."""
-        if self.is_int2:
+        if self.fmt != N.OSCAR_FORMAT_BF16:
             raise ValueError("BF16 pages need the BF16 format")
         n = self.cfg.max_pages * self.cfg.n_kv_heads * self.layout.bf16_page_bytes
         at = self.layout.bf16_pages + layer * n

@@ -1,0 +1,516 @@
+// Decode attention over 4-bit pages (OSCAR_FORMAT_INT4): split-K over the plan's page ranges, the
+// codes taken by the tensor cores in their stored form, as the 2-bit decode does.
+//
+// Persistent-style grid, 8 warps a CTA, two CTAs an SM; warp w takes every eighth half page (32
+// tokens) of an item, which bulk copies bring into stages of its own (no block barriers in the
+// loop).  Per 16 tokens, with mma.sync m16n8k16 (fp16 in, fp32 accumulate):
+//   scores  S[t, h] = sum_c code_K[t, c] q'[c, h]; q.k = s (q . code) + z sum(q) per group, in
+//           fp32.  q' is q (bf16, 8 bits) times a power of two of its head, exact in fp16;
+//   values  O[c, h] += sum_t code_V[c, t] P'[t, h], P' = p s_V / r (fp16), and sum_t p z_V in
+//           fp32.  r is a power of two no smaller than any scale so far (raised with O rescaled),
+//           so P' <= 1 at any magnitude of the values.  Its rounding to 11 bits is the one that
+//           the sums carry: 2^-12 of each token's share, where the output's own is up to 2^-8 of all.
+// A nibble masked in place (w & 0x000f000f, or << 4) is an fp16 subnormal, code * 2^-24 or 16 code *
+// 2^-24: one AND turns two codes into an MMA operand (one shift in four ANDs, and a byte permute in
+// four for the values, whose pairs are two tokens' codes of a channel).  The 16 is folded into q'
+// or into the output row's factor.
+//
+// Bound by HBM at 136 bytes (group 128) or 160 (group 32) a token and kv-head.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "int4.cuh"
+#include "oscar_internal.h"
+
+namespace oscar {
+namespace {
+
+constexpr int NW = 8, kThreads = 32 * NW;
+constexpr int kUnit = 32;  // tokens of a stage: half a page
+
+template <int G, int GROUP>
+struct Shape4 {
+  static constexpr int NG = kHeadDim / GROUP;
+  static constexpr int kCodeBytes = kUnit * kInt4Row;  // K; the same of V behind them
+  static constexpr int kSzBytes = kUnit * NG * 4;
+  static constexpr int kStageBytes = 2 * kCodeBytes + 2 * kSzBytes;
+  static constexpr int kStages = GROUP == 32 ? 2 : 3;  // two CTAs an SM
+  static constexpr int kPipe = NW * kStages * kStageBytes;
+  static constexpr int kQs = kPipe;                                // fp32 [G][kQRow]
+  static constexpr int kBars = (kQs + G * kQRow * 4 + 15) / 16 * 16;  // NW * kStages barriers, the slab's
+  static constexpr int kCtl = kBars + (NW * kStages + 1) * 8;      // last, next, poison
+  static constexpr int kSmemBytes = kCtl + 16;
+  static constexpr int kSlabSlots = kPipe / PartialSlot<G>::kBytes;
+  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert((NW * G * (kHeadDim + 4) + 8) * 4 <= kPipe, "per-warp results reuse the stages");
+  static_assert(kSzBytes % 16 == 0 && kStageBytes % 16 == 0, "bulk copies");
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+template <int G, int GROUP>
+__global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q,
+                                                                 uint8_t* __restrict__ partials, uint16_t* __restrict__ out,
+                                                                 float* __restrict__ out_f32) {
+  using C = Shape4<G, GROUP>;
+  constexpr int NG = C::NG, ST = C::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem + C::kQs);
+  uint64_t* all_bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint64_t* slab_bar = all_bars + NW * ST;
+  int* s_last = reinterpret_cast<int*>(smem + C::kCtl);
+  int* s_next = s_last + 1;
+  int* s_poison = s_last + 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i <= NW * ST; ++i) mbar_init(smem_u32(&all_bars[i]), 1);
+    *s_poison = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  uint8_t* pipe = smem + size_t(warp) * ST * C::kStageBytes;
+  uint64_t* bars = all_bars + warp * ST;
+  uint32_t phase_bits = 0, slab_phase = 0;  // bit st: parity of the next completion of stage st
+  // The plan and the page table were uploaded before the preceding kernels, and no kernel of the
+  // step writes the rows below H_pre, so the first item's pages wholly below it are copied before
+  // the wait on the preceding kernel.
+  const int n_items = reinterpret_cast<const int*>(kp.base + kp.lay.decode_counts)[0];
+  const WorkQueue wq{reinterpret_cast<unsigned*>(kp.base + kp.lay.sched), n_items, 0, n_items};
+  const float scale = kLog2e * rsqrtf(float(kHeadDim));
+  bool waited = false;
+  // (a CTA whose copies did not land takes no further work: *s_poison, written before the item's
+  // last barriers)
+  for (int ix = wq.first(); ix >= 0; ix = *s_poison ? -1 : wq.next(s_next)) {
+    const DecodeItem it = reinterpret_cast<const DecodeItem*>(kp.base + kp.lay.decode_items)[ix];
+    const DecodeReq dr = reinterpret_cast<const DecodeReq*>(kp.base + kp.lay.decode_reqs)[it.req];
+    const bool slot_ok = dr.slot >= 0 && dr.slot < kp.max_requests;
+    if (!slot_ok && threadIdx.x == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
+    const int t0 = it.begin * kPage, t1 = slot_ok && it.kind == 0 ? min(it.end * kPage, dr.L) : t0;
+    const int n_units = t1 > t0 ? (t1 - t0 + kUnit - 1) / kUnit : 0;
+    const int n_my = n_units > warp ? (n_units - warp + NW - 1) / NW : 0;
+    const int* ptab =
+        reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(slot_ok ? dr.slot : 0) * kp.max_pages_per_request;
+    // copies of the warp's k-th half page into stage k % ST; false (none) if the page id is out of range
+    auto issue = [&](int k) -> bool {
+      const int u = warp + NW * k, lp = it.begin + u / 2, half = u & 1;
+      const int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+      if (phys < 0 || phys >= kp.max_pages) return false;
+      if (lane == 0) {
+        const uint8_t* code = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
+                              size_t(phys) * kp.lay.codes_page_stride + size_t(it.kvh) * kp.lay.codes_head_stride +
+                              half * C::kCodeBytes;
+        const uint8_t* sz = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(phys) * kp.lay.sz_page_stride +
+                            size_t(it.kvh) * kp.lay.sz_head_stride + half * C::kSzBytes;
+        const uint32_t bar = smem_u32(&bars[k % ST]), dst = smem_u32(pipe + (k % ST) * C::kStageBytes);
+        fence_proxy_async();
+        mbar_expect_tx(bar, C::kStageBytes);
+        bulk_g2s(dst, code, C::kCodeBytes, bar);
+        bulk_g2s(dst + C::kCodeBytes, code + kPage * kInt4Row, C::kCodeBytes, bar);
+        bulk_g2s(dst + 2 * C::kCodeBytes, sz, C::kSzBytes, bar);
+        bulk_g2s(dst + 2 * C::kCodeBytes + C::kSzBytes, sz + kPage * NG * 4, C::kSzBytes, bar);
+      }
+      return true;
+    };
+    uint32_t ok_mask = 0;  // bit st: a copy into stage st is in flight
+    int issued = 0;
+    for (; issued < min(ST, n_my); ++issued) {
+      const int lp = it.begin + (warp + NW * issued) / 2;
+      if (!waited && (lp + 1) * kPage > dr.H_pre) break;
+      if (issue(issued)) ok_mask |= 1u << issued;
+    }
+    const size_t head0 = size_t(it.req) * kp.n_q_heads + size_t(it.kvh) * G;
+    if (!waited) {
+      if (threadIdx.x < 2 * G) prefetch_l2(q + head0 * kHeadDim + 64 * threadIdx.x);
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+      for (; issued < min(ST, n_my); ++issued)
+        if (issue(issued)) ok_mask |= 1u << issued;
+    }
+    for (int e = threadIdx.x; e < G * kHeadDim; e += kThreads)
+      qs[(e / kHeadDim) * kQRow + e % kHeadDim] = bf16_f32(q[head0 * kHeadDim + e]);
+    __syncthreads();
+    // ---- q' as score-MMA B fragments: column gid = head, channels 32 g + 8 tig + {n, n + 4}
+    uint32_t bq[8][2];
+    float back = 0.f;  // of column gid's head: what a product of codes and q' is short of, with the scale
+    {
+      float top = 0.f, x[4][8];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int n = 0; n < 8; n += 4) {
+          const float4 v = G == 8 || gid < G ? *reinterpret_cast<const float4*>(qs + gid * kQRow + 32 * g + 8 * tig + n)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[g][n] = v.x;
+          x[g][n + 1] = v.y;
+          x[g][n + 2] = v.z;
+          x[g][n + 3] = v.w;
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(13 - exponent of the largest); the exponent is held in [-110, 100], so that this and its
+      // inverse with the 2^24 stay in range
+      const int ex = min(max(int((__float_as_uint(top) >> 23) & 255u) - 127, -110), 100);
+      const float up = __uint_as_float(uint32_t(127 + 13 - ex) << 23);
+      back = scale * __uint_as_float(uint32_t(127 + 24 - 13 + ex) << 23);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float f = n & 1 ? up * 0.0625f : up;
+          bq[2 * g + (n >> 1)][n & 1] = half2_bits(x[g][n] * f, x[g][n + 4] * f);
+        }
+    }
+    // the heads of this thread's scores: 2 tig, 2 tig + 1 (idle past G)
+    float bk[2], qz[2][NG];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) bk[j] = __shfl_sync(0xffffffffu, back, 4 * (2 * tig + j));
+    {
+      // sums of q over the groups: lanes of column gid have theirs, then as above
+      float sum[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        sum[g] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) sum[g] += G == 8 || gid < G ? qs[gid * kQRow + 32 * g + 8 * tig + n] : 0.f;
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          qz[j][g] = scale * __shfl_sync(0xffffffffu, NG == 4 ? sum[g] : (sum[0] + sum[1]) + (sum[2] + sum[3]), 4 * (2 * tig + j));
+    }
+    // ---- the warp's half pages
+    float m_run[2] = {-INFINITY, -INFINITY}, muse[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f}, zv[2][NG], oacc[8][4];
+    float r_inv = 8.507059173023462e37f, r = 1.1754943508222875e-38f;  // 2^126 and its inverse
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) zv[j][g] = 0.f;
+#pragma unroll
+    for (int f = 0; f < 8; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oacc[f][e] = 0.f;
+    bool broken = false;
+    for (int k = 0; k < n_my; ++k) {
+      const int st = k % ST;
+      if ((ok_mask >> st) & 1u) {
+        if (!mbar_wait(smem_u32(&bars[st]), (phase_bits >> st) & 1u)) {
+          if (lane == 0) flag(kp, OSCAR_FLAG_TIMEOUT);
+          broken = true;
+          break;
+        }
+        phase_bits ^= 1u << st;
+        ok_mask &= ~(1u << st);
+      } else {  // a page that was not copied contributes nothing
+        if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+        __syncwarp();
+        if (k + ST < n_my && issue(k + ST)) ok_mask |= 1u << st;
+        continue;
+      }
+      const int valid = t1 - (t0 + (warp + NW * k) * kUnit);  // tokens of the unit (32 or more: all)
+      const uint8_t* stage = pipe + st * C::kStageBytes;
+      const uint8_t* kc = stage + 16 * (tig ^ ((gid >> 1) & 3));
+      const uint8_t* vc = stage + C::kCodeBytes + 16 * ((gid >> 1) ^ tig);
+      const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * C::kCodeBytes);
+      const uint32_t* vsz = ksz + kUnit * NG;
+      float lg[2][2][2];  // block, token gid or gid + 8, head
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ta = 16 * b + gid;
+        const uint4 va = *reinterpret_cast<const uint4*>(kc + ta * kInt4Row);
+        const uint4 vb = *reinterpret_cast<const uint4*>(kc + (ta + 8) * kInt4Row);
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        constexpr int NA = NG == 4 ? 4 : 2;  // at group 128 two chains of products
+        float acc[NA][4];
+#pragma unroll
+        for (int g = 0; g < NA; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[g][e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float(&a)[4] = acc[NG == 4 ? g : g & 1];
+          mma_f16_16816(a, wa[g] & kLow, wb[g] & kLow, wa[g] & kHigh, wb[g] & kHigh, bq[2 * g][0], bq[2 * g][1]);
+          const uint32_t sa = wa[g] >> 8, sb = wb[g] >> 8;
+          mma_f16_16816(a, sa & kLow, sb & kLow, sa & kHigh, sb & kHigh, bq[2 * g + 1][0], bq[2 * g + 1][1]);
+        }
+        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, off[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t sz[NG];
+          if constexpr (NG == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(ksz + (ta + 8 * i) * NG);
+            sz[0] = v.x, sz[1] = v.y, sz[2] = v.z, sz[3] = v.w;
+          } else {
+            sz[0] = ksz[ta + 8 * i];
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float s = bf16_lo(sz[g]), z = bf16_hi(sz[g]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float T = NG == 4 ? acc[g][2 * i + j] : acc[0][2 * i + j] + acc[1][2 * i + j];
+              sum[i][j] = fmaf(T, s, sum[i][j]);
+              off[i][j] = fmaf(z, qz[j][g], off[i][j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) lg[b][i][j] = fmaf(sum[i][j], bk[j], off[i][j]);
+        }
+      }
+      if (valid < kUnit) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (16 * b + 8 * i + gid >= valid) lg[b][i][0] = lg[b][i][1] = -INFINITY;
+      }
+      // ---- scales of the values, and the references of the maximum and of the scales
+      uint32_t szv[2][2][NG];
+      float top = 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t* at = vsz + (16 * b + 8 * i + gid) * NG;
+          if constexpr (NG == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at);
+            szv[b][i][0] = v.x, szv[b][i][1] = v.y, szv[b][i][2] = v.z, szv[b][i][3] = v.w;
+          } else {
+            szv[b][i][0] = *at;
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) top = fmaxf(top, bf16_lo(szv[b][i][g]));
+        }
+      float mloc[2];
+      bool over = top > r;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mloc[j] = fmaxf(fmaxf(lg[0][0][j], lg[0][1][j]), fmaxf(lg[1][0][j], lg[1][1][j]));
+        over |= mloc[j] > m_run[j];
+      }
+      if (__any_sync(0xffffffffu, over)) {
+        float alpha[2];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mloc[0] = fmaxf(mloc[0], __shfl_xor_sync(0xffffffffu, mloc[0], o));
+          mloc[1] = fmaxf(mloc[1], __shfl_xor_sync(0xffffffffu, mloc[1], o));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        float down = 1.f;
+        if (top > r) {  // (the lanes of a token have the same scales: uniform)
+          const float next = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x00800000u);  // < 2^126: finite
+          down = r * (1.f / next);
+          r = next;
+          r_inv = 1.f / next;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mnew = fmaxf(m_run[j], mloc[j]);
+          muse[j] = mnew == -INFINITY ? 0.f : mnew;
+          alpha[j] = ex2(m_run[j] - muse[j]);  // 0 while the reference was -inf
+          m_run[j] = mnew;
+          l_part[j] *= alpha[j];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) zv[j][g] *= alpha[j];
+          alpha[j] *= down;
+        }
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          oacc[f][0] *= alpha[0];
+          oacc[f][1] *= alpha[1];
+          oacc[f][2] *= alpha[0];
+          oacc[f][3] *= alpha[1];
+        }
+      }
+      // ---- values
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float p[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            p[i][j] = ex2(lg[b][i][j] - muse[j]);  // masked: exactly 0, and scale and zero are finite
+            l_part[j] += p[i][j];
+          }
+        uint32_t bp[NG][2];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float s = bf16_lo(szv[b][i][g]) * r_inv, z = bf16_hi(szv[b][i][g]);
+            bp[g][i] = movmatrix_trans(half2_bits(p[i][0] * s, p[i][1] * s));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) zv[j][g] = fmaf(p[i][j], z, zv[j][g]);
+          }
+        // tokens 2 tig, + 1, + 8, + 9 of the block; chunk gid / 2 of each, its half gid % 2
+        const uint8_t* at = vc + (16 * b + 2 * tig) * kInt4Row;
+        const uint4 a = *reinterpret_cast<const uint4*>(at), a1 = *reinterpret_cast<const uint4*>(at + kInt4Row);
+        const uint4 c = *reinterpret_cast<const uint4*>(at + 8 * kInt4Row), c1 = *reinterpret_cast<const uint4*>(at + 9 * kInt4Row);
+        const uint32_t wA[4] = {a.x, a.y, a.z, a.w}, wB[4] = {a1.x, a1.y, a1.z, a1.w};
+        const uint32_t wC[4] = {c.x, c.y, c.z, c.w}, wD[4] = {c1.x, c1.y, c1.z, c1.w};
+        const uint32_t sel = gid & 1 ? 0x7632u : 0x5410u;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t X = permute(wA[g], wB[g], sel), Y = permute(wC[g], wD[g], sel);
+          const int gg = NG == 4 ? g : 0;
+          mma_f16_16816(oacc[2 * g], X & kLow, X & kHigh, Y & kLow, Y & kHigh, bp[gg][0], bp[gg][1]);
+          const uint32_t X8 = X >> 8, Y8 = Y >> 8;
+          mma_f16_16816(oacc[2 * g + 1], X8 & kLow, X8 & kHigh, Y8 & kLow, Y8 & kHigh, bp[gg][0], bp[gg][1]);
+        }
+      }
+      __syncwarp();
+      if (k + ST < n_my && issue(k + ST)) ok_mask |= 1u << st;
+    }
+    if (broken) {
+      // copies still in flight land (bounded) before the stages are reused or the CTA exits
+      bool drained = true;
+      for (int st = 0; st < ST; ++st)
+        if ((ok_mask >> st) & 1u) {
+          if (mbar_wait(smem_u32(&bars[st]), (phase_bits >> st) & 1u)) phase_bits ^= 1u << st;
+          else drained = false;
+        }
+      if (!drained && lane == 0) *s_poison = 1;
+    }
+    // ---- the warps' sums into the partial
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l_part[j] += __shfl_xor_sync(0xffffffffu, l_part[j], o);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) zv[j][g] += __shfl_xor_sync(0xffffffffu, zv[j][g], o);
+      }
+    __syncthreads();  // every warp is done with its stages
+    float* wm = reinterpret_cast<float*>(smem);  // [NW][G] maxima
+    float* wl = wm + NW * G;                     // [NW][G] denominators
+    float* wo = wl + NW * G;                     // [NW][G][kRow]
+    constexpr int kRow = kHeadDim + 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int head = 2 * tig + j;
+      if (G == 8 || head < G) {
+        if (gid == 0) {
+          wm[warp * G + head] = broken ? -INFINITY : m_run[j];
+          wl[warp * G + head] = broken ? 0.f : l_part[j];
+        }
+        float* mine = wo + (warp * G + head) * kRow + 4 * gid;
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          // rows gid: 2^-24 a code; rows gid + 8: 2^-20
+          const float z = zv[j][NG == 4 ? f >> 1 : 0];
+          mine[32 * (f >> 1) + 2 * (f & 1)] = fmaf(oacc[f][j] * 16777216.f, r, z);
+          mine[32 * (f >> 1) + 2 * (f & 1) + 1] = fmaf(oacc[f][2 + j] * 1048576.f, r, z);
+        }
+      }
+    }
+    __syncthreads();
+    uint8_t* part = partials + size_t(it.slot) * PartialSlot<G>::kBytes;
+    for (int e = threadIdx.x; e < G * kHeadDim; e += kThreads) {
+      const int h = e / kHeadDim, c = e % kHeadDim;
+      float ms = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) ms = fmaxf(ms, wm[w * G + h]);
+      float l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float mw = wm[w * G + h];
+        if (mw == -INFINITY) continue;
+        const float a = ex2(mw - ms);
+        l = fmaf(a, wl[w * G + h], l);
+        o = fmaf(a, wo[(w * G + h) * kRow + c], o);
+      }
+      store_slot<G>(part, h, c, ms, l, o);
+    }
+    __syncthreads();  // read before the merge's copies or the next item's
+    MergeAcc<G, kThreads> acc;
+    if (merge_partial<G, kThreads>(kp, it, it.head_count, partials, acc, s_last, smem, C::kSlabSlots, smem_u32(slab_bar), slab_phase,
+                                   [] {})) {
+      const int c = threadIdx.x & (kHeadDim - 1), hb = threadIdx.x / kHeadDim;
+#pragma unroll
+      for (int i = 0; i < MergeAcc<G, kThreads>::HPT; ++i) {
+        const int h = hb + MergeAcc<G, kThreads>::kStride * i;
+        const float o = acc.L[i] > 0.f ? acc.O[i] / acc.L[i] : 0.f;
+        out[(head0 + h) * kHeadDim + c] = bf16_rne(o);
+        if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = o;
+      }
+    }
+    fence_proxy_async();  // generic use of the stages is over before later bulk copies
+    __syncthreads();
+  }
+  if (!waited) {  // no item: the launch still orders itself after the preceding kernel
+    pdl_wait();
+    pdl_trigger();
+  }
+  wq.leave();
+}
+
+template <int G, int GROUP>
+int resident_t(int n_sm) {
+  static PerDevice resident;
+  return resident.get([=] {
+    int e = int(cudaFuncSetAttribute(int4_split_kernel<G, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Shape4<G, GROUP>::kSmemBytes));
+    int per_sm = 0;
+    if (!e)
+      e = int(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, int4_split_kernel<G, GROUP>, kThreads,
+                                                            Shape4<G, GROUP>::kSmemBytes));
+    return e ? -e : (per_sm > 0 ? per_sm : 1) * n_sm;
+  });
+}
+
+template <int G, int GROUP>
+int launch_t(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* partials, int n_sm,
+             void* stream, int* launches) {
+  const int resident = resident_t<G, GROUP>(n_sm);
+  if (resident < 0) return -resident;
+  const int e = launch_ex(int4_split_kernel<G, GROUP>, dim3(resident), dim3(kThreads), size_t(Shape4<G, GROUP>::kSmemBytes),
+                          stream, kp, layer, static_cast<const uint16_t*>(q), partials, static_cast<uint16_t*>(out), out_f32);
+  if (!e) *launches += 1;
+  return e;
+}
+
+}  // namespace
+
+int int4_decode_resident_ctas(int gqa, int group, int n_sm) {
+  if (gqa == 4) return group == 32 ? resident_t<4, 32>(n_sm) : resident_t<4, 128>(n_sm);
+  if (gqa == 8) return group == 32 ? resident_t<8, 32>(n_sm) : resident_t<8, 128>(n_sm);
+  return n_sm;
+}
+
+int launch_int4_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
+                       const DecodeWorkspace& wl, int n_sm, void* stream, int* launches) {
+  uint8_t* partials = ws + wl.partials;
+  if (kp.gqa == 4)
+    return kp.group == 32 ? launch_t<4, 32>(kp, layer, q, out, out_f32, partials, n_sm, stream, launches)
+                          : launch_t<4, 128>(kp, layer, q, out, out_f32, partials, n_sm, stream, launches);
+  if (kp.gqa == 8)
+    return kp.group == 32 ? launch_t<8, 32>(kp, layer, q, out, out_f32, partials, n_sm, stream, launches)
+                          : launch_t<8, 128>(kp, layer, q, out, out_f32, partials, n_sm, stream, launches);
+  return int(cudaErrorInvalidValue);
+}
+
+}  // namespace oscar

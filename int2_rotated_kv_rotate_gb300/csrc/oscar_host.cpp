@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "int4.cuh"
 #include "oscar_internal.h"
 
 using namespace oscar;
@@ -77,8 +78,9 @@ bool config_ok(const oscar_config* c, std::string* why) {
     return false;
   };
   if (!c) return bad("config is NULL");
-  if (c->format != OSCAR_FORMAT_INT2 && c->format != OSCAR_FORMAT_BF16 && c->format != OSCAR_FORMAT_INT2_CM)
-    return bad("format must be INT2, INT2_CM or BF16");
+  if (c->format != OSCAR_FORMAT_INT2 && c->format != OSCAR_FORMAT_BF16 && c->format != OSCAR_FORMAT_INT2_CM &&
+      c->format != OSCAR_FORMAT_INT4)
+    return bad("format must be INT2, INT2_CM, BF16 or INT4");
   if (c->head_dim != kHeadDim) return bad("head_dim must be 128");
   if (c->page != kPage) return bad("page must be 64");
   if (c->n_kv_heads <= 0 || c->n_q_heads <= 0 || c->n_q_heads % c->n_kv_heads) return bad("bad head counts");
@@ -87,8 +89,8 @@ bool config_ok(const oscar_config* c, std::string* why) {
   if (c->n_layers <= 0 || c->max_requests <= 0 || c->max_pages <= 0 || c->max_pages_per_request <= 0)
     return bad("layers, requests and pages must be positive");
   if (c->max_pages_per_request > (1 << 20)) return bad("max_pages_per_request too large");
+  if (c->format != OSCAR_FORMAT_BF16 && c->group != 32 && c->group != 128) return bad("group must be 32 or 128");
   if (c->format == OSCAR_FORMAT_INT2 || c->format == OSCAR_FORMAT_INT2_CM) {
-    if (c->group != 32 && c->group != 128) return bad("group must be 32 or 128");
     if (c->format == OSCAR_FORMAT_INT2_CM && c->group == 32 && g != 4)
       return bad("the INT2_CM format supports group 32 at GQA 4 only");
     if (c->n_sink < 0 || c->n_sink > kPage) return bad("n_sink must be in [0, 64]");
@@ -131,6 +133,16 @@ DeviceLayout compute_layout(const oscar_config& c) {
     L.R_Vt = take(layers * Hkv * d * d * 4);
     L.clip_K = take(layers * Hkv * 4);
     L.clip_V = take(layers * Hkv * 4);
+  } else if (c.format == OSCAR_FORMAT_INT4) {
+    const size_t ng = d / c.group;
+    L.codes_head_stride = 2 * kPage * kInt4Row;
+    L.codes_page_stride = Hkv * L.codes_head_stride;
+    L.codes_layer_stride = pages * L.codes_page_stride;
+    L.codes = take(layers * L.codes_layer_stride);
+    L.sz_head_stride = 2 * kPage * ng * 4;
+    L.sz_page_stride = Hkv * L.sz_head_stride;
+    L.sz_layer_stride = pages * L.sz_page_stride;
+    L.sz = take(layers * L.sz_layer_stride);
   } else {
     L.bf16_head_stride = 2 * kPage * d * 2;
     L.bf16_page_stride = Hkv * L.bf16_head_stride;
@@ -294,11 +306,13 @@ oscar_status upload_rows(oscar_cache* c, const Upload& u, const std::vector<int>
 bool is_int2(const oscar_cache* c) {
   return c->cfg.format == OSCAR_FORMAT_INT2 || c->cfg.format == OSCAR_FORMAT_INT2_CM;
 }
+bool is_bf16(const oscar_cache* c) { return c->cfg.format == OSCAR_FORMAT_BF16; }
+bool is_int4(const oscar_cache* c) { return c->cfg.format == OSCAR_FORMAT_INT4; }
 // Channel-major value pages, decoded on the tcgen05 tensor cores; never a fused launch.
 bool is_cm(const oscar_cache* c) { return c->cfg.format == OSCAR_FORMAT_INT2_CM; }
 
 // Pages a request needs to hold its stored tokens: the INT2 format pages positions < H
-// (sinks and recent tokens live elsewhere), the BF16 format pages all L positions.
+// (sinks and recent tokens live elsewhere), the BF16 and INT4 formats page all L positions.
 int pages_needed(const oscar_cache* c, int L, int H) {
   if (is_int2(c)) return H > c->cfg.n_sink ? ceil_div(H, kPage) : 0;
   return ceil_div(L, kPage);
@@ -516,7 +530,7 @@ oscar_status oscar_cache_create(const oscar_config* cfg, void* device_mem, size_
   if (e == cudaSuccess) e = cudaMemset(c->base + lay.sched, 0, 16);
   // scale/zero words of rows no append has written yet (sink positions, the tail of a
   // page) are read with p = 0 by the decode: they must be finite, so the pool starts at 0
-  if (e == cudaSuccess && is_int2(c)) e = cudaMemset(c->base + lay.sz, 0, size_t(cfg->n_layers) * lay.sz_layer_stride);
+  if (e == cudaSuccess && !is_bf16(c)) e = cudaMemset(c->base + lay.sz, 0, size_t(cfg->n_layers) * lay.sz_layer_stride);
   if (e == cudaSuccess)
     e = cudaMemset(c->base + lay.app_done, 0, size_t(cfg->n_layers) * cfg->max_requests * cfg->n_kv_heads * 8);
   if (e == cudaSuccess && is_int2(c)) {
@@ -823,7 +837,7 @@ oscar_status oscar_quantize_append(oscar_cache* c, int layer, const void* k_new,
 oscar_status oscar_bf16_append(oscar_cache* c, int layer, const void* k_new, const void* v_new, void* stream) {
   g_launches = 0;
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
-  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_append needs the BF16 format");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_append needs the BF16 format");
   if (!c->reserved) return fail(OSCAR_ERR_STATE, "no reservation");
   if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
   if (c->app_rows > 0 && (!k_new || !v_new)) return fail(OSCAR_ERR_INVALID_ARG, "NULL token arrays");
@@ -831,6 +845,144 @@ oscar_status oscar_bf16_append(oscar_cache* c, int layer, const void* k_new, con
   int e = launch_bf16_append(kernel_params(c), layer, k_new, v_new, std::min(c->app_items, 4 * c->n_sm), stream,
                              &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "bf16 append launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+// Bytes that a call's rows reach past its pointer, or -1: a stride or their sum is out of range.
+static long long rows_reach(long long n_rows, int n_heads, long long row, long long head, size_t size) {
+  if (n_rows <= 0) return 0;
+  const long long limit = 1LL << 46;
+  if (row < 0 || head < 0 || row > limit / n_rows || head > limit / n_heads) return -1;
+  return ((n_rows - 1) * row + (n_heads - 1) * head + kHeadDim) * (long long)size;
+}
+
+oscar_status oscar_append_rotated(oscar_cache* c, int layer, const uint64_t* steps, int rotary_dim, float magnitude,
+                                  uint32_t flags, const void* positions, const oscar_rope_tensor* q, const oscar_rows* k,
+                                  const oscar_rows* v, void* stream) {
+  g_launches = 0;
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_append_rotated needs the BF16 or the INT4 format");
+  if (!c->reserved) return fail(OSCAR_ERR_STATE, "no reservation");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > kHeadDim)
+    return fail(OSCAR_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, 128]", rotary_dim);
+  if (flags & ~(OSCAR_ROPE_INTERLEAVED | OSCAR_ROPE_POSITIONS64))
+    return fail(OSCAR_ERR_INVALID_ARG, "unknown flags %#x", flags);
+  if (!k || !v) return fail(OSCAR_ERR_INVALID_ARG, "NULL k or v");
+  const long long n = c->app_rows;
+  AppendRowsParams p = {};
+  struct In {
+    const char* name;
+    uintptr_t at;
+    long long row, head, reach;
+    int heads;
+  };
+  In in[3] = {{"k", reinterpret_cast<uintptr_t>(k->in), k->row, k->head, 0, c->cfg.n_kv_heads},
+              {"v", reinterpret_cast<uintptr_t>(v->in), v->row, v->head, 0, c->cfg.n_kv_heads},
+              {"q", 0, 0, 0, 0, 0}};
+  if (q) {
+    if (q->n_heads < 1 || q->n_heads > 65536) return fail(OSCAR_ERR_INVALID_ARG, "q: %d heads", q->n_heads);
+    in[2] = {"q", reinterpret_cast<uintptr_t>(q->in), q->in_row, q->in_head, 0, q->n_heads};
+  }
+  for (In& x : in) {
+    if (!x.heads) continue;
+    if (n > 0 && !x.at) return fail(OSCAR_ERR_INVALID_ARG, "%s: NULL", x.name);
+    if (x.at % 2) return fail(OSCAR_ERR_INVALID_ARG, "%s: not aligned to bf16", x.name);
+    x.reach = rows_reach(n, x.heads, x.row, x.head, 2);
+    if (x.row < 0 || x.head < 0 || x.reach < 0) return fail(OSCAR_ERR_INVALID_ARG, "%s: strides out of range", x.name);
+  }
+  auto vec = [](uintptr_t at, long long row, long long head) { return (at | uintptr_t(2 * row) | uintptr_t(2 * head)) % 16 == 0; };
+  if (q) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q->out);
+    if (n > 0 && !at) return fail(OSCAR_ERR_INVALID_ARG, "q: NULL out");
+    if (at % 2) return fail(OSCAR_ERR_INVALID_ARG, "q: out is not aligned to bf16");
+    const long long reach = rows_reach(n, q->n_heads, q->out_row, q->out_head, 2);
+    if (q->out_row < 0 || q->out_head < 0 || reach < 0) return fail(OSCAR_ERR_INVALID_ARG, "q: strides out of range");
+    // heads inside their row, or rows inside their head
+    const bool rows_out = (q->n_heads == 1 || q->out_head >= kHeadDim) &&
+                          (n <= 1 || q->out_row >= (q->n_heads - 1) * q->out_head + kHeadDim);
+    const bool heads_out = (n <= 1 || q->out_row >= kHeadDim) &&
+                           (q->n_heads == 1 || q->out_head >= (n - 1) * q->out_row + kHeadDim);
+    if (!rows_out && !heads_out) return fail(OSCAR_ERR_INVALID_ARG, "q: output rows or heads overlap");
+    if (q->in == q->out && ((n > 1 && q->in_row != q->out_row) || (q->n_heads > 1 && q->in_head != q->out_head)))
+      return fail(OSCAR_ERR_INVALID_ARG, "q: in place with other strides");
+    p.q = {q->in, q->out, q->n_heads, q->in_row, q->in_head, q->out_row, q->out_head};
+    p.q_in_vec = vec(in[2].at, q->in_row, q->in_head);
+    p.q_out_vec = vec(at, q->out_row, q->out_head);
+  }
+  if (n == 0) return OSCAR_OK;
+  if (!steps) return fail(OSCAR_ERR_INVALID_ARG, "NULL steps");
+  const size_t pos_size = flags & OSCAR_ROPE_POSITIONS64 ? 8 : 4;
+  if (reinterpret_cast<uintptr_t>(steps) % 8 || reinterpret_cast<uintptr_t>(positions) % pos_size)
+    return fail(OSCAR_ERR_INVALID_ARG, "steps or positions are not aligned to their type");
+  oscar_status st = check_device(c);
+  if (st) return st;
+  p.k = k->in;
+  p.v = v->in;
+  p.k_row = k->row;
+  p.k_head = k->head;
+  p.v_row = v->row;
+  p.v_head = v->head;
+  p.k_vec = vec(in[0].at, k->row, k->head);
+  p.v_vec = vec(in[1].at, v->row, v->head);
+  p.steps = steps;
+  p.positions = positions;
+  p.rotary_dim = rotary_dim;
+  p.magnitude = magnitude;
+  p.interleaved = (flags & OSCAR_ROPE_INTERLEAVED) != 0;
+  p.positions64 = (flags & OSCAR_ROPE_POSITIONS64) != 0;
+  const int e = launch_append_rows(kernel_params(c), layer, p, is_int4(c), true, c->app_items, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "rotated append launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+oscar_status oscar_int4_append(oscar_cache* c, int layer, const void* k_new, const void* v_new, void* stream) {
+  g_launches = 0;
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!is_int4(c)) return fail(OSCAR_ERR_STATE, "oscar_int4_append needs the INT4 format");
+  if (!c->reserved) return fail(OSCAR_ERR_STATE, "no reservation");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (c->app_rows > 0 && (!k_new || !v_new)) return fail(OSCAR_ERR_INVALID_ARG, "NULL token arrays");
+  if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) % 2)
+    return fail(OSCAR_ERR_INVALID_ARG, "token arrays are not aligned to bf16");
+  if (c->app_items == 0) return OSCAR_OK;
+  AppendRowsParams p = {};
+  p.k = k_new;
+  p.v = v_new;
+  p.k_head = p.v_head = kHeadDim;
+  p.k_row = p.v_row = (long long)c->cfg.n_kv_heads * kHeadDim;
+  p.k_vec = reinterpret_cast<uintptr_t>(k_new) % 16 == 0;
+  p.v_vec = reinterpret_cast<uintptr_t>(v_new) % 16 == 0;
+  const int e = launch_append_rows(kernel_params(c), layer, p, true, false, c->app_items, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "int4 append launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
+oscar_status oscar_int4_read(oscar_cache* c, int layer, int slot, int begin, int end, void* k_out, void* v_out, int dtype,
+                             void* stream) {
+  g_launches = 0;
+  oscar_status st = check_slot(c, slot);
+  if (st) return st;
+  if (!is_int4(c)) return fail(OSCAR_ERR_STATE, "oscar_int4_read needs the INT4 format");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_F32)
+    return fail(OSCAR_ERR_UNSUPPORTED, "rows are read as bf16 or fp32, not dtype %d", dtype);
+  int L = c->reqs[slot].L;
+  if (c->reserved)
+    for (const AppendReq& a : c->app_reqs)
+      if (a.slot == slot) L = a.L1;
+  if (begin < 0 || end < begin || end > L)
+    return fail(OSCAR_ERR_INVALID_ARG, "tokens [%d, %d) of a request of %d", begin, end, L);
+  if (begin == end) return OSCAR_OK;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(k_out), b = reinterpret_cast<uintptr_t>(v_out);
+  if (!a || !b || (a | b) % 16) return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out must be given, 16-byte aligned");
+  const uintptr_t bytes = uintptr_t(end - begin) * c->cfg.n_kv_heads * kHeadDim * (dtype == OSCAR_DTYPE_F32 ? 4 : 2);
+  if (a < b + bytes && b < a + bytes) return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out overlap");
+  st = check_device(c);
+  if (st) return st;
+  const int e = launch_int4_read(kernel_params(c), layer, slot, begin, end, k_out, v_out, dtype == OSCAR_DTYPE_F32, c->n_sm,
+                                 stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "int4 read launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }
 
@@ -850,7 +1002,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   const bool shared = (flags & OSCAR_PLAN_SHARED_PREFIX) != 0;
   if ((flags & OSCAR_PLAN_SHARED_ALWAYS) && !shared)
     return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_SHARED_ALWAYS goes with OSCAR_PLAN_SHARED_PREFIX");
-  if (shared && is_int2(c))
+  if (shared && !is_bf16(c))
     return fail(OSCAR_ERR_INVALID_ARG, "OSCAR_PLAN_SHARED_PREFIX applies to the BF16 format");
   if (max_split_pages < 0) return fail(OSCAR_ERR_INVALID_ARG, "max_split_pages < 0");
   std::vector<char> seen(c->cfg.max_requests, 0);
@@ -912,8 +1064,9 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   const std::vector<int>& p0_of = runs.first_private;
   std::vector<int> np_of(n_req), nbf_of(n_req), bfnew_of(n_req), pgnew_of(n_req);
   int max_np = 1;
-  const int ng = kHeadDim / (is_int2(c) ? c->cfg.group : kHeadDim);
-  const long long page_bytes = is_int2(c) ? 2LL * kPage * (kRowBytes + 4 * ng) : 2LL * kPage * kHeadDim * 2;
+  const int ng = kHeadDim / (is_bf16(c) ? kHeadDim : c->cfg.group);
+  const long long page_bytes = is_bf16(c) ? 2LL * kPage * kHeadDim * 2
+                                          : 2LL * kPage * ((is_int4(c) ? kInt4Row : kRowBytes) + 4 * ng);
   long long total_bytes = 0;
   for (int i = 0; i < n_req; ++i) {
     np_of[i] = pages_needed(c, Ls[i], Hs[i]);
@@ -938,7 +1091,7 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
     const int r_wide = decode_resident_ctas(G, c->cfg.group, true, is_cm(c), c->n_sm);
     wide = r_wide > 0 && total_bytes <= kItemBytes * r_wide;
   }
-  if (!is_int2(c)) {  // BF16: the deeper row pipeline for steps that one wave holds
+  if (is_bf16(c)) {  // the deeper row pipeline for steps that one wave holds
     const int r_deep = bf16_decode_resident_ctas(G, true, c->n_sm);
     wide = r_deep > 0 && total_bytes <= kItemBytes * r_deep;
   }
@@ -968,13 +1121,14 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   };
   int chunk = max_split_pages;
   if (chunk == 0) {
-    int resident =
-        is_int2(c) ? decode_resident_ctas(G, c->cfg.group, wide, is_cm(c), c->n_sm) : bf16_decode_resident_ctas(G, wide, c->n_sm);
+    int resident = is_int2(c)   ? decode_resident_ctas(G, c->cfg.group, wide, is_cm(c), c->n_sm)
+                   : is_int4(c) ? int4_decode_resident_ctas(G, c->cfg.group, c->n_sm)
+                                : bf16_decode_resident_ctas(G, wide, c->n_sm);
     if (resident <= 0) resident = 2 * c->n_sm;
     if (total_bytes <= kItemBytes * resident) {
       // a fused append + decode launch runs the reservation's append tasks in the same wave
       const long long n_app_tasks =
-          c->reserved && !is_cm(c) ? (long long)c->app_items * Hkv * 2 * append_task_split(nw) : 0;
+          c->reserved && !is_cm(c) && !is_int4(c) ? (long long)c->app_items * Hkv * 2 * append_task_split(nw) : 0;
       const long long slots = std::max<long long>(1, resident - n_bf_items - n_app_tasks);
       chunk = int(std::max<long long>(4, (total_pages + slots - 1) / slots));
       while (chunk < max_np && count_items(chunk) + n_app_tasks > resident) ++chunk;
@@ -1190,7 +1344,7 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   g_launches = 0;
   oscar_status st = check_decode(c, layer, q, out, workspace, ws_bytes);
   if (st) return st;
-  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_attention needs the BF16 format");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_attention needs the BF16 format");
   int e = 0;
   // A captured decode is replayed under later plans, which may share.
   bool with_shared = c->dec_shared && c->dec_shared_items > 0;
@@ -1212,17 +1366,31 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* c, int layer, const void* 
   return OSCAR_OK;
 }
 
+oscar_status oscar_int4_decode_attention(oscar_cache* c, int layer, const void* q, void* out, void* workspace,
+                                         size_t ws_bytes, float* out_f32, void* stream) {
+  g_launches = 0;
+  oscar_status st = check_decode(c, layer, q, out, workspace, ws_bytes);
+  if (st) return st;
+  if (!is_int4(c)) return fail(OSCAR_ERR_STATE, "oscar_int4_decode_attention needs the INT4 format");
+  st = check_device(c);
+  if (st) return st;
+  const int e = launch_int4_decode(kernel_params(c), layer, q, out, out_f32, static_cast<uint8_t*>(workspace), c->ws, c->n_sm,
+                                   stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "int4 decode launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
 int oscar_weights_stride(const oscar_cache* c) {
-  if (!c || is_int2(c)) return 0;
+  if (!c || !is_bf16(c)) return 0;
   return kPage * std::min(c->cfg.max_pages_per_request, c->cfg.max_pages);
 }
 
 size_t oscar_decode_weights_workspace_bytes(const oscar_cache* c) {
-  return c && c->planned && !is_int2(c) ? weights_workspace(c, size_t(c->dec_tokens)).total : 0;
+  return c && c->planned && is_bf16(c) ? weights_workspace(c, size_t(c->dec_tokens)).total : 0;
 }
 
 size_t oscar_decode_weights_workspace_max_bytes(const oscar_cache* c) {
-  if (!c || is_int2(c)) return 0;
+  if (!c || !is_bf16(c)) return 0;
   return weights_workspace(c, size_t(c->cfg.max_requests) * c->cfg.n_kv_heads * size_t(oscar_weights_stride(c))).total;
 }
 
@@ -1231,7 +1399,7 @@ oscar_status oscar_bf16_decode_weights(oscar_cache* c, int layer, const void* q,
                                        void* stream) {
   g_launches = 0;
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
-  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_weights needs the BF16 format");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "oscar_bf16_decode_weights needs the BF16 format");
   if (!c->planned) return fail(OSCAR_ERR_STATE, "no decode plan (plan after every append commit)");
   if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
   if (c->dec_shared)
@@ -1259,7 +1427,7 @@ oscar_status oscar_evict_begin(oscar_cache* c, const int* slots, const int* keep
                                void* stream) try {
   if (!c || !slots || !keep || n_req <= 0 || n_req > c->cfg.max_requests)
     return fail(OSCAR_ERR_INVALID_ARG, "bad evict arguments");
-  if (is_int2(c)) return fail(OSCAR_ERR_STATE, "eviction needs the BF16 format");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "eviction needs the BF16 format");
   if (c->reserved) return fail(OSCAR_ERR_STATE, "a reservation is pending");
   if (c->evicting) return fail(OSCAR_ERR_STATE, "an eviction is pending");
   if (n_sink < 0 || n_recent < 0) return fail(OSCAR_ERR_INVALID_ARG, "negative n_sink or n_recent");

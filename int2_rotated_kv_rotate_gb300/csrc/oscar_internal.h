@@ -245,6 +245,30 @@ struct RopeParams {
 // `aligned`: every row and head of every tensor starts on a 16-byte boundary.
 int launch_rope(const RopeParams& p, int dtype, bool aligned, int n_sm, void* stream, int* launches);
 
+// Appends with rotary positions and of 4-bit rows (append_rows.cu): bf16 rows of the pending
+// reservation, strides in elements; *_vec: rows and heads start on 16-byte boundaries.  The last
+// field is the launcher's.
+struct AppendRowsParams {
+  RopeTensor q;  // n_heads 0: none
+  const void *k, *v;
+  long long k_row, k_head, v_row, v_head;
+  const uint64_t* steps;
+  const void* positions;  // null: the tokens' places in their requests
+  int rotary_dim;
+  float magnitude;
+  bool interleaved, positions64;
+  bool q_in_vec, q_out_vec, k_vec, v_vec;
+  int chunk_heads;
+};
+int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bool int4, bool rope, int n_items, void* stream,
+                       int* launches);
+int launch_int4_read(const KernelParams& kp, int layer, int slot, int begin, int end, void* k_out, void* v_out, bool f32,
+                     int n_sm, void* stream, int* launches);
+// Decode over 4-bit pages (int4.cu).
+int launch_int4_decode(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* ws,
+                       const DecodeWorkspace& wl, int n_sm, void* stream, int* launches);
+int int4_decode_resident_ctas(int gqa, int group, int n_sm);
+
 // Decode with the library's own fixed device scratch instead of a caller workspace
 // (decode.cu).  Returns a cudaError_t as int; `too_big` is set when the plan's workspace
 // exceeds static_scratch_bytes().
