@@ -297,6 +297,33 @@ oscar_status oscar_int4_read(oscar_cache* cache, int layer, int slot, int begin,
 oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const void* q, void* out, void* workspace,
                                          size_t ws_bytes, float* out_f32, void* stream);
 
+/* Attention within a sliding window and over the first tokens (format OSCAR_FORMAT_BF16), for one
+ * or many of each request's last tokens: decode steps, prompts and chunks of them, drafted tokens.
+ * The query at position p (its token's place in the request) attends the tokens t <= p with
+ * t < n_sink or t > p - window; window 0: all t <= p.
+ *
+ * oscar_plan_window (host): the queries are the last n_queries[i] tokens (0 .. L; NULL: one each)
+ * of request slots[i] [host, n_req distinct], a pending reservation's tokens counted; uploads the
+ * plan on `stream`.  It stands beside the decode plan, so that layers with and without a window
+ * take turns, serves every layer, and ends as that one does (the next window plan, reservation
+ * or append commit).  oscar_plan_window_info: work items of the single queries, those of the others
+ * (tiles of 256 / G queries and a kv-head, or parts of them), and how many tiles were cut.
+ * oscar_window_attention (device, per layer): out = softmax(q K^T / sqrt(d)) V over what each query
+ * attends.  q, out [dev] bf16 [sum n_queries][H_q][d], requests in plan order, out_f32 nullable
+ * (before the rounding); all 16-byte aligned.  workspace [dev], 256-byte aligned, of
+ * oscar_window_workspace_bytes for the current plan, _max_bytes for every plan (as captured
+ * launches need it, which may be replayed under any later plan).  Values of tokens that no
+ * query attends are not used, and infinities and NaN reach only queries that attend them.  With
+ * several queries a request, weights enter the product with the values as bf16; values below 2^95.
+ * The current device must be the cache's. */
+oscar_status oscar_plan_window(oscar_cache* cache, const int* slots, const int* n_queries, int n_req, int n_sink,
+                               int window, void* stream);
+oscar_status oscar_plan_window_info(const oscar_cache* cache, int* n_row_items, int* n_tiles, int* n_cut);
+size_t oscar_window_workspace_bytes(const oscar_cache* cache);
+size_t oscar_window_workspace_max_bytes(const oscar_cache* cache);
+oscar_status oscar_window_attention(oscar_cache* cache, int layer, const void* q, void* out, void* workspace,
+                                    size_t ws_bytes, float* out_f32, void* stream);
+
 /* Accumulated attention weights (format OSCAR_FORMAT_BF16).  A row of weights is
  * oscar_weights_stride tokens, 64 * min(max_pages_per_request, max_pages); a buffer of one
  * layer is fp32 [max_requests][H_kv][stride] [dev], indexed by request slot and position and

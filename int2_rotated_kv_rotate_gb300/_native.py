@@ -73,6 +73,8 @@ EXPORTS = [
     "oscar_decode_weights_workspace_max_bytes", "oscar_bf16_decode_weights", "oscar_evict_begin", "oscar_evict",
     "oscar_evict_pages", "oscar_evict_commit", "oscar_evict_cancel",
     "oscar_append_rotated", "oscar_int4_append", "oscar_int4_read", "oscar_int4_decode_attention",
+    "oscar_plan_window", "oscar_plan_window_info", "oscar_window_workspace_bytes", "oscar_window_workspace_max_bytes",
+    "oscar_window_attention",
     "oscar_set_wait_limit", "oscar_inject_fault", "oscar_get_status",
     "oscar_last_error", "oscar_last_launch_count",
 ]
@@ -138,6 +140,11 @@ def lib() -> ctypes.CDLL:
                 "oscar_int4_append": (I, [P, I, P, P, P]),
                 "oscar_int4_read": (I, [P, I, I, I, I, P, P, I, P]),
                 "oscar_int4_decode_attention": (I, [P, I, P, P, P, S, P, P]),
+                "oscar_plan_window": (I, [P, IP, IP, I, I, I, P]),
+                "oscar_plan_window_info": (I, [P, IP, IP, IP]),
+                "oscar_window_workspace_bytes": (S, [P]),
+                "oscar_window_workspace_max_bytes": (S, [P]),
+                "oscar_window_attention": (I, [P, I, P, P, P, S, P, P]),
                 "oscar_set_wait_limit": (I, [P, ctypes.c_uint32]),
                 "oscar_inject_fault": (I, [P, ctypes.c_uint32]),
                 "oscar_get_status": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -476,3 +483,32 @@ def oscar_int4_read(handle: int, layer: int, slot: int, begin: int, end: int, k_
 def oscar_int4_decode_attention(handle: int, layer: int, q, out, workspace, out_f32=None, stream=None) -> None:
     _check(lib().oscar_int4_decode_attention(handle, layer, _ptr(q), _ptr(out), _ptr(workspace), workspace.numel(),
                                              _ptr(out_f32), _stream(stream)))
+
+
+def oscar_plan_window(handle: int, slots, n_queries=None, n_sink: int = 0, window: int = 0, stream=None) -> None:
+    s, n = _ints(slots)
+    m = None
+    if n_queries is not None:
+        m, n2 = _ints(n_queries)
+        assert n == n2
+    _check(lib().oscar_plan_window(handle, s, m, n, n_sink, window, _stream(stream)))
+
+
+def oscar_plan_window_info(handle: int):
+    """(work items of single queries, tiles or parts of the others, tiles that were cut)."""
+    a, b, c = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    _check(lib().oscar_plan_window_info(handle, ctypes.byref(a), ctypes.byref(b), ctypes.byref(c)))
+    return a.value, b.value, c.value
+
+
+def oscar_window_workspace_bytes(handle: int) -> int:
+    return lib().oscar_window_workspace_bytes(handle)
+
+
+def oscar_window_workspace_max_bytes(handle: int) -> int:
+    return lib().oscar_window_workspace_max_bytes(handle)
+
+
+def oscar_window_attention(handle: int, layer: int, q, out, workspace, out_f32=None, stream=None) -> None:
+    _check(lib().oscar_window_attention(handle, layer, _ptr(q), _ptr(out), _ptr(workspace), workspace.numel(), _ptr(out_f32),
+                                        _stream(stream)))

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liboscar.so")
 SOURCES = ["oscar_host.cpp", "append.cu", "decode.cu", "bf16.cu", "calib.cu", "rope.cu", "evict.cu", "shared.cu",
-           "append_rows.cu", "int4.cu"]
+           "append_rows.cu", "int4.cu", "window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -26,6 +26,8 @@ class KVCache:
         self.handle = N.oscar_cache_create(self.cfg, self.mem, self.nbytes)
         self.layout = N.oscar_cache_layout(self.handle)
         self.workspace = None
+        self.window_workspace = None
+        self._n_window = None  # queries of the current window plan
         self.weights_workspace = None
         self._weights_full = N.oscar_decode_weights_workspace_max_bytes(self.handle)  # bytes of it for every plan
         self._weights_need = 0  # and for the current one
@@ -192,8 +194,8 @@ class KVCache:
         """(work items, pages) that the plan attends once for several requests."""
         return N.oscar_plan_shared_info(self.handle)
 
-    def _check_decode(self, q, out, out_f32, stream):
-        shape = (self._n_plan, self.cfg.n_q_heads, self.cfg.head_dim)
+    def _check_decode(self, q, out, out_f32, stream, rows=None):
+        shape = (self._n_plan if rows is None else rows, self.cfg.n_q_heads, self.cfg.head_dim)
         if tuple(q.shape) != shape or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.device != self.mem.device:
             raise ValueError(f"q must be contiguous bf16 {shape} on {self.mem.device}")
         if out is None:
@@ -218,6 +220,38 @@ class KVCache:
             N.oscar_int4_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
         else:
             N.oscar_bf16_decode_attention(self.handle, layer, q, out, self.workspace, out_f32, stream)
+        return out
+
+    # ------------------------------------------------------------------ sliding window and sinks (BF16 format)
+    def plan_window(self, slots, n_queries=None, *, n_sink: int = 0, window: int = 0, stream=None) -> int:
+        """Plan attention of the last n_queries[i] tokens (one each by default) of request slots[i]: each
+        query attends the first n_sink tokens and the last `window` up to its own (0: all of them).
+        Stands beside the decode plan.  The number of queries."""
+        slots = list(slots)
+        n_queries = None if n_queries is None else [int(n) for n in n_queries]
+        if n_queries is not None and len(n_queries) != len(slots):
+            raise ValueError("n_queries must have an entry for every slot")
+        N.oscar_plan_window(self.handle, slots, n_queries, n_sink, window, stream)
+        self._n_window = len(slots) if n_queries is None else sum(n_queries)
+        if self.window_workspace is None:
+            # sized for every plan of the cache, once: launches captured into a graph keep
+            # this pointer across later plans
+            with N.on_stream(stream):
+                self.window_workspace = torch.empty(N.oscar_window_workspace_max_bytes(self.handle), dtype=torch.uint8,
+                                                    device=self.device)
+        return self._n_window
+
+    def window_info(self):
+        """(work items of single queries, tiles or parts of the others, tiles that were cut into parts)."""
+        return N.oscar_plan_window_info(self.handle)
+
+    def attend_window(self, layer: int, q, out=None, out_f32=None, stream=None):
+        """Attention of the window plan's queries, bf16 [queries, H_q, 128] in plan order."""
+        if self._n_window is None:
+            raise ValueError("no window plan")
+        out = self._check_decode(q, out, out_f32, stream, self._n_window)
+        if self._n_window:
+            N.oscar_window_attention(self.handle, layer, q, out, self.window_workspace, out_f32, stream)
         return out
 
     # ------------------------------------------------------------------ accumulated weights (BF16 format)

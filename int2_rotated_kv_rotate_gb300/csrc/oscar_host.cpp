@@ -51,6 +51,8 @@ size_t score_base_offset(size_t reqs) { return 256 + align256(reqs * sizeof(Deco
 size_t decode_items_offset(size_t reqs) { return score_base_offset(reqs) + align256(reqs * 8); }
 // offset of the items behind the order of a plan's shared runs
 size_t shared_items_offset(size_t reqs) { return align256(reqs * 4); }
+// offset of the lists behind the requests of a window plan
+size_t window_lists_offset(size_t reqs) { return 256 + align256(reqs * sizeof(WindowReq)); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kAppendChunk = 16;     // tokens (or ring slots) per append work item
@@ -70,6 +72,9 @@ constexpr int kSharedItemPages = 16;  // an item's fixed time in the shared laun
 constexpr double kSharedLaunchBytes = 8e6, kSharedSlotBytes = 1e6, kSharedRowBytes = 40e6 / 128;
 constexpr double kSharedPrivateBytes = 30e6, kSharedPrivateWeight = 2.5;
 constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages is none by itself: its members attend them, or their own runs do
+constexpr int kMaxWindowRowItems = 4096;  // row items of a window plan, beside one per request and kv-head
+constexpr int kMaxWindowTiles = 65536;
+constexpr int kWindowItemSteps = 3;  // an item's fixed time in the tile kernel, in steps
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
 bool config_ok(const oscar_config* c, std::string* why) {
@@ -150,6 +155,11 @@ DeviceLayout compute_layout(const oscar_config& c) {
     L.bf16_pages = take(layers * L.bf16_layer_stride);
     L.evict_plan = take(256 + reqs * sizeof(EvictReq));
     L.evict_pages = take(reqs * size_t(c.max_pages_per_request) * 4);
+    L.max_window_rows = reqs * Hkv + kMaxWindowRowItems;
+    L.max_window_tiles = kMaxWindowTiles;
+    L.window_plan_bytes = window_lists_offset(reqs) + align256(L.max_window_rows * sizeof(DecodeItem)) +
+                          align256(L.max_window_tiles * sizeof(WindowTile)) + align256(kWindowSlots * sizeof(WindowMerge));
+    L.window_plan = take(L.window_plan_bytes);
   }
   L.page_table = take(reqs * size_t(c.max_pages_per_request) * 4);
   L.status = take(256);
@@ -221,6 +231,11 @@ struct oscar_cache {
   bool dec_shared = false;  // OSCAR_PLAN_SHARED_PREFIX: the shared launch goes before the decode's
   int dec_shared_items = 0, dec_shared_pages = 0;
   bool map_ready = false;
+  // window plan (BF16 format)
+  bool win_planned = false, win_with_reservation = false;
+  int win_row_items = 0, win_tiles = 0, win_merges = 0;
+  bool win_deep = false;
+  WindowWorkspace win_ws{};
   alignas(64) unsigned char page_map[128];  // tensor map of the BF16 page pool
   int dec_n_req = 0, dec_items = 0, dec_bf16_items = 0, dec_max_pages = 0;
   long long dec_tokens = 0;  // of all kv-heads
@@ -457,6 +472,28 @@ SharedRuns find_shared_runs(const oscar_cache* c, const int* slots, const std::v
   return out;
 }
 
+// The tensor map of the BF16 page pool, on first use.
+oscar_status make_page_map(oscar_cache* c, const char* what) {
+  if (c->map_ready) return OSCAR_OK;
+  const unsigned long long rows = 2ull * kPage * c->cfg.n_layers * c->cfg.max_pages * c->cfg.n_kv_heads;
+  if (rows > 0x7fffffffull) return fail(OSCAR_ERR_UNSUPPORTED, "%s: a pool of %llu rows is too large", what, rows);
+  const int e = encode_page_map(kernel_params(c), c->page_map);
+  if (e) return fail(OSCAR_ERR_CUDA, "tensor map of the page pool: %s", cudaGetErrorString(cudaError_t(e)));
+  c->map_ready = true;
+  return OSCAR_OK;
+}
+
+// Workspace of windowed attention with room for `slots` parts of cut tiles.  Only the total depends
+// on the plan: a captured launch keeps its offsets.
+WindowWorkspace window_workspace(const oscar_cache* c, size_t slots) {
+  const size_t G = size_t(c->cfg.n_q_heads / c->cfg.n_kv_heads);
+  WindowWorkspace w;
+  w.rows = 0;
+  w.tiles = align256(c->lay.max_window_rows * G * (8 + 4 * kHeadDim));
+  w.total = w.tiles + slots * kWindowSlotBytes;
+  return w;
+}
+
 // Workspace of a decode with weights over `tokens` tokens of all kv-heads.  Only the total
 // depends on the plan: a captured launch keeps its offsets.
 WeightsWorkspace weights_workspace(const oscar_cache* c, size_t tokens) {
@@ -513,12 +550,14 @@ oscar_status oscar_cache_create(const oscar_config* cfg, void* device_mem, size_
                               decode_items_offset(cfg->max_requests) + lay.max_decode_items * sizeof(DecodeItem));
   if (cfg->format == OSCAR_FORMAT_BF16)  // a plan's shared runs go up behind its items
     c->staging_bytes += 256 + shared_items_offset(cfg->max_requests) + lay.max_shared_items * sizeof(SharedItem);
+  c->staging_bytes = std::max(c->staging_bytes, lay.window_plan_bytes);
   c->upload_bytes = align256(pt_bytes) + align256(c->staging_bytes);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&c->h_page_table), pt_bytes);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&c->h_upload), kUploadSlots * c->upload_bytes);
   if (e == cudaSuccess) e = cudaMallocHost(reinterpret_cast<void**>(&c->h_status), 256);
   if (e == cudaSuccess) e = cudaMemset(c->base + lay.append_counts, 0, 16);
   if (e == cudaSuccess) e = cudaMemset(c->base + lay.decode_counts, 0, 16);
+  if (e == cudaSuccess && is_bf16(c)) e = cudaMemset(c->base + lay.window_plan, 0, 256);
   for (int i = 0; i < kUploadSlots && e == cudaSuccess; ++i)
     e = cudaEventCreateWithFlags(&c->upload_done[i], cudaEventDisableTiming);
   if (e == cudaSuccess) {
@@ -629,7 +668,7 @@ oscar_status oscar_request_free(oscar_cache* c, int slot) {
   std::fill(c->h_page_table + size_t(slot) * c->cfg.max_pages_per_request,
             c->h_page_table + size_t(slot + 1) * c->cfg.max_pages_per_request, -1);
   r = Request();
-  c->planned = false;
+  c->planned = c->win_planned = false;
   return OSCAR_OK;
 }
 
@@ -700,7 +739,7 @@ oscar_status oscar_request_share_prefix(oscar_cache* c, int dst, int src, int n_
   }
   st = end_upload(c, u, strm);
   if (st) return st;
-  c->planned = false;
+  c->planned = c->win_planned = false;
   return OSCAR_OK;
 }
 
@@ -802,8 +841,8 @@ oscar_status oscar_reserve(oscar_cache* c, const int* slots, const int* n_new, i
   c->app_items = int(items.size());
   c->app_rows = int(rows);
   c->reserved = true;
-  c->planned = false;  // lengths change: plan again (a plan made now counts the new tokens)
-  c->planned_with_reservation = false;
+  c->planned = c->win_planned = false;  // lengths change: plan again (a plan made now counts the new tokens)
+  c->planned_with_reservation = c->win_with_reservation = false;
   return OSCAR_OK;
 }
 
@@ -816,6 +855,8 @@ oscar_status oscar_commit_append(oscar_cache* c) {
   }
   c->reserved = false;
   if (!c->planned_with_reservation) c->planned = false;
+  if (!c->win_with_reservation) c->win_planned = false;
+  c->win_with_reservation = false;
   c->planned_with_reservation = false;
   c->plan_covers_reservation = false;
   return OSCAR_OK;
@@ -1036,14 +1077,8 @@ oscar_status oscar_plan_decode_ex(oscar_cache* c, const int* slots, int n_req, i
   }
   SharedRuns runs;
   if (shared) {
-    if (!c->map_ready) {
-      const unsigned long long rows = 2ull * kPage * c->cfg.n_layers * c->cfg.max_pages * Hkv;
-      if (rows > 0x7fffffffull)
-        return fail(OSCAR_ERR_UNSUPPORTED, "OSCAR_PLAN_SHARED_PREFIX: a pool of %llu rows is too large", rows);
-      const int e = encode_page_map(kernel_params(c), c->page_map);
-      if (e) return fail(OSCAR_ERR_CUDA, "tensor map of the page pool: %s", cudaGetErrorString(cudaError_t(e)));
-      c->map_ready = true;
-    }
+    oscar_status st = make_page_map(c, "OSCAR_PLAN_SHARED_PREFIX");
+    if (st) return st;
     runs = find_shared_runs(c, slots, Ls, (flags & OSCAR_PLAN_SHARED_ALWAYS) != 0);
   } else {
     runs.first_private.assign(n_req, 0);
@@ -1380,6 +1415,223 @@ oscar_status oscar_int4_decode_attention(oscar_cache* c, int layer, const void* 
   return OSCAR_OK;
 }
 
+oscar_status oscar_plan_window(oscar_cache* c, const int* slots, const int* n_queries, int n_req, int n_sink, int window,
+                               void* stream) try {
+  if (!c || !slots || n_req <= 0 || n_req > c->cfg.max_requests)
+    return fail(OSCAR_ERR_INVALID_ARG, "bad window plan arguments");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "windowed attention needs the BF16 format");
+  if (n_sink < 0 || window < 0) return fail(OSCAR_ERR_INVALID_ARG, "negative n_sink or window");
+  std::vector<char> seen(c->cfg.max_requests, 0);
+  const int Hkv = c->cfg.n_kv_heads, G = c->cfg.n_q_heads / Hkv;
+  std::vector<WindowReq> reqs(n_req);
+  long long rows = 0, list_tokens = 0;
+  int longest_list = 0;
+  for (int i = 0; i < n_req; ++i) {
+    oscar_status st = check_slot(c, slots[i]);
+    if (st) return st;
+    if (seen[slots[i]]) return fail(OSCAR_ERR_INVALID_ARG, "slot %d listed twice", slots[i]);
+    seen[slots[i]] = 1;
+    WindowReq& r = reqs[i];
+    int L_pre = c->reqs[slots[i]].L;
+    r.slot = slots[i];
+    r.L = L_pre;
+    if (c->reserved)  // a pending reservation's tokens count
+      for (const AppendReq& a : c->app_reqs)
+        if (a.slot == slots[i]) r.L = a.L1;
+    r.n = n_queries ? n_queries[i] : 1;
+    if (r.n < 0 || r.n > r.L) return fail(OSCAR_ERR_INVALID_ARG, "slot %d: %d queries of %d tokens", slots[i], r.n, r.L);
+    r.first = r.L - r.n;
+    r.row = int(rows);
+    rows += r.n;
+    if (rows > (1 << 30)) return fail(OSCAR_ERR_INVALID_ARG, "too many queries");
+    r.n_sink = std::min(n_sink, r.L);
+    r.window = window >= r.L ? 0 : window;  // (0: everything before)
+    const int start = r.window && r.first >= r.window ? r.first - r.window + 1 : 0;
+    r.sinks = std::min(r.n_sink, start);
+    r.skip = start - r.sinks;
+    r.u_pre = std::min(r.sinks, L_pre) + std::max(0, L_pre - start);
+    if (r.n == 1) {
+      list_tokens += (long long)Hkv * (r.L - r.skip);
+      longest_list = std::max(longest_list, r.L - r.skip);
+    }
+  }
+  // ---- one query a request: the list's tokens, cut as the decode's pages are
+  constexpr long long kItemTokens = (512 << 10) / (2 * kHeadDim * 2), kWaves = 2;
+  const int r_deep = window_rows_resident_ctas(G, true, c->n_sm);
+  const bool deep = r_deep > 0 && list_tokens <= kItemTokens * r_deep;
+  int resident = window_rows_resident_ctas(G, deep, c->n_sm);
+  if (resident <= 0) resident = 2 * c->n_sm;
+  auto count_items = [&](int chunk) {
+    long long n = 0;
+    for (const WindowReq& r : reqs)
+      if (r.n == 1) n += (long long)Hkv * ceil_div(r.L - r.skip, chunk);
+    return n;
+  };
+  int chunk = 2 * kPage;
+  if (list_tokens <= kItemTokens * resident) {
+    while (chunk < longest_list && count_items(chunk) > resident) chunk += kPage;
+  } else {
+    chunk = int(std::max(kItemTokens, list_tokens / (kWaves * resident)) / kPage * kPage);
+  }
+  while (count_items(chunk) > (long long)c->lay.max_window_rows) chunk += chunk / 4 / kPage * kPage + kPage;
+  std::vector<DecodeItem> items;
+  for (int i = 0; i < n_req; ++i) {
+    const WindowReq& r = reqs[i];
+    if (r.n != 1) continue;
+    const int len = r.L - r.skip, n = ceil_div(len, chunk);
+    for (int h = 0; h < Hkv; ++h) {
+      const int first = int(items.size());
+      for (int k = 0; k < n; ++k)
+        items.push_back({i, h, 0, k * chunk, std::min(len, (k + 1) * chunk), first, n, kDepNone, 0, first + k});
+    }
+  }
+  std::stable_sort(items.begin(), items.end(), [](const DecodeItem& a, const DecodeItem& b) { return a.end - a.begin > b.end - b.begin; });
+  // ---- several: tiles, and their steps cut into parts where that ends the launch sooner
+  const int per_tile = kWindowRows / G;
+  std::vector<WindowTile> whole;
+  long long n_tiles = 0, total_steps = 0;
+  int longest = 0;
+  for (const WindowReq& r : reqs)
+    if (r.n > 1) n_tiles += (long long)Hkv * ceil_div(r.n, per_tile);
+  if (n_tiles > (long long)c->lay.max_window_tiles)
+    return fail(OSCAR_ERR_INVALID_ARG, "%lld tiles of queries exceed %zu; plan fewer queries", n_tiles, c->lay.max_window_tiles);
+  whole.reserve(size_t(n_tiles));
+  for (int i = 0; i < n_req; ++i) {
+    const WindowReq& r = reqs[i];
+    if (r.n < 2) continue;
+    for (int h = 0; h < Hkv; ++h)
+      for (int t = 0; t < r.n; t += per_tile) {
+        const int n = std::min(per_tile, r.n - t);
+        const int steps = ceil_div(window_pages(r.first + t, n, r.n_sink, r.window).pages, 2);
+        whole.push_back({i, h, t, n, 0, steps, -1});
+        total_steps += steps;
+        longest = std::max(longest, steps);
+      }
+  }
+  int cap = longest;
+  if (!whole.empty()) {
+    // a launch lasts as long as its longest item, or as all of them over the SMs; parts add an
+    // item's fixed time each, and the merge
+    double best = -1;
+    for (int k = 1; k <= std::min(longest, 64); ++k) {
+      const int ch = ceil_div(longest, k);
+      long long n = 0, cut = 0;
+      for (const WindowTile& t : whole) {
+        const int m = ceil_div(t.end, ch);
+        n += m;
+        cut += m > 1 ? m : 0;
+      }
+      if (cut > kWindowSlots || n > (long long)c->lay.max_window_tiles) break;
+      const double rounds = double((n + c->n_sm - 1) / c->n_sm);
+      const double even = double(total_steps + kWindowItemSteps * n) / c->n_sm;
+      const double cost = std::max(even, std::min(rounds * (ch + kWindowItemSteps), even + ch)) + (k > 1 ? 4.0 + 0.02 * double(cut) : 0.0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        cap = ch;
+      }
+    }
+  }
+  std::vector<WindowTile> tiles;
+  std::vector<WindowMerge> merges;
+  tiles.reserve(whole.size());
+  int n_slots = 0;
+  for (const WindowTile& t : whole) {
+    const int m = ceil_div(t.end, cap);
+    if (m < 2) {
+      tiles.push_back(t);
+      continue;
+    }
+    merges.push_back({t.req, t.kvh, t.tok0, t.n_tok, n_slots, m});
+    for (int k = 0; k < m; ++k)  // as even as whole steps allow
+      tiles.push_back({t.req, t.kvh, t.tok0, t.n_tok, int((long long)t.end * k / m), int((long long)t.end * (k + 1) / m), n_slots++});
+  }
+  std::stable_sort(tiles.begin(), tiles.end(), [](const WindowTile& a, const WindowTile& b) { return a.end - a.begin > b.end - b.begin; });
+  if (!tiles.empty()) {
+    oscar_status st = make_page_map(c, "several queries a request");
+    if (st) return st;
+  } else if (!c->map_ready) {
+    make_page_map(c, "");  // for launches that are captured; without one they serve single queries
+  }
+  Upload u;
+  oscar_status st = begin_upload(c, &u);
+  if (st) return st;
+  const size_t rows_off = window_lists_offset(c->cfg.max_requests);
+  const size_t tiles_off = rows_off + align256(items.size() * sizeof(DecodeItem));
+  const size_t merges_off = tiles_off + align256(tiles.size() * sizeof(WindowTile));
+  int32_t* counts = reinterpret_cast<int32_t*>(u.staging);
+  counts[0] = int(items.size());
+  counts[1] = int(tiles.size());
+  counts[2] = int(merges.size());
+  counts[3] = 0;
+  counts[4] = int(rows_off);
+  counts[5] = int(tiles_off);
+  counts[6] = int(merges_off);
+  counts[7] = 0;
+  std::memcpy(u.staging + 256, reqs.data(), reqs.size() * sizeof(WindowReq));
+  if (!items.empty()) std::memcpy(u.staging + rows_off, items.data(), items.size() * sizeof(DecodeItem));
+  if (!tiles.empty()) std::memcpy(u.staging + tiles_off, tiles.data(), tiles.size() * sizeof(WindowTile));
+  if (!merges.empty()) std::memcpy(u.staging + merges_off, merges.data(), merges.size() * sizeof(WindowMerge));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.window_plan, u.staging, merges_off + merges.size() * sizeof(WindowMerge),
+                           cudaMemcpyHostToDevice, s));
+  st = end_upload(c, u, s);
+  if (st) return st;
+  c->win_planned = true;
+  c->win_with_reservation = c->reserved;
+  c->win_row_items = int(items.size());
+  c->win_tiles = int(tiles.size());
+  c->win_merges = int(merges.size());
+  c->win_deep = deep;
+  c->win_ws = window_workspace(c, size_t(n_slots));
+  return OSCAR_OK;
+} catch (const std::bad_alloc&) {
+  return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed");
+}
+
+oscar_status oscar_plan_window_info(const oscar_cache* c, int* n_row_items, int* n_tiles, int* n_cut) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->win_planned) return fail(OSCAR_ERR_STATE, "no window plan");
+  if (n_row_items) *n_row_items = c->win_row_items;
+  if (n_tiles) *n_tiles = c->win_tiles;
+  if (n_cut) *n_cut = c->win_merges;
+  return OSCAR_OK;
+}
+
+size_t oscar_window_workspace_bytes(const oscar_cache* c) { return c && c->win_planned ? c->win_ws.total : 0; }
+
+size_t oscar_window_workspace_max_bytes(const oscar_cache* c) {
+  return c && is_bf16(c) ? window_workspace(c, kWindowSlots).total : 0;
+}
+
+oscar_status oscar_window_attention(oscar_cache* c, int layer, const void* q, void* out, void* workspace, size_t ws_bytes,
+                                    float* out_f32, void* stream) {
+  g_launches = 0;
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (!is_bf16(c)) return fail(OSCAR_ERR_STATE, "windowed attention needs the BF16 format");
+  if (!c->win_planned) return fail(OSCAR_ERR_STATE, "no window plan (plan after every append commit)");
+  if (layer < 0 || layer >= c->cfg.n_layers) return fail(OSCAR_ERR_INVALID_ARG, "layer %d out of range", layer);
+  bool rows = c->win_row_items > 0, tiles = c->win_tiles > 0, merges = c->win_merges > 0;
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  CUDA_TRY(cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capturing));
+  if (capturing != cudaStreamCaptureStatusNone) {  // a captured launch is replayed under later plans
+    rows = true;
+    tiles = merges = c->map_ready;
+  }
+  if (!rows && !tiles) return OSCAR_OK;  // no queries
+  if (!q || !out || !workspace) return fail(OSCAR_ERR_INVALID_ARG, "NULL q, out or workspace");
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(out_f32)) % 16)
+    return fail(OSCAR_ERR_INVALID_ARG, "q, out and out_f32 must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(OSCAR_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const size_t need = capturing != cudaStreamCaptureStatusNone ? oscar_window_workspace_max_bytes(c) : c->win_ws.total;
+  if (ws_bytes < need) return fail(OSCAR_ERR_INVALID_ARG, "workspace %zu < %zu bytes", ws_bytes, need);
+  oscar_status st = check_device(c);
+  if (st) return st;
+  const int e = launch_window(kernel_params(c), layer, c->page_map, q, out, out_f32, static_cast<uint8_t*>(workspace), c->win_ws, rows,
+                              c->win_deep, tiles, merges, c->n_sm, stream, &g_launches);
+  if (e) return fail(OSCAR_ERR_CUDA, "window launch: %s", cudaGetErrorString(cudaError_t(e)));
+  return OSCAR_OK;
+}
+
 int oscar_weights_stride(const oscar_cache* c) {
   if (!c || !is_bf16(c)) return 0;
   return kPage * std::min(c->cfg.max_pages_per_request, c->cfg.max_pages);
@@ -1554,7 +1806,7 @@ oscar_status oscar_evict_commit(oscar_cache* c, void* stream) try {
   c->evicting = false;
   c->ev_reqs.clear();
   c->ev_pages.clear();
-  if (!changed.empty()) c->planned = false;  // lengths changed: plan again
+  if (!changed.empty()) c->planned = c->win_planned = false;  // lengths changed: plan again
   st = upload_rows(c, u, changed, static_cast<cudaStream_t>(stream));
   if (st) return st;
   return end_upload(c, u, static_cast<cudaStream_t>(stream));

@@ -105,6 +105,49 @@ struct EvictReq {
   int n_sink, n_recent;
 };
 
+// Windowed attention (BF16 format): one request of its plan, whose n queries are the tokens first ..
+// L - 1 and rows row .. of the call's q.  With one query, the tokens that it sees are a list: the
+// sinks, then position u + skip of list index u; the first u_pre of them are older than the step.
+struct WindowReq {
+  int slot, L;
+  int first, n, row;
+  int n_sink, window;
+  int sinks, skip, u_pre;
+};
+// One work item of the tile kernel: queries tok0 .. tok0 + n_tok - 1 of request req, the heads of
+// kvh, steps [begin, end) of the tile's list of pages (two a step); slot: where the part's results
+// go, -1 where it is the whole tile.  And a tile that was cut: parts first_slot ..
+constexpr int kWindowRows = 256;  // query rows (queries x G) of a tile at most
+constexpr size_t kWindowSlotBytes = kWindowRows * (8 + 4 * kHeadDim);  // (maximum, denominator), then rows
+constexpr int kWindowSlots = 608;  // parts of a plan at most
+struct WindowTile {
+  int req, kvh, tok0, n_tok, begin, end, slot;
+};
+struct WindowMerge {
+  int req, kvh, tok0, n_tok, first_slot, n_parts;
+};
+
+#ifdef __CUDACC__
+#define OSCAR_HOST_DEVICE_FN __host__ __device__ inline
+#else
+#define OSCAR_HOST_DEVICE_FN inline
+#endif
+// The pages that some query of n from position p on sees, in order: sink_pages from 0, then those
+// from window_page on, `pages` in all.
+struct WindowPages {
+  int sink_pages, window_page, pages;
+};
+OSCAR_HOST_DEVICE_FN WindowPages window_pages(int p, int n, int n_sink, int window) {
+  WindowPages w;
+  const int start = window > 0 && p >= window ? p - window + 1 : 0;  // the first token of the first query's window
+  const int sinks = n_sink < start ? n_sink : start;
+  w.sink_pages = (sinks + kPage - 1) / kPage;
+  w.window_page = start / kPage > w.sink_pages ? start / kPage : w.sink_pages;
+  const int last = (p + n - 1) / kPage;
+  w.pages = w.sink_pages + (last >= w.window_page ? last - w.window_page + 1 : 0);
+  return w;
+}
+
 struct DeviceLayout {
   // pools (byte offsets in the device block)
   size_t codes, sz, sink, ring, bf16_pages;
@@ -134,6 +177,10 @@ struct DeviceLayout {
   // BF16 format: the shared runs of the decode plan, uploaded as one block: int32
   // order[max_requests] (plan indices) and the items, whose number is decode counts [3]
   size_t shared_order, shared_items;
+  // BF16 format: the window plan, one block: int32 counts[8] at +0 (row items, tiles, cut tiles, 0,
+  // and the byte offsets of the three lists), WindowReq at +256, the lists behind them
+  size_t window_plan, window_plan_bytes;
+  size_t max_window_rows, max_window_tiles;
   // decode plan, in front of the items: int64 [max_requests], the tokens of all kv-heads of the
   // requests before each (where its scores begin in a decode with weights)
   size_t score_base;
@@ -206,6 +253,16 @@ int launch_shared(const KernelParams& kp, int layer, const void* map, const void
 // max_keep_pages: the longest request of the plan, and the most new pages of one.
 int launch_evict(const KernelParams& kp, int layer, const float* weights, float* weights_out, int* kept, int n_req,
                  int max_len, int max_keep_pages, int n_sm, void* stream, int* launches);
+
+// Windowed attention (window.cu): the launches that the plan has work for.  map as launch_shared's.
+struct WindowWorkspace {
+  size_t rows;   // partial slots of the row items
+  size_t tiles;  // kWindowSlotBytes a part
+  size_t total;
+};
+int launch_window(const KernelParams& kp, int layer, const void* map, const void* q, void* out, float* out_f32, uint8_t* ws,
+                  const WindowWorkspace& wl, bool rows, bool deep, bool tiles, bool merges, int n_sm, void* stream, int* launches);
+int window_rows_resident_ctas(int gqa, bool deep, int n_sm);
 
 // CTAs of the decode kernel of this shape that fit on the GPU at once (occupancy x SMs);
 // the planner sizes work items so that one wave holds them all.

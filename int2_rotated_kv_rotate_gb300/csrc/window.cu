@@ -1,0 +1,753 @@
+// Attention over the BF16 pages within a sliding window and over the first tokens (sinks): the
+// query at position p attends t <= p with t < n_sink or t > p - window (window 0: all t <= p).
+//
+// Requests with one query (a decode step): window_rows_kernel, the split-K decode of bf16.cu over
+// the list of visible tokens (the sinks, then the window), so that neither the bytes nor the values
+// of other tokens are touched.  HBM-bound, 512 bytes a visible token and kv-head.
+//
+// Requests with more (a prompt's chunk, drafted tokens): window_tile_kernel on the tcgen05 tensor
+// cores.  A tile is the G heads of a kv-head for 256 / G neighbouring queries, two blocks of 128
+// rows (row m: query m / G, head m % G), over the pages that any of them sees, 128 tokens (two pages,
+// not always neighbours) a step:
+//   S = Q K^T      M = 128 rows, N = 128 tokens, K = 128 channels, both from shared memory;
+//   P = 2^(S - m)  one thread a row, the step's whole row in registers;
+//   O += P V       M = 128, N = 128 channels, K = 128 tokens, P from tensor memory.
+// P is bf16 (8 bits, up to 2^-8 of each weight, at random): as V is bf16 the tensor core takes no
+// other type beside it, and a second product with P's lower half would be half as much work again;
+// its error is about that of the output's own rounding.  Maxima, denominators and O are fp32, and the
+// denominator is the sum of the weights before their rounding.  A row's reference m moves only
+// when a score exceeds it by more than kRaise (base 2), so O is rarely rescaled.
+//
+// Masks cost nothing in steps that every row of a block sees whole.  In the others (the window's
+// edge, the diagonal, the end) a row's visible tokens are 128 bits, and the step's values are looked
+// over first: an infinity or NaN in a row of values that is hidden from some row would turn that
+// row's 0 into NaN in the product, so it is replaced by 0 there, and added to the rows that do see
+// it when O is complete (weights are positive, so the sum is that infinity or NaN).
+//
+// Roles, as in the launch of shared prefixes: warp 0 copies pages (TMA, a ring of five stages of 32
+// KB, keys and values in turn), warp 1 issues the products of S and warp 2 those of O, warps 4-7 and
+// 8-11 are the softmax of the two blocks.  P of a step lies over its S, and S of the next is
+// computed when O of this one is: while a block is at its softmax the tensor core works for the other.
+// Where few tiles would leave SMs idle, the plan cuts their pages into parts, whose partial results
+// window_merge_kernel joins, in a fixed order.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "oscar_internal.h"
+#include "tmem.cuh"
+
+namespace oscar {
+namespace {
+
+__device__ __forceinline__ const int* plan_counts(const KernelParams& kp) {
+  return reinterpret_cast<const int*>(kp.base + kp.lay.window_plan);
+}
+__device__ __forceinline__ const WindowReq* plan_reqs(const KernelParams& kp) {
+  return reinterpret_cast<const WindowReq*>(kp.base + kp.lay.window_plan + 256);
+}
+
+// ---------------------------------------------------------------- one query a request
+template <int NBUF>
+constexpr int kRowsPerSM = NBUF == 3 ? 2 : 3;
+constexpr int kRowsSmem(int G, int nbuf) {
+  return (nbuf == 3 ? Bf16Rows<4, 3>::kSmemBytes : Bf16Rows<4, 2>::kSmemBytes) + G * kQRow * 4 + 32;  // + flags, barrier
+}
+template <int G, int NBUF>
+constexpr int kRowsSlabSlots = Bf16Rows<4, NBUF>::kSmemBytes / PartialSlot<G>::kBytes;
+
+template <int G, int NBUF>
+__global__ void __launch_bounds__(128, kRowsPerSM<NBUF>)
+    window_rows_kernel(KernelParams kp, int layer, const uint16_t* __restrict__ q, uint8_t* __restrict__ partials,
+                       uint16_t* __restrict__ out, float* __restrict__ out_f32) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem + Bf16Rows<4, NBUF>::kSmemBytes);
+  int* s_last = reinterpret_cast<int*>(smem + Bf16Rows<4, NBUF>::kSmemBytes + G * kQRow * 4);
+  int* s_next = s_last + 1;
+  uint64_t* slab_bar = reinterpret_cast<uint64_t*>(smem + Bf16Rows<4, NBUF>::kSmemBytes + G * kQRow * 4 + 16);
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(slab_bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  uint32_t slab_phase = 0;
+  const int* counts = plan_counts(kp);
+  const DecodeItem* items = reinterpret_cast<const DecodeItem*>(kp.base + kp.lay.window_plan + counts[4]);
+  const WorkQueue wq{reinterpret_cast<unsigned*>(kp.base + kp.lay.sched), counts[0], 0, counts[0]};
+  bool waited = false;
+  for (int ix = wq.first(); ix >= 0; ix = wq.next(s_next)) {
+    const DecodeItem it = items[ix];
+    const WindowReq wr = plan_reqs(kp)[it.req];
+    const size_t head0 = size_t(wr.row) * kp.n_q_heads + size_t(it.kvh) * G;
+    uint8_t* part = partials + size_t(it.slot) * PartialSlot<G>::kBytes;
+    const bool slot_ok = wr.slot >= 0 && wr.slot < kp.max_requests;
+    if (!slot_ok && threadIdx.x == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
+    const int u0 = it.begin, u1 = slot_ok ? it.end : it.begin;
+    const int* ptab =
+        reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(slot_ok ? wr.slot : 0) * kp.max_pages_per_request;
+    const uint8_t* head_base = kp.base + kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride +
+                               size_t(it.kvh) * kp.lay.bf16_head_stride;
+    // token u of the list: a sink or one of the window; a bad page id reads page 0 of the pool
+    // instead and raises the flag
+    auto row_of = [=](int u, int kv) -> const uint16_t* {
+      const int t = u < wr.sinks ? u : u + wr.skip, lp = t / kPage;
+      int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+      if (phys < 0 || phys >= kp.max_pages) {
+        flag(kp, OSCAR_FLAG_BAD_PAGE);
+        phys = 0;
+      }
+      return reinterpret_cast<const uint16_t*>(head_base + size_t(phys) * kp.lay.bf16_page_stride) +
+             size_t(kv * kPage + t % kPage) * kHeadDim;
+    };
+    auto rowK = [=](int u) { return row_of(u, 0); };
+    auto rowV = [=](int u) { return row_of(u, 1); };
+    int staged = 0;
+    if (!waited) {
+      // rows that no kernel of the step writes are copied before the wait on the preceding kernel
+      if (threadIdx.x < 2 * G) prefetch_l2(q + head0 * kHeadDim + 64 * threadIdx.x);
+      constexpr int kAheadTok = (NBUF > 1 ? NBUF - 1 : 1) * Bf16Rows<4, NBUF>::kChunk;
+      const int upto = min(min(u1, wr.u_pre), u0 + kAheadTok);
+      if (upto > u0) {
+        bf16_prestage<4, NBUF>(rowK, rowV, u0, upto, smem);
+        staged = upto - u0;
+      }
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+    for (int e = threadIdx.x; e < G * kHeadDim; e += 128) qs[(e / kHeadDim) * kQRow + e % kHeadDim] = bf16_f32(q[head0 * kHeadDim + e]);
+    __syncthreads();
+    auto nothing = [] {};
+    bf16_rows_mma<G, 4, NBUF, decltype(rowK), decltype(rowV), decltype(nothing), NoScores, true>(rowK, rowV, u0, u1, qs, part, smem,
+                                                                                                 staged, nothing);
+    MergeAcc<G, 128> acc;
+    if (merge_partial<G, 128>(kp, it, it.head_count, partials, acc, s_last, smem, kRowsSlabSlots<G, NBUF>, smem_u32(slab_bar),
+                              slab_phase, [] {})) {
+      const int c = threadIdx.x;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float r = acc.L[h] > 0.f ? acc.O[h] / acc.L[h] : 0.f;
+        out[(head0 + h) * kHeadDim + c] = bf16_rne(r);
+        if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = r;
+      }
+    }
+    fence_proxy_async();  // generic use of the buffers is over before later bulk copies
+  }
+  if (!waited) {  // no item: the launch still orders itself after the preceding kernel
+    pdl_wait();
+    pdl_trigger();
+  }
+  wq.leave();
+}
+
+// ---------------------------------------------------------------- several queries a request
+constexpr int kStages = 5;
+constexpr int kStep = 2 * kPage;                       // tokens of a step
+constexpr int kStageBytes = kStep * kHeadDim * 2;      // keys or values of a step
+constexpr int kHalf = kStageBytes / 2;                 // of 64 channels
+constexpr int kBlockRows = 128;
+constexpr int kQBlock = kBlockRows * kHeadDim * 2;
+constexpr int kThreads = 384;
+static_assert(kWindowRows == 2 * kBlockRows, "warps 4-7 and 8-11");
+
+struct Control {
+  // Stage s's completion n is its n-th filling (leaving).
+  uint64_t full[kStages], empty[kStages];
+  // Completion n is item n of those in which the block has rows.
+  uint64_t q_full[2];
+  // Completion n is step n of the block: S is written, P is written, O holds the steps up to n
+  // (and P and S are read).  Whoever waits for one waits for every step in order, and none gets two
+  // ahead.
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drain[2];
+  uint32_t tmem;
+  int abort;
+  int odd;  // an infinity or NaN was met among values that not every row of a tile sees (in any of the CTA's)
+};
+constexpr int kOffStages = 2 * kQBlock;
+constexpr int kOffControl = kOffStages + kStages * kStageBytes;
+constexpr int kTileSmem = kOffControl + int(sizeof(Control)) + 1024;  // + alignment to 1024
+static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
+
+// Tensor-memory columns of block b: S of 128 (P over its first 64), O of 128.
+constexpr uint32_t kBlockCols = 256, kColO = 128;
+
+constexpr float kRaise = 16.f;
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The n lowest bits (n in any range).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// Everything a role needs of an item: the list of pages is sink_pages pages from 0, then those
+// from window_page on; step i is list pages 2 i and 2 i + 1 (the last may have only one).
+struct Work {
+  WindowTile it;
+  WindowReq rq;
+  int rows, blocks, sink_pages, window_page, pages;
+  __device__ int page(int j) const { return j < sink_pages ? j : window_page + j - sink_pages; }
+  __device__ int steps() const { return it.end - it.begin; }
+  // Tokens of list page j that the query at position p sees.
+  __device__ uint64_t visible(int j, int p) const {
+    if (j >= pages) return 0;
+    const int t0 = page(j) * kPage;
+    const uint64_t upto = low_bits(p - t0 + 1);
+    if (rq.window == 0) return upto;
+    return upto & (~low_bits(p - rq.window - t0 + 1) | low_bits(rq.n_sink - t0));
+  }
+  // Whether every query from position p0 to p1 sees all of list page j.
+  __device__ bool whole(int j, int p0, int p1) const { return (visible(j, p0) & visible(j, p1)) == ~0ull; }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_tile_kernel(KernelParams kp, int layer, const __grid_constant__ CUtensorMap map, const uint16_t* __restrict__ q,
+                       uint8_t* __restrict__ parts, uint16_t* __restrict__ out, float* __restrict__ out_f32) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Control* ctl = reinterpret_cast<Control*>(smem + kOffControl);
+  const uint32_t sq = smem_u32(smem), sst = sq + kOffStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
+      mbar_init(smem_u32(&ctl->s_full[b]), 1);
+      mbar_init(smem_u32(&ctl->p_full[b]), kBlockRows);
+      mbar_init(smem_u32(&ctl->o_done[b]), 1);
+      mbar_init(smem_u32(&ctl->drain[b]), 1);
+    }
+    ctl->abort = ctl->odd = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem::alloc(smem_u32(&ctl->tmem), 512);
+  tmem::fence_before();
+  __syncthreads();
+  tmem::fence_after();
+  const uint32_t tm = ctl->tmem;
+  pdl_wait();
+  pdl_trigger();
+  const int* counts = plan_counts(kp);
+  const int n_items = counts[1], G = kp.gqa;
+  const WindowTile* items = reinterpret_cast<const WindowTile*>(kp.base + kp.lay.window_plan + counts[5]);
+  auto load_work = [&](int ix) {
+    Work w;
+    w.it = items[ix];
+    w.rq = plan_reqs(kp)[w.it.req];
+    w.rows = w.it.n_tok * G;
+    w.blocks = w.rows > kBlockRows ? 2 : 1;
+    const WindowPages p = window_pages(w.rq.first + w.it.tok0, w.it.n_tok, w.rq.n_sink, w.rq.window);
+    w.sink_pages = p.sink_pages;
+    w.window_page = p.window_page;
+    w.pages = p.pages;
+    return w;
+  };
+  // Bounded wait of a whole warp for completions of one or two barriers (index: of the
+  // completion); lane 0 polls the first, lane 1 the second.  Each lane has its own poll's result:
+  // the roles vote once a step, where the warp meets anyway, so after a wait that ran out MMAs and
+  // stores of that step still go out, on memory of this CTA, and every role then leaves its loop.
+  auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> int {
+    int done = 1;
+    if (lane < 2) {
+      const uint32_t a = lane ? smem_u32(&bar1) : smem_u32(&bar0), par = (lane ? index1 : index0) & 1u;
+      done = mbar_try_wait(a, par);
+      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+        done = mbar_try_wait_for(a, par, 1000000u);
+        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+      }
+      if (!done) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        flag(kp, OSCAR_FLAG_TIMEOUT);
+      }
+    }
+    __syncwarp();
+    return done;
+  };
+  auto wait = [&](uint64_t& bar, uint32_t index) -> int {
+    int done = 1;
+    if (lane == 0) {
+      const uint32_t a = smem_u32(&bar);
+      done = mbar_try_wait(a, index & 1u);
+      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+        done = mbar_try_wait_for(a, index & 1u, 1000000u);
+        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+      }
+      if (!done) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        flag(kp, OSCAR_FLAG_TIMEOUT);
+      }
+    }
+    __syncwarp();
+    return done;
+  };
+  auto all = [](int done) -> bool { return __all_sync(0xffffffffu, done); };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- pages
+    uint32_t n = 0, issued = 0;  // fillings of stages: keys and values of each step in turn
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
+      if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
+      const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
+                        size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+      for (int i = w.it.begin; ok && i < w.it.end; ++i) {
+        const int two = min(2, w.pages - 2 * i);
+        int y[2] = {0, 0};
+        for (int j = 0; j < two; ++j) {
+          const int lp = w.page(2 * i + j);
+          int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+          if (phys < 0 || phys >= kp.max_pages) {  // page 0 instead, and the flag
+            if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+            phys = 0;
+          }
+          y[j] = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
+        }
+        for (int kv = 0; ok && kv < 2; ++kv, ++n) {
+          const uint32_t st = n % kStages;
+          const int done = n >= kStages ? wait(ctl->empty[st], n / kStages - 1) : 1;
+          if (lane == 0 && done) {  // (lane 0 polled: no copy into a stage that was not left)
+            const uint32_t bar = smem_u32(&ctl->full[st]), dst = sst + st * kStageBytes;
+            mbar_expect_tx(bar, two * (kStageBytes / 2));
+            for (int j = 0; j < two; ++j) {
+              tma_load(dst + j * (kHalf / 2), &map, 0, y[j] + kv * kPage, bar);
+              tma_load(dst + kHalf + j * (kHalf / 2), &map, 64, y[j] + kv * kPage, bar);
+            }
+          }
+          if ((ok = all(done))) issued = n + 1;
+        }
+      }
+    }
+    // the last arrivals on the stages' barriers come before the CTA leaves
+    for (uint32_t k = n > kStages ? n - kStages : 0; ok && k < n; ++k) ok = all(wait(ctl->empty[k % kStages], k / kStages));
+    if (!ok)  // copies still in flight land first, too
+      for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+        mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S = Q K^T
+    constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kStep, false);
+    const uint64_t qd = tmem::sdesc_sw128(sq, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
+    uint32_t n = 0, q0 = 0, q1 = 0, n0 = 0, n1 = 0;  // stages; items and steps of each block
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      ok = all(wait(ctl->q_full[0], q0++));
+      if (ok && w.blocks > 1) ok = all(wait(ctl->q_full[1], q1++));
+      for (int i = 0; ok && i < w.steps(); ++i, n += 2) {
+        const uint32_t st = n % kStages;
+        for (int b = 0; ok && b < w.blocks; ++b) {
+          const uint32_t k = b ? n1++ : n0++;
+          int done = 1;
+          if (b == 0) done = k ? wait2(ctl->full[st], n / kStages, ctl->o_done[b], k - 1) : wait(ctl->full[st], n / kStages);
+          else if (k) done = wait(ctl->o_done[b], k - 1);
+          tmem::fence_after();
+          if (elect_one()) {
+            const uint32_t d = tm + b * kBlockCols;
+            const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kStageBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              tmem::mma_ss(d, qb + ((c >> 2) * (kQBlock / 2) + (c & 3) * 32) / 16, kb + ((c >> 2) * kHalf + (c & 3) * 32) / 16,
+                           kIdS, c > 0);
+            tmem::commit(smem_u32(&ctl->s_full[b]));
+            if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+          }
+          ok = all(done);
+        }
+      }
+    }
+    if (!ok) {  // MMAs in flight end before the tensor memory is freed
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[0]));
+      __syncwarp();
+      mbar_wait(smem_u32(&ctl->drain[0]), 0);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- O += P V
+    constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
+    const uint64_t vd = tmem::sdesc_sw128(sst, kHalf, 1024);
+    uint32_t n = 1, n0 = 0, n1 = 0;
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      for (int i = 0; ok && i < w.steps(); ++i, n += 2) {
+        const uint32_t st = n % kStages;
+        for (int b = 0; ok && b < w.blocks; ++b) {
+          const uint32_t k = b ? n1++ : n0++;
+          const int done = b == 0 ? wait2(ctl->full[st], n / kStages, ctl->p_full[b], k) : wait(ctl->p_full[b], k);
+          tmem::fence_after();
+          if (elect_one()) {
+            const uint32_t a = tm + b * kBlockCols, d = a + kColO;
+            const uint64_t vb = vd + st * (kStageBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, i > 0 || c > 0);
+            tmem::commit(smem_u32(&ctl->o_done[b]));
+            if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+          }
+          ok = all(done);
+        }
+      }
+    }
+    if (!ok) {
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[1]));
+      __syncwarp();
+      mbar_wait(smem_u32(&ctl->drain[1]), 0);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax of block b
+    const int b = (warp - 4) >> 2, wq = warp & 3, r = (wq << 5) | lane;
+    const float scale = kLog2e * rsqrtf(float(kHeadDim));
+    const uint32_t tl = tm + b * kBlockCols + (uint32_t(32 * wq) << 16);
+    uint32_t n = 0, nv = 1;  // steps of this block; fillings up to the item's first values
+    bool ok = true;
+    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+      const Work w = load_work(ix);
+      const int steps = w.steps();
+      if (b >= w.blocks) {
+        nv += 2 * steps;
+        continue;
+      }
+      const int m = b * kBlockRows + r;
+      const bool mine = m < w.rows;
+      // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
+      {
+        const long long row = mine ? (long long)(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + w.it.kvh * G + m % G : -1;
+        uint4 v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const long long src = __shfl_sync(0xffffffffu, row, 2 * k + (lane >> 4));
+          v[k] = src >= 0 ? reinterpret_cast<const uint4*>(q + size_t(src) * kHeadDim)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int rr = 32 * wq + 2 * k + (lane >> 4), c = lane & 15;
+          *reinterpret_cast<uint4*>(smem + b * kQBlock + (c >> 3) * (kQBlock / 2) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v[k];
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(smem_u32(&ctl->q_full[b]));
+      // positions of the block's first and last query and of this row's
+      const int p0 = w.rq.first + w.it.tok0 + b * kBlockRows / G;
+      const int p1 = w.rq.first + w.it.tok0 + min(w.it.n_tok, (b + 1) * kBlockRows / G) - 1;
+      const int pos = min(p0 + r / G, p1);
+      // Steps that some row of the tile does not see whole: both blocks look over their values
+      // (whoever comes first replaces what the other's product reads, too).
+      const int first_pos = w.rq.first + w.it.tok0, last_pos = first_pos + w.it.n_tok - 1;
+      auto looked = [&](int j0) { return !w.whole(j0, first_pos, last_pos) || !w.whole(j0 + 1, first_pos, last_pos); };
+      float m_ref = -INFINITY, l = 0.f;
+      const bool idle = b * kBlockRows + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
+      for (int i = 0; i < steps; ++i, ++n) {
+        const int j0 = 2 * (w.it.begin + i);
+        const bool masked = !w.whole(j0, p0, p1) || !w.whole(j0 + 1, p0, p1);
+        int done = wait(ctl->s_full[b], n);
+        if (looked(j0)) {
+          const uint32_t f = nv + 2 * i, st = f % kStages;
+          done &= wait(ctl->full[st], f / kStages);
+          uint4* at = reinterpret_cast<uint4*>(smem + kOffStages + st * kStageBytes) + r;
+#pragma unroll 4
+          for (int k = 0; k < kStageBytes / 16 / kBlockRows; ++k) {
+            uint4 v = at[k * kBlockRows];
+            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool lo = (x[e] & 0x7f80u) == 0x7f80u, hi = (x[e] & 0x7f800000u) == 0x7f800000u;
+              bad |= lo | hi;
+              x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+            }
+            if (bad) {  // (the flag first: the other block may find only the zeros)
+              *reinterpret_cast<volatile int*>(&ctl->odd) = 1;
+              __threadfence_block();
+              at[k * kBlockRows] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          fence_proxy_async();
+        }
+        if (idle) {
+          mbar_arrive(smem_u32(&ctl->p_full[b]));
+          if (!(ok = all(done))) break;
+          continue;
+        }
+        tmem::fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem::ld_x32(tl + 32 * c, s[c]);
+        tmem::wait_ld();
+        if (masked) {
+          const uint64_t see[2] = {w.visible(j0, pos), w.visible(j0 + 1, pos)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = uint32_t(see[c >> 1] >> (32 * (c & 1)));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((bits >> e) & 1u)) s[c][e] = 0xff800000u;  // -inf
+          }
+        }
+        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          mx = max3(mx, __uint_as_float(s[0][e]), __uint_as_float(s[1][e]));
+          my = max3(my, __uint_as_float(s[2][e]), __uint_as_float(s[3][e]));
+        }
+        mx = fmaxf(mx, my) * scale;
+        const bool raise = mx > m_ref + kRaise;  // also from -inf
+        if (i == 0) {
+          m_ref = mx;
+        } else if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2(m_ref - mx) : 1.f;
+          if (raise) m_ref = mx;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < kHeadDim; c += 16) {
+            uint32_t o[16];
+            tmem::ld_x16(tl + kColO + c, o);
+            tmem::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem::st_x16(tl + kColO + c, o);
+          }
+        }
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t scale2 = pack2(scale, scale), minus_ref = pack2(-ref, -ref);
+        uint64_t l2 = pack2(0.f, 0.f), l3 = pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* x = e < 16 ? s[c] + 2 * e : s[c + 1] + 2 * (e - 16);
+            float pa, pb;
+            unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, minus_ref), pa, pb);
+            pa = ex2(pa);
+            pb = ex2(pb);
+            if (e & 1) l2 = add2(l2, pack2(pa, pb));
+            else l3 = add2(l3, pack2(pa, pb));
+            pw[e] = pack_bf16(pa, pb);
+          }
+          tmem::st_x32(tl + 16 * c, pw);
+        }
+        float la, lb;
+        unpack2(add2(l2, l3), la, lb);
+        l += la + lb;
+        tmem::wait_st();
+        tmem::fence_before();
+        mbar_arrive(smem_u32(&ctl->p_full[b]));
+        if (!(ok = all(done))) break;
+      }
+      nv += 2 * steps;
+      if (!ok) break;
+      // ---- the rows' results
+      if (!(ok = all(wait(ctl->o_done[b], n - 1)))) break;
+      tmem::fence_after();
+      const bool odd = *reinterpret_cast<volatile int*>(&ctl->odd) != 0;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool whole_tile = w.it.slot < 0;
+      const size_t row = size_t(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + size_t(w.it.kvh) * G + m % G;
+      uint8_t* slot = parts + size_t(whole_tile ? 0 : w.it.slot) * kWindowSlotBytes;
+      float* part = reinterpret_cast<float*>(slot + kWindowRows * 8) + size_t(m) * kHeadDim;
+      if (mine && !whole_tile) reinterpret_cast<float2*>(slot)[m] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
+      if (!idle) {
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 16) {
+          uint32_t o[16];
+          tmem::ld_x16(tl + kColO + c, o);
+          tmem::wait_ld();
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * inv;
+          if (odd && mine) {  // infinities and NaN that this row sees of the steps that were looked over
+            const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
+            const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
+                              size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+            for (int j = 2 * w.it.begin; j < 2 * w.it.end; ++j) {
+              if (!looked(j & ~1)) continue;
+              const uint64_t see = w.visible(j, pos);
+              const int lp = w.page(j);
+              int phys = see && lp < kp.max_pages_per_request ? ptab[lp] : 0;
+              if (phys < 0 || phys >= kp.max_pages) phys = 0;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                                      kp.base + kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride +
+                                      size_t(phys) * kp.lay.bf16_page_stride + size_t(w.it.kvh) * kp.lay.bf16_head_stride) +
+                                  kPage * kHeadDim + c;
+              for (int t = 0; t < kPage; ++t)
+                if ((see >> t) & 1ull)
+                  for (int e = 0; e < 16; ++e) {
+                    const float y = bf16_f32(v[t * kHeadDim + e]);
+                    if (!(fabsf(y) < INFINITY)) {
+#pragma unroll
+                      for (int g = 0; g < 16; ++g)
+                        if (g == e) x[g] += y;
+                    }
+                  }
+            }
+          }
+          if (mine) {
+            if (whole_tile) {
+              uint4* dst = reinterpret_cast<uint4*>(out + row * kHeadDim + c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                dst[e] = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
+                                    pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
+            }
+            float4* f = whole_tile ? (out_f32 ? reinterpret_cast<float4*>(out_f32 + row * kHeadDim + c) : nullptr)
+                                   : reinterpret_cast<float4*>(part + c);
+            if (f)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          }
+        }
+      }
+      tmem::fence_before();  // O is read before the next item's first MMA writes it
+    }
+  }
+  __syncwarp();
+  tmem::fence_before();
+  __syncthreads();
+  tmem::fence_after();
+  if (warp == 0) tmem::dealloc(tm, 512);
+}
+
+// Rows of tiles whose pages were cut into parts, a warp each: the parts' results by their maxima
+// and denominators, in order.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParams kp, const uint8_t* __restrict__ parts,
+                                                                     uint16_t* __restrict__ out, float* __restrict__ out_f32) {
+  pdl_wait();
+  pdl_trigger();
+  const int* counts = plan_counts(kp);
+  const WindowMerge* merges = reinterpret_cast<const WindowMerge*>(kp.base + kp.lay.window_plan + counts[6]);
+  const int lane = threadIdx.x & 31, n_rows = counts[2] * kWindowRows, G = kp.gqa;
+  for (int e = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); e < n_rows; e += gridDim.x * (kMergeThreads / 32)) {
+    const WindowMerge mg = merges[e / kWindowRows];
+    const int m = e % kWindowRows;
+    if (m >= mg.n_tok * G) continue;
+    const uint8_t* slot = parts + size_t(mg.first_slot) * kWindowSlotBytes;
+    float top = -INFINITY;
+    for (int k = 0; k < mg.n_parts; ++k)
+      top = fmaxf(top, reinterpret_cast<const float2*>(slot + size_t(k) * kWindowSlotBytes)[m].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < mg.n_parts; ++k) {
+      const uint8_t* at = slot + size_t(k) * kWindowSlotBytes;
+      const float2 ml = reinterpret_cast<const float2*>(at)[m];
+      if (ml.x == -INFINITY) continue;
+      const float f = ex2(ml.x - top) * ml.y;
+      const float4 x = reinterpret_cast<const float4*>(at + kWindowRows * 8)[m * (kHeadDim / 4) + lane];
+      l += f;
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const WindowReq rq = plan_reqs(kp)[mg.req];
+    const size_t row = size_t(rq.row + mg.tok0 + m / G) * kp.n_q_heads + size_t(mg.kvh) * G + m % G;
+    const float4 y = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    reinterpret_cast<uint2*>(out + row * kHeadDim)[lane] = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    if (out_f32) reinterpret_cast<float4*>(out_f32 + row * kHeadDim)[lane] = y;
+  }
+}
+
+template <int G, int NBUF>
+int resident_t(int n_sm) {
+  static PerDevice resident;
+  return resident.get([=] {
+    int e = int(cudaFuncSetAttribute(window_rows_kernel<G, NBUF>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem(G, NBUF)));
+    int per_sm = 0;
+    if (!e)
+      e = int(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, window_rows_kernel<G, NBUF>, 128, kRowsSmem(G, NBUF)));
+    return e ? -e : (per_sm > 0 ? per_sm : 1) * n_sm;
+  });
+}
+
+template <int G, int NBUF>
+int launch_rows_t(const KernelParams& kp, int layer, const void* q, void* out, float* out_f32, uint8_t* partials, int n_sm,
+                  void* stream, int* launches) {
+  const int resident = resident_t<G, NBUF>(n_sm);
+  if (resident < 0) return -resident;
+  const int e = launch_ex(window_rows_kernel<G, NBUF>, dim3(resident), dim3(128), size_t(kRowsSmem(G, NBUF)), stream, kp, layer,
+                          static_cast<const uint16_t*>(q), partials, static_cast<uint16_t*>(out), out_f32);
+  if (!e) *launches += 1;
+  return e;
+}
+
+}  // namespace
+
+int window_rows_resident_ctas(int gqa, bool deep, int n_sm) {
+  if (gqa == 4) return deep ? resident_t<4, 3>(n_sm) : resident_t<4, 2>(n_sm);
+  if (gqa == 8) return deep ? resident_t<8, 3>(n_sm) : resident_t<8, 2>(n_sm);
+  return n_sm;
+}
+
+int launch_window(const KernelParams& kp, int layer, const void* map, const void* q, void* out, float* out_f32, uint8_t* ws,
+                  const WindowWorkspace& wl, bool rows, bool deep, bool tiles, bool merges, int n_sm, void* stream, int* launches) {
+  int e = 0;
+  if (rows) {
+    uint8_t* p = ws + wl.rows;
+    if (kp.gqa == 4)
+      e = deep ? launch_rows_t<4, 3>(kp, layer, q, out, out_f32, p, n_sm, stream, launches)
+               : launch_rows_t<4, 2>(kp, layer, q, out, out_f32, p, n_sm, stream, launches);
+    else
+      e = deep ? launch_rows_t<8, 3>(kp, layer, q, out, out_f32, p, n_sm, stream, launches)
+               : launch_rows_t<8, 2>(kp, layer, q, out, out_f32, p, n_sm, stream, launches);
+  }
+  if (!e && tiles) {
+    static PerDevice attr;
+    const int ready = attr.get([] {
+      const int x = int(cudaFuncSetAttribute(window_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
+      return x ? -x : 1;
+    });
+    if (ready < 0) return -ready;
+    e = launch_ex(window_tile_kernel, dim3(n_sm), dim3(kThreads), size_t(kTileSmem), stream, kp, layer,
+                  *static_cast<const CUtensorMap*>(map), static_cast<const uint16_t*>(q), ws + wl.tiles,
+                  static_cast<uint16_t*>(out), out_f32);
+    if (!e) *launches += 1;
+  }
+  if (!e && merges) {
+    e = launch_ex(window_merge_kernel, dim3(4 * n_sm), dim3(kMergeThreads), 0, stream, kp,
+                  static_cast<const uint8_t*>(ws + wl.tiles), static_cast<uint16_t*>(out), out_f32);
+    if (!e) *launches += 1;
+  }
+  return e;
+}
+
+}  // namespace oscar
