@@ -233,6 +233,14 @@ struct Work {
     if (rq.window == 0) return upto;
     return upto & (~low_bits(p - rq.window - t0 + 1) | low_bits(rq.n_sink - t0));
   }
+  // Tokens that some query from position p0 to p1 sees.
+  __device__ uint64_t seen(int j, int p0, int p1) const {
+    if (j >= pages) return 0;
+    const int t0 = page(j) * kPage;
+    const uint64_t upto = low_bits(p1 - t0 + 1);
+    if (rq.window == 0) return upto;
+    return upto & (~low_bits(p0 - rq.window - t0 + 1) | low_bits(rq.n_sink - t0));
+  }
   // Whether every query from position p0 to p1 sees all of list page j.
   __device__ bool whole(int j, int p0, int p1) const { return (visible(j, p0) & visible(j, p1)) == ~0ull; }
 };
@@ -494,9 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               bad |= lo | hi;
               x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
             }
-            if (bad) {  // (the flag first: the other block may find only the zeros)
-              *reinterpret_cast<volatile int*>(&ctl->odd) = 1;
-              __threadfence_block();
+            if (bad) {
+              const int t = (k * kBlockRows + r) % (kStep * 8) / 8, j = j0 + t / kPage;  // eight chunks a token and half
+              if ((w.seen(j, first_pos, last_pos) >> (t % kPage)) & 1ull) {  // (not what lies behind the last token)
+                *reinterpret_cast<volatile int*>(&ctl->odd) = 1;  // first: the other block may find only the zeros
+                __threadfence_block();
+              }
               at[k * kBlockRows] = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
