@@ -74,7 +74,10 @@ constexpr double kSharedPrivateBytes = 30e6, kSharedPrivateWeight = 2.5;
 constexpr int kSharedMinSaved = 4;  // a run that saves fewer pages is none by itself: its members attend them, or their own runs do
 constexpr int kMaxWindowRowItems = 4096;  // row items of a window plan, beside one per request and kv-head
 constexpr int kMaxWindowTiles = 65536;
-constexpr int kWindowItemSteps = 3;  // an item's fixed time in the tile kernel, in steps
+constexpr int kWindowItemSteps = 2;   // an item's fixed time in the tile kernel, in steps
+constexpr int kWindowMinSteps = 2;    // of a part of a tile
+constexpr int kWindowMergeCost = 8;   // of a plan with cut tiles: the merge's launch, in half steps
+constexpr int kWindowSplitSteps = 3;  // of a tile whose pages go to two blocks of accumulators
 constexpr int kBf16ItemTokens = 128;  // sink+ring tokens per decode work item (at least; one chunk of the CTA)
 
 bool config_ok(const oscar_config* c, std::string* why) {
@@ -156,9 +159,9 @@ DeviceLayout compute_layout(const oscar_config& c) {
     L.evict_plan = take(256 + reqs * sizeof(EvictReq));
     L.evict_pages = take(reqs * size_t(c.max_pages_per_request) * 4);
     L.max_window_rows = reqs * Hkv + kMaxWindowRowItems;
-    L.max_window_tiles = kMaxWindowTiles;
+    L.max_window_tiles = kMaxWindowTiles + 1024;  // + cuts
     L.window_plan_bytes = window_lists_offset(reqs) + align256(L.max_window_rows * sizeof(DecodeItem)) +
-                          align256(L.max_window_tiles * sizeof(WindowTile)) + align256(kWindowSlots * sizeof(WindowMerge));
+                          align256(L.max_window_tiles * sizeof(WindowTile)) + align256(kWindowSlots * sizeof(WindowMerge)) + 4096;  // + the first tiles of up to 1023 CTAs
     L.window_plan = take(L.window_plan_bytes);
   }
   L.page_table = take(reqs * size_t(c.max_pages_per_request) * 4);
@@ -481,6 +484,97 @@ oscar_status make_page_map(oscar_cache* c, const char* what) {
   if (e) return fail(OSCAR_ERR_CUDA, "tensor map of the page pool: %s", cudaGetErrorString(cudaError_t(e)));
   c->map_ready = true;
   return OSCAR_OK;
+}
+
+// The tiles of a window plan as work items by CTA.  Either whole tiles, the longest first, each to
+// the CTA that is done soonest; or, where that leaves CTAs idle, an equal share of all steps to
+// each, so that a tile at a border of shares is cut.  Tiles of one block of rows are split over the
+// two blocks of accumulators where they are long enough and there is room for their parts.
+void place_tiles(const oscar_cache* c, const std::vector<WindowTile>& whole, int G, std::vector<WindowTile>* tiles,
+                 std::vector<WindowMerge>* merges, std::vector<int>* first_item, int* n_slots) {
+  const int P = c->n_sm, n = int(whole.size());
+  if (!n) return;
+  auto one_block = [&](const WindowTile& t) { return t.n_tok * G <= kWindowRows / 2; };
+  // An item's time in half steps (pages of two blocks, or two of one): its pages, and a fixed part.
+  long long n_split = 0;
+  for (const WindowTile& t : whole) n_split += one_block(t) && t.end >= kWindowSplitSteps;
+  const bool split = 2 * n_split <= kWindowSlots;
+  auto splits = [&](const WindowTile& t) { return split && one_block(t) && t.end >= kWindowSplitSteps; };
+  auto cost = [&](const WindowTile& t, long long steps) { return (splits(t) ? 1 : 2) * steps + 2 * kWindowItemSteps; };
+  // whole tiles
+  std::vector<int> order(n), cta_of(n);
+  for (int i = 0; i < n; ++i) order[i] = i;
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return cost(whole[a], whole[a].end) > cost(whole[b], whole[b].end); });
+  std::vector<std::pair<long long, int>> load(P);  // a heap, least first (equal: the lowest CTA)
+  for (int i = 0; i < P; ++i) load[i] = {0, i};
+  auto later = [](const std::pair<long long, int>& a, const std::pair<long long, int>& b) { return a > b; };
+  long long longest = 0, total = 0, shared_total = 0;
+  for (int i : order) {
+    std::pop_heap(load.begin(), load.end(), later);
+    const long long t = cost(whole[i], whole[i].end);
+    load.back().first += t;
+    longest = std::max(longest, load.back().first);
+    cta_of[i] = load.back().second;
+    std::push_heap(load.begin(), load.end(), later);
+    total += t;
+    shared_total += cost(whole[i], whole[i].end) - 2 * kWindowItemSteps;
+  }
+  // equal shares: P borders at most, an item's fixed time each, and the merge's
+  const long long share = (shared_total + 2LL * kWindowItemSteps * (n + P) + P - 1) / P;
+  const long long cuts = std::min<long long>(P, n * 64LL);
+  const long long shared_cost = std::max<long long>(share, 2 * kWindowMinSteps + 2 * kWindowItemSteps) + kWindowMergeCost + cuts / 32;
+  const bool cut = shared_cost < longest && 4LL * P + 2 * (split ? n_split : 0) <= kWindowSlots;
+  std::vector<std::vector<WindowTile>> of(P);
+  auto add = [&](int cta, const WindowTile& t) { of[cta].push_back(t); };
+  auto finish = [&](const WindowTile& t, const std::vector<std::pair<int, WindowTile>>& parts) {
+    // a tile's parts by CTA: their slots, and its merge
+    const bool s = splits(t);
+    if (parts.size() == 1 && !s) {
+      add(parts[0].first, parts[0].second);
+      return;
+    }
+    const int per = s || !one_block(t) ? 2 : 1;
+    merges->push_back({t.req, t.kvh, t.tok0, t.n_tok, *n_slots, int(parts.size()) * (s ? 2 : 1), s ? 1 : per});
+    for (const auto& p : parts) {
+      WindowTile w = p.second;
+      w.slot = *n_slots;
+      w.split = s;
+      *n_slots += per;
+      add(p.first, w);
+    }
+  };
+  if (!cut) {
+    for (int i : order) finish(whole[i], {{cta_of[i], whole[i]}});
+  } else {
+    int cta = 0;
+    long long left = share;  // of this CTA
+    std::vector<std::pair<int, WindowTile>> parts;
+    for (const WindowTile& t : whole) {
+      parts.clear();
+      const long long unit = splits(t) ? 1 : 2;
+      for (int at = 0; at < t.end;) {
+        int take = int(std::max<long long>(kWindowMinSteps, (left - 2 * kWindowItemSteps) / unit));
+        if (cta == P - 1 || t.end - at - take < kWindowMinSteps) take = t.end - at;  // (no crumbs)
+        take = std::min(take, t.end - at);
+        WindowTile w = t;
+        w.begin = at;
+        w.end = at + take;
+        parts.push_back({cta, w});
+        at += take;
+        left -= unit * take + 2 * kWindowItemSteps;
+        if (left < unit * kWindowMinSteps + 2 * kWindowItemSteps && cta < P - 1) {
+          ++cta;
+          left += share;
+        }
+      }
+      finish(t, parts);
+    }
+  }
+  first_item->assign(P + 1, 0);
+  for (int i = 0; i < P; ++i) {
+    tiles->insert(tiles->end(), of[i].begin(), of[i].end());
+    (*first_item)[i + 1] = int(tiles->size());
+  }
 }
 
 // Workspace of windowed attention with room for `slots` parts of cut tiles.  Only the total depends
@@ -1486,15 +1580,14 @@ oscar_status oscar_plan_window(oscar_cache* c, const int* slots, const int* n_qu
     }
   }
   std::stable_sort(items.begin(), items.end(), [](const DecodeItem& a, const DecodeItem& b) { return a.end - a.begin > b.end - b.begin; });
-  // ---- several: tiles, and their steps cut into parts where that ends the launch sooner
+  // ---- several: tiles
   const int per_tile = kWindowRows / G;
   std::vector<WindowTile> whole;
-  long long n_tiles = 0, total_steps = 0;
-  int longest = 0;
+  long long n_tiles = 0;
   for (const WindowReq& r : reqs)
     if (r.n > 1) n_tiles += (long long)Hkv * ceil_div(r.n, per_tile);
-  if (n_tiles > (long long)c->lay.max_window_tiles)
-    return fail(OSCAR_ERR_INVALID_ARG, "%lld tiles of queries exceed %zu; plan fewer queries", n_tiles, c->lay.max_window_tiles);
+  if (n_tiles > kMaxWindowTiles)
+    return fail(OSCAR_ERR_INVALID_ARG, "%lld tiles of queries exceed %d; plan fewer queries", n_tiles, kMaxWindowTiles);
   whole.reserve(size_t(n_tiles));
   for (int i = 0; i < n_req; ++i) {
     const WindowReq& r = reqs[i];
@@ -1502,50 +1595,14 @@ oscar_status oscar_plan_window(oscar_cache* c, const int* slots, const int* n_qu
     for (int h = 0; h < Hkv; ++h)
       for (int t = 0; t < r.n; t += per_tile) {
         const int n = std::min(per_tile, r.n - t);
-        const int steps = ceil_div(window_pages(r.first + t, n, r.n_sink, r.window).pages, 2);
-        whole.push_back({i, h, t, n, 0, steps, -1});
-        total_steps += steps;
-        longest = std::max(longest, steps);
+        whole.push_back({i, h, t, n, 0, ceil_div(window_pages(r.first + t, n, r.n_sink, r.window).pages, 2), -1, 0});
       }
-  }
-  int cap = longest;
-  if (!whole.empty()) {
-    // a launch lasts as long as its longest item, or as all of them over the SMs; parts add an
-    // item's fixed time each, and the merge
-    double best = -1;
-    for (int k = 1; k <= std::min(longest, 64); ++k) {
-      const int ch = ceil_div(longest, k);
-      long long n = 0, cut = 0;
-      for (const WindowTile& t : whole) {
-        const int m = ceil_div(t.end, ch);
-        n += m;
-        cut += m > 1 ? m : 0;
-      }
-      if (cut > kWindowSlots || n > (long long)c->lay.max_window_tiles) break;
-      const double rounds = double((n + c->n_sm - 1) / c->n_sm);
-      const double even = double(total_steps + kWindowItemSteps * n) / c->n_sm;
-      const double cost = std::max(even, std::min(rounds * (ch + kWindowItemSteps), even + ch)) + (k > 1 ? 4.0 + 0.02 * double(cut) : 0.0);
-      if (best < 0 || cost < best) {
-        best = cost;
-        cap = ch;
-      }
-    }
   }
   std::vector<WindowTile> tiles;
   std::vector<WindowMerge> merges;
-  tiles.reserve(whole.size());
+  std::vector<int> first_item;
   int n_slots = 0;
-  for (const WindowTile& t : whole) {
-    const int m = ceil_div(t.end, cap);
-    if (m < 2) {
-      tiles.push_back(t);
-      continue;
-    }
-    merges.push_back({t.req, t.kvh, t.tok0, t.n_tok, n_slots, m});
-    for (int k = 0; k < m; ++k)  // as even as whole steps allow
-      tiles.push_back({t.req, t.kvh, t.tok0, t.n_tok, int((long long)t.end * k / m), int((long long)t.end * (k + 1) / m), n_slots++});
-  }
-  std::stable_sort(tiles.begin(), tiles.end(), [](const WindowTile& a, const WindowTile& b) { return a.end - a.begin > b.end - b.begin; });
+  place_tiles(c, whole, G, &tiles, &merges, &first_item, &n_slots);
   if (!tiles.empty()) {
     oscar_status st = make_page_map(c, "several queries a request");
     if (st) return st;
@@ -1558,21 +1615,23 @@ oscar_status oscar_plan_window(oscar_cache* c, const int* slots, const int* n_qu
   const size_t rows_off = window_lists_offset(c->cfg.max_requests);
   const size_t tiles_off = rows_off + align256(items.size() * sizeof(DecodeItem));
   const size_t merges_off = tiles_off + align256(tiles.size() * sizeof(WindowTile));
+  const size_t first_off = merges_off + align256(merges.size() * sizeof(WindowMerge));
   int32_t* counts = reinterpret_cast<int32_t*>(u.staging);
   counts[0] = int(items.size());
   counts[1] = int(tiles.size());
   counts[2] = int(merges.size());
-  counts[3] = 0;
+  counts[3] = first_item.empty() ? 0 : int(first_item.size()) - 1;
   counts[4] = int(rows_off);
   counts[5] = int(tiles_off);
   counts[6] = int(merges_off);
-  counts[7] = 0;
+  counts[7] = int(first_off);
   std::memcpy(u.staging + 256, reqs.data(), reqs.size() * sizeof(WindowReq));
   if (!items.empty()) std::memcpy(u.staging + rows_off, items.data(), items.size() * sizeof(DecodeItem));
   if (!tiles.empty()) std::memcpy(u.staging + tiles_off, tiles.data(), tiles.size() * sizeof(WindowTile));
   if (!merges.empty()) std::memcpy(u.staging + merges_off, merges.data(), merges.size() * sizeof(WindowMerge));
+  if (!first_item.empty()) std::memcpy(u.staging + first_off, first_item.data(), first_item.size() * 4);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.window_plan, u.staging, merges_off + merges.size() * sizeof(WindowMerge),
+  CUDA_TRY(cudaMemcpyAsync(c->base + c->lay.window_plan, u.staging, first_off + first_item.size() * 4,
                            cudaMemcpyHostToDevice, s));
   st = end_upload(c, u, s);
   if (st) return st;

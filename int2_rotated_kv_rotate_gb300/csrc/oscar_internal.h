@@ -115,16 +115,19 @@ struct WindowReq {
   int sinks, skip, u_pre;
 };
 // One work item of the tile kernel: queries tok0 .. tok0 + n_tok - 1 of request req, the heads of
-// kvh, steps [begin, end) of the tile's list of pages (two a step); slot: where the part's results
-// go, -1 where it is the whole tile.  And a tile that was cut: parts first_slot ..
-constexpr int kWindowRows = 256;  // query rows (queries x G) of a tile at most
-constexpr size_t kWindowSlotBytes = kWindowRows * (8 + 4 * kHeadDim);  // (maximum, denominator), then rows
-constexpr int kWindowSlots = 608;  // parts of a plan at most
+// kvh, steps [begin, end) of the tile's list of pages (two a step).  split (at most 128 rows): the
+// even pages of the list go to one block of accumulators, the odd ones to another, a part each.
+// slot: where the blocks' results go, one after the other; -1 where the item is the whole tile and
+// not split.  Items are stored by CTA.
+constexpr int kWindowRows = 256;  // query rows (queries x G) of a tile at most, two blocks of 128
+constexpr size_t kWindowSlotBytes = kWindowRows / 2 * (8 + 4 * kHeadDim);  // (maximum, denominator), then rows
+constexpr int kWindowSlots = 1216;  // of a plan at most
 struct WindowTile {
-  int req, kvh, tok0, n_tok, begin, end, slot;
+  int req, kvh, tok0, n_tok, begin, end, slot, split;
 };
+// A tile of several parts: part k of block b is slot first_slot + stride k + b.
 struct WindowMerge {
-  int req, kvh, tok0, n_tok, first_slot, n_parts;
+  int req, kvh, tok0, n_tok, first_slot, n_parts, stride;
 };
 
 #ifdef __CUDACC__
@@ -177,8 +180,9 @@ struct DeviceLayout {
   // BF16 format: the shared runs of the decode plan, uploaded as one block: int32
   // order[max_requests] (plan indices) and the items, whose number is decode counts [3]
   size_t shared_order, shared_items;
-  // BF16 format: the window plan, one block: int32 counts[8] at +0 (row items, tiles, cut tiles, 0,
-  // and the byte offsets of the three lists), WindowReq at +256, the lists behind them
+  // BF16 format: the window plan, one block: int32 counts[8] at +0 (row items, tiles, cut tiles,
+  // CTAs with tiles, and the byte offsets of the three lists and of the first tile of each CTA),
+  // WindowReq at +256, the lists behind them
   size_t window_plan, window_plan_bytes;
   size_t max_window_rows, max_window_tiles;
   // decode plan, in front of the items: int64 [max_requests], the tokens of all kv-heads of the

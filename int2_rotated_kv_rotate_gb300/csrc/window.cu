@@ -158,10 +158,9 @@ struct Control {
   uint64_t full[kStages], empty[kStages];
   // Completion n is item n of those in which the block has rows.
   uint64_t q_full[2];
-  // Completion n is step n of the block: S is written, P is written, O holds the steps up to n
-  // (and P and S are read).  Whoever waits for one waits for every step in order, and none gets two
-  // ahead.
-  uint64_t s_full[2], p_full[2], o_done[2];
+  // Page n of the block has buffer n % 2, whose completion is n / 2: S is written, P is written, O
+  // holds the pages up to n (and P is read).
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
   uint64_t drain[2];
   uint32_t tmem;
   int abort;
@@ -172,10 +171,11 @@ constexpr int kOffControl = kOffStages + kStages * kStageBytes;
 constexpr int kTileSmem = kOffControl + int(sizeof(Control)) + 1024;  // + alignment to 1024
 static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 
-// Tensor-memory columns of block b: S of 128 (P over its first 64), O of 128.
+// Tensor-memory columns of block b: two buffers of S of 64 (P over the first 32 of each), O of 128.
 constexpr uint32_t kBlockCols = 256, kColO = 128;
 
 constexpr float kRaise = 16.f;
+constexpr int kSpins = 1024;
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -211,6 +211,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -223,8 +232,14 @@ struct Work {
   WindowTile it;
   WindowReq rq;
   int rows, blocks, sink_pages, window_page, pages;
+  // Pages of block b: all, or, split, every other one.
+  __device__ int page0(int b) const { return first_page() + (it.split ? b : 0); }
+  __device__ int stride() const { return it.split ? 2 : 1; }
+  // Row r of block b in the tile.
+  __device__ int row(int b, int r) const { return (it.split ? 0 : b * kBlockRows) + r; }
   __device__ int page(int j) const { return j < sink_pages ? j : window_page + j - sink_pages; }
-  __device__ int steps() const { return it.end - it.begin; }
+  __device__ int first_page() const { return 2 * it.begin; }
+  __device__ int end_page() const { return min(2 * it.end, pages); }
   // Tokens of list page j that the query at position p sees.
   __device__ uint64_t visible(int j, int p) const {
     if (j >= pages) return 0;
@@ -241,8 +256,17 @@ struct Work {
     if (rq.window == 0) return upto;
     return upto & (~low_bits(p0 - rq.window - t0 + 1) | low_bits(rq.n_sink - t0));
   }
-  // Whether every query from position p0 to p1 sees all of list page j.
-  __device__ bool whole(int j, int p0, int p1) const { return (visible(j, p0) & visible(j, p1)) == ~0ull; }
+  // Pages of the list of which every query from position p0 to p1 sees all: those of the window
+  // between its edge for the last query and the diagonal of the first.  (Sink pages are not counted.)
+  struct Range {
+    int begin, end;
+    __device__ bool has(int i) const { return i >= begin && i < end; }
+  };
+  __device__ Range whole(int p0, int p1) const {
+    const int edge = rq.window > 0 ? max(0, p1 - rq.window + 1) : 0;          // first token that all see
+    const int a = max((edge + kPage - 1) / kPage, window_page), b = (p0 + 1) / kPage;  // pages [a, b)
+    return {sink_pages + a - window_page, min(sink_pages + b - window_page, pages)};
+  }
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -260,9 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
-      mbar_init(smem_u32(&ctl->s_full[b]), 1);
-      mbar_init(smem_u32(&ctl->p_full[b]), kBlockRows);
-      mbar_init(smem_u32(&ctl->o_done[b]), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&ctl->s_full[b][i]), 1);
+        mbar_init(smem_u32(&ctl->p_full[b][i]), kBlockRows);
+        mbar_init(smem_u32(&ctl->o_done[b][i]), 1);
+      }
       mbar_init(smem_u32(&ctl->drain[b]), 1);
     }
     ctl->abort = ctl->odd = 0;
@@ -276,55 +302,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   const int* counts = plan_counts(kp);
-  const int n_items = counts[1], G = kp.gqa;
+  const int G = kp.gqa;
+  const int* first_item = reinterpret_cast<const int*>(kp.base + kp.lay.window_plan + counts[7]);  // of each CTA
+  const int ix0 = int(blockIdx.x) < counts[3] ? first_item[blockIdx.x] : 0;
+  const int ix1 = int(blockIdx.x) < counts[3] ? first_item[blockIdx.x + 1] : 0;
   const WindowTile* items = reinterpret_cast<const WindowTile*>(kp.base + kp.lay.window_plan + counts[5]);
   auto load_work = [&](int ix) {
     Work w;
     w.it = items[ix];
     w.rq = plan_reqs(kp)[w.it.req];
     w.rows = w.it.n_tok * G;
-    w.blocks = w.rows > kBlockRows ? 2 : 1;
     const WindowPages p = window_pages(w.rq.first + w.it.tok0, w.it.n_tok, w.rq.n_sink, w.rq.window);
     w.sink_pages = p.sink_pages;
     w.window_page = p.window_page;
     w.pages = p.pages;
+    w.blocks = (w.it.split ? w.end_page() - w.first_page() > 1 : w.rows > kBlockRows) ? 2 : 1;
     return w;
   };
   // Bounded wait of a whole warp for completions of one or two barriers (index: of the
-  // completion); lane 0 polls the first, lane 1 the second.  Each lane has its own poll's result:
-  // the roles vote once a step, where the warp meets anyway, so after a wait that ran out MMAs and
-  // stores of that step still go out, on memory of this CTA, and every role then leaves its loop.
+  // completion); lane 0 polls the first, lane 1 the second, without being suspended for the first
+  // kSpins polls (a suspended thread takes some hundred cycles to wake, and every step has three
+  // such hand-overs one after the other).  Each lane has its own poll's result: the roles vote once a
+  // page, where the warp meets anyway, so after a wait that ran out MMAs and stores of that page
+  // still go out, on memory of this CTA, and every role then leaves its loop.
+  auto poll = [&](uint32_t a, uint32_t par) -> int {
+    int done = 0;
+    for (int i = 0; i < kSpins && !done; ++i) done = mbar_test_wait(a, par);
+    for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
+      done = mbar_try_wait_for(a, par, 1000000u);
+      if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
+    }
+    if (!done) {
+      *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+      flag(kp, OSCAR_FLAG_TIMEOUT);
+    }
+    return done;
+  };
   auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> int {
     int done = 1;
-    if (lane < 2) {
-      const uint32_t a = lane ? smem_u32(&bar1) : smem_u32(&bar0), par = (lane ? index1 : index0) & 1u;
-      done = mbar_try_wait(a, par);
-      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
-        done = mbar_try_wait_for(a, par, 1000000u);
-        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
-      }
-      if (!done) {
-        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-        flag(kp, OSCAR_FLAG_TIMEOUT);
-      }
-    }
+    if (lane < 2) done = poll(lane ? smem_u32(&bar1) : smem_u32(&bar0), (lane ? index1 : index0) & 1u);
     __syncwarp();
     return done;
   };
   auto wait = [&](uint64_t& bar, uint32_t index) -> int {
     int done = 1;
-    if (lane == 0) {
-      const uint32_t a = smem_u32(&bar);
-      done = mbar_try_wait(a, index & 1u);
-      for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
-        done = mbar_try_wait_for(a, index & 1u, 1000000u);
-        if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
-      }
-      if (!done) {
-        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-        flag(kp, OSCAR_FLAG_TIMEOUT);
-      }
-    }
+    if (lane == 0) done = poll(smem_u32(&bar), index & 1u);
     __syncwarp();
     return done;
   };
@@ -334,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- pages
     uint32_t n = 0, issued = 0;  // fillings of stages: keys and values of each step in turn
     bool ok = true;
-    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+    for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
       const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
       if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
@@ -374,34 +396,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S = Q K^T
-    constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kStep, false);
+    constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
     const uint64_t qd = tmem::sdesc_sw128(sq, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
-    uint32_t n = 0, q0 = 0, q1 = 0, n0 = 0, n1 = 0;  // stages; items and steps of each block
+    uint32_t f = 0, q0 = 0, q1 = 0, n0 = 0, n1 = 0;  // fillings; items and pages of each block
     bool ok = true;
-    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+    for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
       ok = all(wait(ctl->q_full[0], q0++));
       if (ok && w.blocks > 1) ok = all(wait(ctl->q_full[1], q1++));
-      for (int i = 0; ok && i < w.steps(); ++i, n += 2) {
-        const uint32_t st = n % kStages;
-        for (int b = 0; ok && b < w.blocks; ++b) {
-          const uint32_t k = b ? n1++ : n0++;
+      const int end = w.end_page();
+      for (int j = w.first_page(); ok && j < end; ++j) {
+        const uint32_t st = f % kStages;
+        const bool leaves = (j & 1) || j == end - 1;
+        const int b0 = w.it.split ? j & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
+        for (int b = b0; ok && b < b1; ++b) {
+          const uint32_t n = b ? n1++ : n0++, buf = n & 1u;
           int done = 1;
-          if (b == 0) done = k ? wait2(ctl->full[st], n / kStages, ctl->o_done[b], k - 1) : wait(ctl->full[st], n / kStages);
-          else if (k) done = wait(ctl->o_done[b], k - 1);
+          const bool fresh = b == b0 && !(j & 1);
+          if (fresh && n >= 2) done = wait2(ctl->full[st], f / kStages, ctl->o_done[b][buf], (n >> 1) - 1);
+          else if (fresh) done = wait(ctl->full[st], f / kStages);
+          else if (n >= 2) done = wait(ctl->o_done[b][buf], (n >> 1) - 1);
           tmem::fence_after();
           if (elect_one()) {
-            const uint32_t d = tm + b * kBlockCols;
-            const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kStageBytes >> 4);
+            const uint32_t d = tm + b * kBlockCols + buf * kPage;
+            const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               tmem::mma_ss(d, qb + ((c >> 2) * (kQBlock / 2) + (c & 3) * 32) / 16, kb + ((c >> 2) * kHalf + (c & 3) * 32) / 16,
                            kIdS, c > 0);
-            tmem::commit(smem_u32(&ctl->s_full[b]));
-            if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            tmem::commit(smem_u32(&ctl->s_full[b][buf]));
+            if (leaves && b == b1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
           }
           ok = all(done);
         }
+        if (leaves) f += 2;
       }
     }
     if (!ok) {  // MMAs in flight end before the tensor memory is freed
@@ -413,26 +441,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
     const uint64_t vd = tmem::sdesc_sw128(sst, kHalf, 1024);
-    uint32_t n = 1, n0 = 0, n1 = 0;
+    uint32_t f = 1, n0 = 0, n1 = 0;
     bool ok = true;
-    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+    for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
-      for (int i = 0; ok && i < w.steps(); ++i, n += 2) {
-        const uint32_t st = n % kStages;
-        for (int b = 0; ok && b < w.blocks; ++b) {
-          const uint32_t k = b ? n1++ : n0++;
-          const int done = b == 0 ? wait2(ctl->full[st], n / kStages, ctl->p_full[b], k) : wait(ctl->p_full[b], k);
+      const int end = w.end_page();
+      for (int j = w.first_page(); ok && j < end; ++j) {
+        const uint32_t st = f % kStages;
+        const bool leaves = (j & 1) || j == end - 1;
+        const int b0 = w.it.split ? j & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
+        for (int b = b0; ok && b < b1; ++b) {
+          const uint32_t n = b ? n1++ : n0++, buf = n & 1u;
+          const int done = b == b0 && !(j & 1) ? wait2(ctl->full[st], f / kStages, ctl->p_full[b][buf], n >> 1)
+                                              : wait(ctl->p_full[b][buf], n >> 1);
           tmem::fence_after();
           if (elect_one()) {
-            const uint32_t a = tm + b * kBlockCols, d = a + kColO;
-            const uint64_t vb = vd + st * (kStageBytes >> 4);
+            const uint32_t a = tm + b * kBlockCols + buf * kPage, d = tm + b * kBlockCols + kColO;
+            const uint64_t vb = vd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, i > 0 || c > 0);
-            tmem::commit(smem_u32(&ctl->o_done[b]));
-            if (b == w.blocks - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            for (int c = 0; c < 4; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, j > w.page0(b) || c > 0);
+            tmem::commit(smem_u32(&ctl->o_done[b][buf]));
+            if (leaves && b == b1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
           }
           ok = all(done);
         }
+        if (leaves) f += 2;
       }
     }
     if (!ok) {
@@ -445,17 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = (warp - 4) >> 2, wq = warp & 3, r = (wq << 5) | lane;
     const float scale = kLog2e * rsqrtf(float(kHeadDim));
     const uint32_t tl = tm + b * kBlockCols + (uint32_t(32 * wq) << 16);
-    uint32_t n = 0, nv = 1;  // steps of this block; fillings up to the item's first values
+    uint32_t n = 0, nv = 1;  // pages of this block; fillings up to the item's first values
     bool ok = true;
-    for (int ix = blockIdx.x; ok && ix < n_items; ix += gridDim.x) {
+    for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
-      const int steps = w.steps();
+      const int first = w.first_page(), end = w.end_page(), fillings = 2 * (w.it.end - w.it.begin);
+      const int m = w.row(b, r);
+      const bool mine = m < w.rows;
+      uint8_t* slot = parts + size_t(w.it.slot < 0 ? 0 : w.it.slot + b) * kWindowSlotBytes;  // of a part, the block's
       if (b >= w.blocks) {
-        nv += 2 * steps;
+        if (w.it.split && mine) reinterpret_cast<float2*>(slot)[r] = make_float2(-INFINITY, 0.f);  // no page for this block
+        nv += fillings;
         continue;
       }
-      const int m = b * kBlockRows + r;
-      const bool mine = m < w.rows;
       // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
       {
         const long long row = mine ? (long long)(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + w.it.kvh * G + m % G : -1;
@@ -474,26 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async();
       mbar_arrive(smem_u32(&ctl->q_full[b]));
       // positions of the block's first and last query and of this row's
-      const int p0 = w.rq.first + w.it.tok0 + b * kBlockRows / G;
-      const int p1 = w.rq.first + w.it.tok0 + min(w.it.n_tok, (b + 1) * kBlockRows / G) - 1;
-      const int pos = min(p0 + r / G, p1);
-      // Steps that some row of the tile does not see whole: both blocks look over their values
-      // (whoever comes first replaces what the other's product reads, too).
       const int first_pos = w.rq.first + w.it.tok0, last_pos = first_pos + w.it.n_tok - 1;
-      auto looked = [&](int j0) { return !w.whole(j0, first_pos, last_pos) || !w.whole(j0 + 1, first_pos, last_pos); };
+      const int p0 = first_pos + w.row(b, 0) / G, p1 = min(last_pos, p0 + kBlockRows / G - 1);
+      const int pos = min(p0 + r / G, p1);
+      // Pages that some row of the tile does not see whole: both blocks look over their values
+      // (whoever comes first replaces what the other's product reads, too).
+      const Work::Range whole_in_tile = w.whole(first_pos, last_pos), whole_in_block = w.whole(p0, p1);
       float m_ref = -INFINITY, l = 0.f;
-      const bool idle = b * kBlockRows + 32 * wq >= w.rows;  // no query in this warp's rows: P is not needed
-      for (int i = 0; i < steps; ++i, ++n) {
-        const int j0 = 2 * (w.it.begin + i);
-        const bool masked = !w.whole(j0, p0, p1) || !w.whole(j0 + 1, p0, p1);
-        int done = wait(ctl->s_full[b], n);
-        if (looked(j0)) {
-          const uint32_t f = nv + 2 * i, st = f % kStages;
+      const bool idle = w.row(b, 32 * wq) >= w.rows;  // no query in this warp's rows: P is not needed
+      for (int j = w.page0(b); j < end; j += w.stride(), ++n) {
+        const uint32_t buf = n & 1u;
+        const bool masked = !whole_in_block.has(j);
+        int done = wait(ctl->s_full[b][buf], n >> 1);
+        if (!whole_in_tile.has(j)) {
+          const uint32_t f = nv + 2 * ((j - first) / 2), st = f % kStages;
           done &= wait(ctl->full[st], f / kStages);
-          uint4* at = reinterpret_cast<uint4*>(smem + kOffStages + st * kStageBytes) + r;
+          uint4* page = reinterpret_cast<uint4*>(smem + kOffStages + st * kStageBytes + (j & 1) * (kHalf / 2)) + r;
 #pragma unroll 4
-          for (int k = 0; k < kStageBytes / 16 / kBlockRows; ++k) {
-            uint4 v = at[k * kBlockRows];
+          for (int k = 0; k < 8; ++k) {  // 512 chunks of 64 channels, then as many of the others
+            uint4* at = page + (k >> 2) * (kHalf / 16) + (k & 3) * kBlockRows;
+            const uint4 v = *at;
             uint32_t x[4] = {v.x, v.y, v.z, v.w};
             bool bad = false;
 #pragma unroll
@@ -503,69 +538,51 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
             }
             if (bad) {
-              const int t = (k * kBlockRows + r) % (kStep * 8) / 8, j = j0 + t / kPage;  // eight chunks a token and half
-              if ((w.seen(j, first_pos, last_pos) >> (t % kPage)) & 1ull) {  // (not what lies behind the last token)
+              const int t = ((k & 3) * kBlockRows + r) / 8;  // eight chunks a token
+              if ((w.seen(j, first_pos, last_pos) >> t) & 1ull) {  // (not what lies behind the last token)
                 *reinterpret_cast<volatile int*>(&ctl->odd) = 1;  // first: the other block may find only the zeros
                 __threadfence_block();
               }
-              at[k * kBlockRows] = make_uint4(x[0], x[1], x[2], x[3]);
+              *at = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
           fence_proxy_async();
         }
         if (idle) {
-          mbar_arrive(smem_u32(&ctl->p_full[b]));
+          mbar_arrive(smem_u32(&ctl->p_full[b][buf]));
           if (!(ok = all(done))) break;
           continue;
         }
+        const uint32_t ts = tl + buf * kPage;
         tmem::fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem::ld_x32(tl + 32 * c, s[c]);
+        uint32_t s[2][32];
+        tmem::ld_x32(ts, s[0]);
+        tmem::ld_x32(ts + 32, s[1]);
         tmem::wait_ld();
         if (masked) {
-          const uint64_t see[2] = {w.visible(j0, pos), w.visible(j0 + 1, pos)};
+          const uint64_t see = w.visible(j, pos);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = uint32_t(see[c >> 1] >> (32 * (c & 1)));
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t bits = uint32_t(see >> (32 * c));
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((bits >> e) & 1u)) s[c][e] = 0xff800000u;  // -inf
           }
         }
-        float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          mx = max3(mx, __uint_as_float(s[0][e]), __uint_as_float(s[1][e]));
-          my = max3(my, __uint_as_float(s[2][e]), __uint_as_float(s[3][e]));
-        }
-        mx = fmaxf(mx, my) * scale;
-        const bool raise = mx > m_ref + kRaise;  // also from -inf
-        if (i == 0) {
-          m_ref = mx;
-        } else if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? ex2(m_ref - mx) : 1.f;
-          if (raise) m_ref = mx;
-          l *= f;
-#pragma unroll
-          for (int c = 0; c < kHeadDim; c += 16) {
-            uint32_t o[16];
-            tmem::ld_x16(tl + kColO + c, o);
-            tmem::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem::st_x16(tl + kColO + c, o);
-          }
-        }
-        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t scale2 = pack2(scale, scale), minus_ref = pack2(-ref, -ref);
-        uint64_t l2 = pack2(0.f, 0.f), l3 = pack2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t pw[32];
+        // The weights by the reference so far, and the page's maximum beside them; where some row's
+        // is above its reference by more than kRaise (so is an item's first page), the references
+        // move, and the weights are taken again.
+        uint32_t pw[32];
+        uint64_t l2, l3;
+        for (bool again = false;; again = true) {
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t scale2 = pack2(scale, scale), minus_ref = pack2(-ref, -ref);
+          l2 = l3 = pack2(0.f, 0.f);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const uint32_t* x = e < 16 ? s[c] + 2 * e : s[c + 1] + 2 * (e - 16);
+            const uint32_t* x = e < 16 ? s[0] + 2 * e : s[1] + 2 * (e - 16);
+            mx[e & 3] = max3(mx[e & 3], __uint_as_float(x[0]), __uint_as_float(x[1]));
             float pa, pb;
             unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, minus_ref), pa, pb);
             pa = ex2(pa);
@@ -574,28 +591,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             else l3 = add2(l3, pack2(pa, pb));
             pw[e] = pack_bf16(pa, pb);
           }
-          tmem::st_x32(tl + 16 * c, pw);
+          if (again) break;
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+          const bool raise = top > m_ref + kRaise;  // also from -inf
+          if (!__any_sync(0xffffffffu, raise)) break;
+          const float f = raise ? ex2(m_ref - top) : 1.f;
+          if (raise) m_ref = top;
+          l *= f;
+          if (j == w.page0(b)) continue;  // (O is not there yet)
+          done &= wait(ctl->o_done[b][buf ^ 1u], (n - 1) >> 1);
+          tmem::fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            uint32_t o[32];
+            tmem::ld_x32(tl + kColO + c, o);
+            tmem::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem::st_x32(tl + kColO + c, o);
+          }
         }
+        tmem::st_x32(ts, pw);
         float la, lb;
         unpack2(add2(l2, l3), la, lb);
         l += la + lb;
         tmem::wait_st();
         tmem::fence_before();
-        mbar_arrive(smem_u32(&ctl->p_full[b]));
+        mbar_arrive(smem_u32(&ctl->p_full[b][buf]));
         if (!(ok = all(done))) break;
       }
-      nv += 2 * steps;
+      nv += fillings;
       if (!ok) break;
       // ---- the rows' results
-      if (!(ok = all(wait(ctl->o_done[b], n - 1)))) break;
+      if (!(ok = all(wait(ctl->o_done[b][(n - 1) & 1u], (n - 1) >> 1)))) break;
       tmem::fence_after();
       const bool odd = *reinterpret_cast<volatile int*>(&ctl->odd) != 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool whole_tile = w.it.slot < 0;
       const size_t row = size_t(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + size_t(w.it.kvh) * G + m % G;
-      uint8_t* slot = parts + size_t(whole_tile ? 0 : w.it.slot) * kWindowSlotBytes;
-      float* part = reinterpret_cast<float*>(slot + kWindowRows * 8) + size_t(m) * kHeadDim;
-      if (mine && !whole_tile) reinterpret_cast<float2*>(slot)[m] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
+      float* part = reinterpret_cast<float*>(slot + kBlockRows * 8) + size_t(r) * kHeadDim;
+      if (mine && !whole_tile) reinterpret_cast<float2*>(slot)[r] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < kHeadDim; c += 16) {
@@ -609,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
             const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                               size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
-            for (int j = 2 * w.it.begin; j < 2 * w.it.end; ++j) {
-              if (!looked(j & ~1)) continue;
+            for (int j = w.page0(b); j < end; j += w.stride()) {
+              if (whole_in_tile.has(j)) continue;
               const uint64_t see = w.visible(j, pos);
               const int lp = w.page(j);
               int phys = see && lp < kp.max_pages_per_request ? ptab[lp] : 0;
@@ -671,23 +706,51 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParam
     const WindowMerge mg = merges[e / kWindowRows];
     const int m = e % kWindowRows;
     if (m >= mg.n_tok * G) continue;
-    const uint8_t* slot = parts + size_t(mg.first_slot) * kWindowSlotBytes;
-    float top = -INFINITY;
-    for (int k = 0; k < mg.n_parts; ++k)
-      top = fmaxf(top, reinterpret_cast<const float2*>(slot + size_t(k) * kWindowSlotBytes)[m].x);
-    float l = 0.f;
+    // part k of block m / 128: slot first_slot + stride k + m / 128
+    const size_t step = size_t(mg.stride) * kWindowSlotBytes;
+    const uint8_t* slot = parts + size_t(mg.first_slot + m / kBlockRows) * kWindowSlotBytes;
+    const int r = m % kBlockRows;
+    // lane k: part k's maximum and denominator, 32 parts at a time; the rows of eight in flight
+    float top = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < mg.n_parts; ++k) {
-      const uint8_t* at = slot + size_t(k) * kWindowSlotBytes;
-      const float2 ml = reinterpret_cast<const float2*>(at)[m];
-      if (ml.x == -INFINITY) continue;
-      const float f = ex2(ml.x - top) * ml.y;
-      const float4 x = reinterpret_cast<const float4*>(at + kWindowRows * 8)[m * (kHeadDim / 4) + lane];
-      l += f;
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+    for (int k0 = 0; k0 < mg.n_parts; k0 += 32) {
+      const int n = min(32, mg.n_parts - k0);
+      const float2 ml = lane < n ? reinterpret_cast<const float2*>(slot + (k0 + lane) * step)[r] : make_float2(-INFINITY, 0.f);
+      float mx = ml.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      if (mx == -INFINITY) continue;
+      mx = fmaxf(mx, top);
+      const float old = ex2(top - mx);  // 0 at first
+      top = mx;
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx) * ml.y;
+      float sum = f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l = fmaf(l, old, sum);
+      o.x *= old;
+      o.y *= old;
+      o.z *= old;
+      o.w *= old;
+      for (int k = 0; k < n; k += 8) {
+        float4 x[8];
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          g[i] = __shfl_sync(0xffffffffu, f, (k + i) & 31);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k + i < n && g[i] != 0.f)  // (a part without a visible token has no row)
+            x[i] = reinterpret_cast<const float4*>(slot + (k0 + k + i) * step + kBlockRows * 8)[r * (kHeadDim / 4) + lane];
+          else g[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o.x = fmaf(g[i], x[i].x, o.x);
+          o.y = fmaf(g[i], x[i].y, o.y);
+          o.z = fmaf(g[i], x[i].z, o.z);
+          o.w = fmaf(g[i], x[i].w, o.w);
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const WindowReq rq = plan_reqs(kp)[mg.req];
