@@ -31,6 +31,7 @@
 // Where few tiles would leave SMs idle, the plan cuts their pages into parts, whose partial results
 // window_merge_kernel joins, in a fixed order.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -525,25 +526,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t f = nv + 2 * ((j - first) / 2), st = f % kStages;
           done &= wait(ctl->full[st], f / kStages);
           uint4* page = reinterpret_cast<uint4*>(smem + kOffStages + st * kStageBytes + (j & 1) * (kHalf / 2)) + r;
-#pragma unroll 4
-          for (int k = 0; k < 8; ++k) {  // 512 chunks of 64 channels, then as many of the others
-            uint4* at = page + (k >> 2) * (kHalf / 16) + (k & 3) * kBlockRows;
-            const uint4 v = *at;
-            uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            bool bad = false;
+          // 512 chunks of 64 channels, then as many of the others; 0 times an infinity or NaN is NaN
+          __nv_bfloat162 sum = __float2bfloat162_rn(0.f);
+          const __nv_bfloat162 zero = sum;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool lo = (x[e] & 0x7f80u) == 0x7f80u, hi = (x[e] & 0x7f800000u) == 0x7f800000u;
-              bad |= lo | hi;
-              x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-            }
-            if (bad) {
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = page[(k >> 2) * (kHalf / 16) + (k & 3) * kBlockRows];
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]), zero, sum);
+          }
+          if (*reinterpret_cast<const uint32_t*>(&sum) & 0x7fff7fffu) {
+            const uint64_t seen = w.seen(j, first_pos, last_pos);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              uint32_t* at = reinterpret_cast<uint32_t*>(page + (k >> 2) * (kHalf / 16) + (k & 3) * kBlockRows);
               const int t = ((k & 3) * kBlockRows + r) / 8;  // eight chunks a token
-              if ((w.seen(j, first_pos, last_pos) >> t) & 1ull) {  // (not what lies behind the last token)
-                *reinterpret_cast<volatile int*>(&ctl->odd) = 1;  // first: the other block may find only the zeros
-                __threadfence_block();
+#pragma unroll 1
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x = at[e];
+                const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+                if (!lo && !hi) continue;
+                if ((seen >> t) & 1ull) {  // (not what lies behind the last token)
+                  *reinterpret_cast<volatile int*>(&ctl->odd) = 1;  // first: the other block may find only the zeros
+                  __threadfence_block();
+                }
+                at[e] = x & (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
               }
-              *at = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
           fence_proxy_async();
