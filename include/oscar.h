@@ -314,7 +314,7 @@ oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const vo
  * oscar_window_workspace_bytes for the current plan, _max_bytes for every plan (as captured
  * launches need it, which may be replayed under any later plan).  Values of tokens that no
  * query attends are not used, and infinities and NaN reach only queries that attend them.  With
- * several queries a request, weights enter the product with the values as bf16; values below 2^95.
+ * several queries a request, weights enter the product with the values as bf16; values below 2^78.
  * The current device must be the cache's. */
 oscar_status oscar_plan_window(oscar_cache* cache, const int* slots, const int* n_queries, int n_req, int n_sink,
                                int window, void* stream);

@@ -24,10 +24,12 @@
 // row's 0 into NaN in the product, so it is replaced by 0 there, and added to the rows that do see
 // it when O is complete (weights are positive, so the sum is that infinity or NaN).
 //
-// Roles, as in the launch of shared prefixes: warp 0 copies pages (TMA, a ring of five stages of 32
-// KB, keys and values in turn), warp 1 issues the products of S and warp 2 those of O, warps 4-7 and
-// 8-11 are the softmax of the two blocks.  P of a step lies over its S, and S of the next is
-// computed when O of this one is: while a block is at its softmax the tensor core works for the other.
+// Roles: warp 0 copies pages (TMA, a ring of five stages of 32 KB: the keys and the values of two
+// pages in turn), warps 1 and 2 issue the products of S of the two blocks, 4 and 5 those of O, and
+// 8-11 and 12-15 are the blocks' softmax, one thread a row.   S of a page is in
+// one of two buffers of 64 columns, P over it, so that S of the next page and O of the last one are
+// computed beside a page's softmax.  An item of at most 128 rows has its even pages in one block
+// and its odd ones in the other, each with results of its own.
 // Where few tiles would leave SMs idle, the plan cuts their pages into parts, whose partial results
 // window_merge_kernel joins, in a fixed order.
 #include <cuda.h>
@@ -151,18 +153,21 @@ constexpr int kStageBytes = kStep * kHeadDim * 2;      // keys or values of a st
 constexpr int kHalf = kStageBytes / 2;                 // of 64 channels
 constexpr int kBlockRows = 128;
 constexpr int kQBlock = kBlockRows * kHeadDim * 2;
-constexpr int kThreads = 384;
-static_assert(kWindowRows == 2 * kBlockRows, "warps 4-7 and 8-11");
+constexpr int kThreads = 512;
+static_assert(kWindowRows == 2 * kBlockRows, "warps 8-11 and 12-15");
+// Registers of a thread: 128 at the launch, then as the roles need them, the same in all.
+constexpr int kRegsControl = 72, kRegsSoftmax = 184;
+static_assert(2 * 128 * (kRegsControl + kRegsSoftmax) <= kThreads * 128, "registers of the launch");
 
 struct Control {
-  // Stage s's completion n is its n-th filling (leaving).
+  // Stage s's completion n is its n-th filling (leaving, which both blocks' warps report).
   uint64_t full[kStages], empty[kStages];
   // Completion n is item n of those in which the block has rows.
   uint64_t q_full[2];
   // Page n of the block has buffer n % 2, whose completion is n / 2: S is written, P is written, O
   // holds the pages up to n (and P is read).
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
-  uint64_t drain[2];
+  uint64_t drain[4];
   uint32_t tmem;
   int abort;
   int odd;  // an infinity or NaN was met among values that not every row of a tile sees (in any of the CTA's)
@@ -175,8 +180,7 @@ static_assert(kTileSmem <= 227 * 1024, "shared memory of a CTA");
 // Tensor-memory columns of block b: two buffers of S of 64 (P over the first 32 of each), O of 128.
 constexpr uint32_t kBlockCols = 256, kColO = 128;
 
-constexpr float kRaise = 16.f;
-constexpr int kSpins = 1024;
+constexpr float kRaise = 32.f;
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -211,15 +215,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -281,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
-      mbar_init(smem_u32(&ctl->empty[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl->q_full[b]), kBlockRows);
@@ -291,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&ctl->o_done[b][i]), 1);
       }
       mbar_init(smem_u32(&ctl->drain[b]), 1);
+      mbar_init(smem_u32(&ctl->drain[2 + b]), 1);
     }
     ctl->abort = ctl->odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -320,15 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.blocks = (w.it.split ? w.end_page() - w.first_page() > 1 : w.rows > kBlockRows) ? 2 : 1;
     return w;
   };
-  // Bounded wait of a whole warp for completions of one or two barriers (index: of the
-  // completion); lane 0 polls the first, lane 1 the second, without being suspended for the first
-  // kSpins polls (a suspended thread takes some hundred cycles to wake, and every step has three
-  // such hand-overs one after the other).  Each lane has its own poll's result: the roles vote once a
-  // page, where the warp meets anyway, so after a wait that ran out MMAs and stores of that page
-  // still go out, on memory of this CTA, and every role then leaves its loop.
-  auto poll = [&](uint32_t a, uint32_t par) -> int {
-    int done = 0;
-    for (int i = 0; i < kSpins && !done; ++i) done = mbar_test_wait(a, par);
+  // Bounded wait of a whole warp for a barrier's completion `index`.  Every lane polls: one lane's
+  // polls, with the warp brought together behind them, cost some 300 cycles of each of a page's three
+  // hand-overs (2432 queries on 8192 tokens: 292 against 188 us).  After a wait that ran out MMAs
+  // and stores of that page still go out, on memory of this CTA; the roles vote once a page, and
+  // every role then leaves its loop.
+  auto wait = [&](uint64_t& bar, uint32_t index) -> int {
+    const uint32_t a = smem_u32(&bar), par = index & 1u;
+    int done = mbar_try_wait(a, par);
     for (uint32_t i = 0; i < kWaitPolls && !done; ++i) {
       done = mbar_try_wait_for(a, par, 1000000u);
       if (!done && *reinterpret_cast<volatile int*>(&ctl->abort)) break;
@@ -339,20 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return done;
   };
-  auto wait2 = [&](uint64_t& bar0, uint32_t index0, uint64_t& bar1, uint32_t index1) -> int {
-    int done = 1;
-    if (lane < 2) done = poll(lane ? smem_u32(&bar1) : smem_u32(&bar0), (lane ? index1 : index0) & 1u);
-    __syncwarp();
-    return done;
-  };
-  auto wait = [&](uint64_t& bar, uint32_t index) -> int {
-    int done = 1;
-    if (lane == 0) done = poll(smem_u32(&bar), index & 1u);
-    __syncwarp();
-    return done;
-  };
   auto all = [](int done) -> bool { return __all_sync(0xffffffffu, done); };
 
+  if (warp < 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
   if (warp == 0) {
     // ---------------------------------------------------------------- pages
     uint32_t n = 0, issued = 0;  // fillings of stages: keys and values of each step in turn
@@ -395,66 +380,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok)  // copies still in flight land first, too
       for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
         mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- S = Q K^T
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------------------------------- S = Q K^T of block b
+    const int b = warp - 1;
     constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
-    const uint64_t qd = tmem::sdesc_sw128(sq, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
-    uint32_t f = 0, q0 = 0, q1 = 0, n0 = 0, n1 = 0;  // fillings; items and pages of each block
+    const uint64_t qb = tmem::sdesc_sw128(sq + b * kQBlock, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
+    uint32_t f = 0, items_done = 0, n = 0;  // fillings; items and pages of the block
     bool ok = true;
     for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
-      ok = all(wait(ctl->q_full[0], q0++));
-      if (ok && w.blocks > 1) ok = all(wait(ctl->q_full[1], q1++));
-      const int end = w.end_page();
-      for (int j = w.first_page(); ok && j < end; ++j) {
+      const bool here = b < w.blocks;
+      if (here) ok = all(wait(ctl->q_full[b], items_done++));
+      for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
         const uint32_t st = f % kStages;
-        const bool leaves = (j & 1) || j == end - 1;
-        const int b0 = w.it.split ? j & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
-        for (int b = b0; ok && b < b1; ++b) {
-          const uint32_t n = b ? n1++ : n0++, buf = n & 1u;
-          int done = 1;
-          const bool fresh = b == b0 && !(j & 1);
-          if (fresh && n >= 2) done = wait2(ctl->full[st], f / kStages, ctl->o_done[b][buf], (n >> 1) - 1);
-          else if (fresh) done = wait(ctl->full[st], f / kStages);
-          else if (n >= 2) done = wait(ctl->o_done[b][buf], (n >> 1) - 1);
+        const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
+        ok = all(wait(ctl->full[st], f / kStages));
+        if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
+        for (int j = j0; ok && j < j1; ++j, ++n) {
+          const uint32_t buf = n & 1u;
+          const int done = n >= 2 ? wait(ctl->o_done[b][buf], (n >> 1) - 1) : 1;
           tmem::fence_after();
           if (elect_one()) {
             const uint32_t d = tm + b * kBlockCols + buf * kPage;
-            const uint64_t qb = qd + b * (kQBlock >> 4), kb = kd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
+            const uint64_t kb = kd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               tmem::mma_ss(d, qb + ((c >> 2) * (kQBlock / 2) + (c & 3) * 32) / 16, kb + ((c >> 2) * kHalf + (c & 3) * 32) / 16,
                            kIdS, c > 0);
             tmem::commit(smem_u32(&ctl->s_full[b][buf]));
-            if (leaves && b == b1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
           }
           ok = all(done);
         }
-        if (leaves) f += 2;
       }
     }
     if (!ok) {  // MMAs in flight end before the tensor memory is freed
-      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[0]));
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[b]));
       __syncwarp();
-      mbar_wait(smem_u32(&ctl->drain[0]), 0);
+      mbar_wait(smem_u32(&ctl->drain[b]), 0);
     }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- O += P V
+  } else if (warp == 4 || warp == 5) {
+    // ---------------------------------------------------------------- O += P V of block b
+    const int b = warp - 4;
     constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
     const uint64_t vd = tmem::sdesc_sw128(sst, kHalf, 1024);
-    uint32_t f = 1, n0 = 0, n1 = 0;
+    uint32_t f = 1, n = 0;
     bool ok = true;
     for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
-      const int end = w.end_page();
-      for (int j = w.first_page(); ok && j < end; ++j) {
+      const bool here = b < w.blocks;
+      for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
         const uint32_t st = f % kStages;
-        const bool leaves = (j & 1) || j == end - 1;
-        const int b0 = w.it.split ? j & 1 : 0, b1 = w.it.split ? b0 + 1 : w.blocks;
-        for (int b = b0; ok && b < b1; ++b) {
-          const uint32_t n = b ? n1++ : n0++, buf = n & 1u;
-          const int done = b == b0 && !(j & 1) ? wait2(ctl->full[st], f / kStages, ctl->p_full[b][buf], n >> 1)
-                                              : wait(ctl->p_full[b][buf], n >> 1);
+        const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
+        ok = all(wait(ctl->full[st], f / kStages));
+        if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
+        for (int j = j0; ok && j < j1; ++j, ++n) {
+          const uint32_t buf = n & 1u;
+          const int done = wait(ctl->p_full[b][buf], n >> 1);
           tmem::fence_after();
           if (elect_one()) {
             const uint32_t a = tm + b * kBlockCols + buf * kPage, d = tm + b * kBlockCols + kColO;
@@ -462,21 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, j > w.page0(b) || c > 0);
             tmem::commit(smem_u32(&ctl->o_done[b][buf]));
-            if (leaves && b == b1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
           }
           ok = all(done);
         }
-        if (leaves) f += 2;
       }
     }
     if (!ok) {
-      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[1]));
+      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[2 + b]));
       __syncwarp();
-      mbar_wait(smem_u32(&ctl->drain[1]), 0);
+      mbar_wait(smem_u32(&ctl->drain[2 + b]), 0);
     }
-  } else if (warp >= 4) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---------------------------------------------------------------- softmax of block b
-    const int b = (warp - 4) >> 2, wq = warp & 3, r = (wq << 5) | lane;
+    const int b = (warp - 8) >> 2, wq = warp & 3, r = (wq << 5) | lane;
     const float scale = kLog2e * rsqrtf(float(kHeadDim));
     const uint32_t tl = tm + b * kBlockCols + (uint32_t(32 * wq) << 16);
     uint32_t n = 0, nv = 1;  // pages of this block; fillings up to the item's first values
