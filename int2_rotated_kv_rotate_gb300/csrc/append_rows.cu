@@ -14,8 +14,11 @@
 //
 // 4 bits, per token and group of 32 or 128 channels: s = bf16((max - min) / 15), z = bf16(min)
 // (exact), code = clamp(rint((x - z) / s), 0, 15), every operation in fp32, 0 where s = 0.  The
-// quotient is taken as a product with 1 / s, which is off by 3 units in the last place at most;
-// where it falls so near to a half that this could matter, the division itself decides.
+// quotient is taken as a product with an approximate 1 / s, off by 4 units in the last place at most;
+// where it falls so near to a half that this could matter, the division itself decides.  The extremes
+// are found on packed bf16, the rest in pairs of fp32 (plain fp32 operations took 42 us for the 8192 tokens of
+// 8 kv-heads that take @A@ now).
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,7 +34,8 @@ namespace {
 
 constexpr int kBatch = 4;       // rows that a half-warp loads before it stores the first
 constexpr int kItemRows = 16;   // of an append item at most
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 256;
+constexpr int kPerSM = 4;
 
 // Values past this count as it (and NaN as it): differences and their fifteenths stay finite.
 constexpr float kInt4Limit = 8.507059173023462e37f;  // 2^126
@@ -56,9 +60,46 @@ __device__ __forceinline__ void store8(uint16_t* p, uint4 v, bool vec) {
   }
 }
 
-// The 8 channels of each of a half-warp's 16 lanes as codes (one word a lane) and the scale and
-// zero point of the lane's group.  lanes: 4 or 16, those of a group.
-__device__ __forceinline__ uint32_t quantize8(uint4 v, int lanes, unsigned mask, uint32_t& sz) {
+// Two floats in one register pair, and operations on both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// Larger of each half, NaN where either is.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The definition as it stands, of the 8 channels of each of a half-warp's 16 lanes: codes (one word
+// a lane) and the scale and zero point of the lane's group.  lanes: 4 or 16, those of a group.
+__device__ __forceinline__ uint2 quantize8_plain(uint4 v, int lanes, unsigned mask) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float x[8];
   float lo = kInt4Limit, hi = -kInt4Limit;
@@ -74,30 +115,89 @@ __device__ __forceinline__ uint32_t quantize8(uint4 v, int lanes, unsigned mask,
   }
   const uint16_t s16 = bf16_rne(__fdiv_rn(hi - lo, 15.f));
   const float s = bf16_f32(s16);
-  sz = uint32_t(s16) | (__float_as_uint(lo) & 0xffff0000u);  // (lo is one of the bf16 values, or 2^126)
   uint32_t codes = 0;
   if (s > 0.f) {
-    const float inv = __fdiv_rn(1.f, s);
-    bool near_half = !(inv < INFINITY);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = (x[i] - lo) * inv, c = rintf(t);
-      near_half |= fabsf(t - c) > 0.5f - 1.52587890625e-5f;  // 2^-16: 16 * 3 units of 2^-24, and as much again
-      codes |= uint32_t(fminf(fmaxf(c, 0.f), 15.f)) << (4 * i);
-    }
-    if (near_half) {
-      codes = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        codes |= uint32_t(fminf(fmaxf(rintf(__fdiv_rn(x[i] - lo, s)), 0.f), 15.f)) << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i) codes |= uint32_t(fminf(fmaxf(rintf(__fdiv_rn(x[i] - lo, s)), 0.f), 15.f)) << (4 * i);
   }
-  return codes;
+  return make_uint2(codes, uint32_t(s16) | (__float_as_uint(lo) & 0xffff0000u));  // (lo is one of the values, or 2^126)
 }
 
-template <bool INT4, bool ROPE>
-__global__ void __launch_bounds__(kMaxThreads, 2) append_rows_kernel(KernelParams kp, int layer, AppendRowsParams p) {
-  extern __shared__ __align__(16) float2 table[];  // [kItemRows][pairs], see slot()
+// The same, for groups without NaN or values past the limit and with a scale that is normal or 0.
+__device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t up = w[0], down = w[0] ^ 0x80008000u;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    up = max_bf16x2(up, w[i]);
+    down = max_bf16x2(down, w[i] ^ 0x80008000u);
+  }
+  uint32_t ends = max_bf16x2(permute(up, down, 0x5410), permute(up, down, 0x7632));  // (maximum, -minimum)
+  ends = max_bf16x2(ends, __shfl_xor_sync(mask, ends, 1));
+  ends = max_bf16x2(ends, __shfl_xor_sync(mask, ends, 2));
+  if (lanes == 16) {
+    ends = max_bf16x2(ends, __shfl_xor_sync(mask, ends, 4));
+    ends = max_bf16x2(ends, __shfl_xor_sync(mask, ends, 8));
+  }
+  const float hi = bf16_lo(ends), neg_lo = bf16_hi(ends);
+  // (a product with 1 / 15 is off by 2 units in the last place at most: where that could cross a
+  // midpoint of bf16, the division decides)
+  const float span = hi + neg_lo;
+  float fifteenth = span * (1.f / 15.f);
+  if (((__float_as_uint(fifteenth) + 4u) & 0xffffu) - 0x8000u <= 8u) fifteenth = __fdiv_rn(span, 15.f);
+  const uint16_t s16 = uint16_t(pack_bf16(fifteenth, 0.f));
+  constexpr uint32_t kLimit16 = 0x7e80u;  // 2^126
+  const bool odd = (ends & 0x7fffu) > kLimit16 || ((ends >> 16) & 0x7fffu) > kLimit16 || (s16 != 0 && s16 < 0x0080u);
+  if (__any_sync(mask, odd)) return quantize8_plain(v, lanes, mask);
+  const uint32_t sz = uint32_t(s16) | ((ends & 0xffff0000u) ^ 0x80000000u);
+  if (s16 == 0) return make_uint2(0u, sz);
+  const float s = bf16_f32(s16);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));  // at most 1 unit in the last place off
+  // t in [0, 15 (1 + 2^-8)]: its nearest whole number is in the low bits of t + 1.5 * 2^23
+  constexpr float kMagic = 12582912.f;
+  const uint64_t neg_lo2 = pair(neg_lo, neg_lo), inv2 = pair(inv, inv), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic),
+                 minus_one = pair(-1.f, -1.f);
+  uint32_t c[8];
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = mul2(add2(pair(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2), inv2);
+    const uint64_t m = add2(t, magic);
+    const float2 off = unpair(fma2(add2(m, unmagic), minus_one, t));
+    far = fmaxf(far, fmaxf(fabsf(off.x), fabsf(off.y)));
+    const float2 bits = unpair(m);
+    c[2 * i] = __float_as_uint(bits.x);
+    c[2 * i + 1] = __float_as_uint(bits.y);
+  }
+  if (far > 0.5f - 1.52587890625e-5f) {  // 2^-16: more than 16 * 4 units of 2^-24
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+      codes |= uint32_t(fminf(fmaxf(rintf(__fdiv_rn(x + neg_lo, s)), 0.f), 15.f)) << (4 * i);
+    }
+    return make_uint2(codes, sz);
+  }
+  // the low bytes of the even and of the odd channels
+  const uint32_t even = permute(permute(c[0], c[2], 0x0040), permute(c[4], c[6], 0x0040), 0x5410);
+  const uint32_t odds = permute(permute(c[1], c[3], 0x0040), permute(c[5], c[7], 0x0040), 0x5410);
+  return make_uint2(even + 16u * odds, sz);
+}
+
+// How a lane finds the partners of its 8 channels: no turning; another lane's 8 (half layout,
+// rotary_dim a multiple of 16); its own (interleaved); anywhere in the row.
+enum Turn { kNoTurn, kLanes, kAdjacent, kAnywhere };
+
+template <bool INT4, Turn TURN>
+__global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(KernelParams kp, int layer, AppendRowsParams p) {
+  // The table, as the lanes multiply: a row's turned channels are X cx + (Y cy), the product in
+  // brackets rounded first.  kLanes: X, Y are a channel of the first half and its partner of the
+  // second, or the other way round, and two channels' factors (cx, cx, cy, cy) are 16 bytes, (cos,
+  // cos, -sin, -sin) for the first half and (sin, sin, cos, cos) for the second, those of the lanes side
+  // by side.  kAdjacent: X, Y are the two channels of a pair, and (cos, sin, -sin, cos) gives both.
+  // kAnywhere: (cos, sin) of each pair.
+  extern __shared__ __align__(16) float table[];  // [kItemRows][row_words]
   const int n_items = reinterpret_cast<const int*>(kp.base + kp.lay.append_counts)[0];
   const int l16 = threadIdx.x & 15, c0 = 8 * l16;
   const unsigned mask = 0xffffu << (threadIdx.x & 16);
@@ -110,13 +210,28 @@ __global__ void __launch_bounds__(kMaxThreads, 2) append_rows_kernel(KernelParam
                        (kind == 0 ? h * p.q.in_head : kind == 1 ? h * p.k_head : h * p.v_head) + c0;
   const long long in_row = kind == 0 ? p.q.in_row : kind == 1 ? p.k_row : p.v_row;
   const bool in_vec = kind == 0 ? p.q_in_vec : kind == 1 ? p.k_vec : p.v_vec;
-  const int R = p.rotary_dim, pairs = R / 2;
-  // the pairs in twos of 16 bytes; the twos of a lane's channels 8 of them apart (half layout) or
-  // side by side, so that lanes read different banks
-  auto slot = [&](int r, int pair) {
-    if (p.interleaved || (pairs & 7)) return r * pairs + pair;
-    return r * pairs + (((pair >> 1) & 3) * (pairs >> 3) + (pair >> 3)) * 2 + (pair & 1);
-  };
+  const int R = p.rotary_dim, pairs = R / 2, eighth = pairs >> 3;
+  const int row_words = TURN == kAnywhere ? 2 * pairs : 4 * pairs;  // floats a row
+  const bool turns = TURN != kNoTurn && kind != 2 && (TURN == kAnywhere || c0 < R);
+  const bool first = c0 < pairs;
+  const int other = TURN != kLanes || c0 >= R ? l16 : first ? l16 + eighth : l16 - eighth;
+  const float* factors = table + (TURN == kLanes ? 4 * (first ? l16 : l16 - eighth + pairs / 2) : TURN == kAdjacent ? 2 * c0 : 0);
+  // the head's keys or values in page 0 of the layer
+  uint8_t* pool = kp.base;
+  uint32_t* sz_pool = nullptr;
+  if (kind != 0) {
+    if constexpr (!INT4) {
+      pool += kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride + size_t(h) * kp.lay.bf16_head_stride +
+              size_t(kind - 1) * (kPage * kHeadDim * 2) + 16 * l16;
+    } else {
+      pool += kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride +
+              size_t(kind - 1) * (kPage * kInt4Row);
+      sz_pool = reinterpret_cast<uint32_t*>(kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride +
+                                            size_t(h) * kp.lay.sz_head_stride +
+                                            size_t(kind - 1) * (kPage * (kHeadDim / kp.group) * 4));
+    }
+  }
+  const unsigned page_stride = unsigned(INT4 ? kp.lay.codes_page_stride : kp.lay.bf16_page_stride);
   bool waited = false;
   for (int ix = blockIdx.x; ix < n_items; ix += gridDim.x) {
     const AppendItem it = reinterpret_cast<const AppendItem*>(kp.base + kp.lay.append_items)[ix];
@@ -125,19 +240,30 @@ __global__ void __launch_bounds__(kMaxThreads, 2) append_rows_kernel(KernelParam
     if (!slot_ok && threadIdx.x == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
     const long long row0 = (long long)a.x_offset + it.begin - a.L0;
     if (waited) __syncthreads();  // the table of the item before is read
-    if (!waited && (!ROPE || p.positions)) {
+    if (!waited && (TURN == kNoTurn || p.positions)) {
       pdl_wait();
       pdl_trigger();
       waited = true;
     }
-    if constexpr (ROPE) {  // (the plan is older than the preceding kernel: places may be turned before the wait)
+    if constexpr (TURN != kNoTurn) {  // (the plan is older than the preceding kernel: places may be turned before the wait)
       for (int e = threadIdx.x; e < it.count * pairs; e += blockDim.x) {
         const int r = e / pairs, i = e - r * pairs;
         const long long pos = !p.positions ? (long long)(it.begin + r)
                               : p.positions64 ? reinterpret_cast<const long long*>(p.positions)[row0 + r]
                                               : (long long)(reinterpret_cast<const int*>(p.positions)[row0 + r]);
         const float2 cs = turn(uint64_t(pos) * p.steps[i]);
-        table[slot(r, i)] = make_float2(cs.x * p.magnitude, cs.y * p.magnitude);
+        const float c = cs.x * p.magnitude, si = cs.y * p.magnitude;
+        float* row = table + r * row_words;
+        if (TURN == kAdjacent) {
+          reinterpret_cast<float4*>(row)[i] = make_float4(c, si, -si, c);
+        } else if (TURN == kLanes) {  // channels 8 u + 2 j, + 1 of a half: twos (half, j, u)
+          float* a0 = row + 4 * (((i >> 1) & 3) * eighth + (i >> 3)) + (i & 1);
+          float* b0 = a0 + 2 * pairs;
+          a0[0] = c, a0[2] = -si;
+          b0[0] = si, b0[2] = c;
+        } else {
+          reinterpret_cast<float2*>(row)[i] = make_float2(c, si);
+        }
       }
       if (!waited) {
         pdl_wait();
@@ -147,98 +273,108 @@ __global__ void __launch_bounds__(kMaxThreads, 2) append_rows_kernel(KernelParam
       __syncthreads();
     }
     if (!mine || !slot_ok) continue;
-    const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(a.slot) * kp.max_pages_per_request;
-    const uint16_t* src = in + row0 * in_row;
-    for (int r0 = 0; r0 < it.count; r0 += kBatch, src += kBatch * in_row) {
-      uint4 x[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (r0 + b < it.count) x[b] = load8(src + b * in_row, in_vec);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int r = r0 + b;
-        if (r >= it.count) break;
-        uint4 v = x[b];
-        if (ROPE && kind != 2) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, y[4] = {0u, 0u, 0u, 0u};
-          if (p.interleaved) {
+    // Where the rows go: the item's lie in one page or two.
+    const int t0 = it.begin % kPage, crossing = kPage - t0;
+    uint8_t *to = pool, *to_next = pool;
+    uint32_t *sz_to = sz_pool, *sz_next = sz_pool;
+    long long to_row = kHeadDim * 2;  // bytes from row to row (4-bit rows are found by their token)
+    bool ok = true, ok_next = true;
+    if (kind == 0) {
+      to = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.q.out) + row0 * p.q.out_row + h * p.q.out_head + c0);
+      to_row = 2 * p.q.out_row;
+    } else {
+      const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(a.slot) * kp.max_pages_per_request;
+      const int lp = it.begin / kPage;
+      const int page = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+      const int next = it.count <= crossing ? page : lp + 1 < kp.max_pages_per_request ? ptab[lp + 1] : -1;
+      ok = page >= 0 && page < kp.max_pages;
+      ok_next = next >= 0 && next < kp.max_pages;
+      if (l16 == 0 && !(ok && ok_next)) flag(kp, OSCAR_FLAG_BAD_PAGE);
+      to += size_t(unsigned(ok ? page : 0)) * page_stride;
+      to_next += size_t(unsigned(ok_next ? next : 0)) * page_stride;
+      if constexpr (INT4) {
+        const unsigned sz_stride = unsigned(kp.lay.sz_page_stride / 4);
+        sz_to += size_t(unsigned(ok ? page : 0)) * sz_stride;
+        sz_next += size_t(unsigned(ok_next ? next : 0)) * sz_stride;
+      } else {
+        to += t0 * (kHeadDim * 2);
+        to_next -= crossing * (kHeadDim * 2);
+      }
+    }
+    auto put = [&](int r, uint4 v) {
+      if (TURN != kNoTurn && kind != 2) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (TURN == kAdjacent) {
+          if (turns) {
+            const float4* at = reinterpret_cast<const float4*>(factors + r * row_words);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (c0 + 2 * i < R) {
-                const float2 cs = table[slot(r, c0 / 2 + i)];
+                const float4 f = at[i];
                 const float u = bf16_lo(w[i]), t = bf16_hi(w[i]);
-                w[i] = pack_bf16(fmaf(u, cs.x, -(t * cs.y)), fmaf(u, cs.y, t * cs.x));
+                const float2 o = unpair(fma2(pair(u, u), pair(f.x, f.y), mul2(pair(t, t), pair(f.z, f.w))));
+                w[i] = pack_bf16(o.x, o.y);
               }
-          } else if (!(pairs & 7)) {
-            const bool first = c0 < pairs;
-            const int other = c0 >= R ? l16 : first ? l16 + (pairs >> 3) : l16 - (pairs >> 3);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(mask, w[i], other, 16);
-            if (c0 < R) {
-              const int pair0 = first ? c0 : c0 - pairs;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 cs = *reinterpret_cast<const float4*>(&table[slot(r, pair0 + 2 * i)]);
-                const float u0 = bf16_lo(w[i]), u1 = bf16_hi(w[i]), t0 = bf16_lo(y[i]), t1 = bf16_hi(y[i]);
-                // (a cos - (b sin) in the first half, a sin + (b cos) in the second: the one in
-                // brackets is rounded first)
-                w[i] = pack_bf16(first ? fmaf(u0, cs.x, -(t0 * cs.y)) : fmaf(t0, cs.y, u0 * cs.x),
-                                 first ? fmaf(u1, cs.z, -(t1 * cs.w)) : fmaf(t1, cs.w, u1 * cs.z));
-              }
-            }
-          } else {  // partners anywhere in the row: read one by one, before any lane stores (q may be turned in place)
-            const uint16_t* row = src + b * in_row - c0;
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int c = c0 + i;
-              o[i] = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-              if (c < R) {
-                const bool first = c < pairs;
-                const float2 cs = table[slot(r, first ? c : c - pairs)];
-                const float t = bf16_f32(row[first ? c + pairs : c - pairs]);
-                o[i] = first ? fmaf(o[i], cs.x, -(t * cs.y)) : fmaf(t, cs.y, o[i] * cs.x);
-              }
-            }
-            __syncwarp(mask);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = c0 + 2 * i < R ? pack_bf16(o[2 * i], o[2 * i + 1]) : w[i];
           }
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (kind == 0) {
-          store8(static_cast<uint16_t*>(p.q.out) + (row0 + r) * p.q.out_row + h * p.q.out_head + c0, v, p.q_out_vec);
-          continue;
-        }
-        const int pos = it.begin + r, lp = pos / kPage;
-        const int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
-        if (phys < 0 || phys >= kp.max_pages) {
-          if (l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
-          continue;
-        }
-        const int t = pos % kPage;
-        if constexpr (!INT4) {
-          uint8_t* dst = kp.base + kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride +
-                         size_t(phys) * kp.lay.bf16_page_stride + size_t(h) * kp.lay.bf16_head_stride +
-                         size_t(kind - 1) * (kPage * kHeadDim * 2) + size_t(t) * (kHeadDim * 2);
-          reinterpret_cast<uint4*>(dst)[l16] = v;
-        } else {
-          const int ng = kHeadDim / kp.group;
-          uint32_t sz;
-          const uint32_t codes = quantize8(v, kp.group / 8, mask, sz);
-          uint8_t* row = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
-                         size_t(phys) * kp.lay.codes_page_stride + size_t(h) * kp.lay.codes_head_stride +
-                         size_t(kind - 1) * (kPage * kInt4Row);
-          *reinterpret_cast<uint32_t*>(row + int4_word(t, l16)) = codes;
-          if (l16 % (kp.group / 8) == 0) {
-            uint32_t* szs = reinterpret_cast<uint32_t*>(
-                kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(phys) * kp.lay.sz_page_stride +
-                size_t(h) * kp.lay.sz_head_stride + size_t(kind - 1) * (kPage * ng * 4));
-            szs[t * ng + l16 / (kp.group / 8)] = sz;
+        } else if constexpr (TURN == kLanes) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(mask, w[i], other, 16);
+          if (turns) {
+            const float4* at = reinterpret_cast<const float4*>(factors + r * row_words);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = at[i * eighth];
+              const uint32_t X = first ? w[i] : y[i], Y = first ? y[i] : w[i];
+              const float2 o = unpair(fma2(pair(bf16_lo(X), bf16_hi(X)), pair(f.x, f.y),
+                                           mul2(pair(bf16_lo(Y), bf16_hi(Y)), pair(f.z, f.w))));
+              w[i] = pack_bf16(o.x, o.y);
+            }
           }
+        } else if constexpr (TURN == kAnywhere) {
+          // read one by one, before any lane stores (q may be turned in place)
+          const uint16_t* from = in + (row0 + r) * in_row - c0;
+          const float2* row = reinterpret_cast<const float2*>(table + r * row_words);
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i;
+            o[i] = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+            if (c < R) {
+              const bool low = c < pairs;
+              const float2 cs = row[low ? c : c - pairs];
+              const float t = bf16_f32(from[low ? c + pairs : c - pairs]);
+              o[i] = low ? fmaf(o[i], cs.x, -(t * cs.y)) : fmaf(t, cs.y, o[i] * cs.x);
+            }
+          }
+          __syncwarp(mask);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = c0 + 2 * i < R ? pack_bf16(o[2 * i], o[2 * i + 1]) : w[i];
         }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      const bool behind = r >= crossing && kind != 0;
+      if (!(behind ? ok_next : ok)) return;  // (flagged above)
+      uint8_t* row = behind ? to_next : to;
+      if (INT4 && kind != 0) {
+        const int t = (t0 + r) % kPage, lanes = kp.group / 8;
+        const uint2 c = quantize8(v, lanes, mask);
+        *reinterpret_cast<uint32_t*>(row + int4_word(t, l16)) = c.x;
+        if (l16 % lanes == 0) (behind ? sz_next : sz_to)[t * (16 / lanes) + l16 / lanes] = c.y;
+      } else {
+        store8(reinterpret_cast<uint16_t*>(row + r * to_row), v, kind != 0 || p.q_out_vec);
+      }
+    };
+    const uint16_t* src = in + row0 * in_row;
+    int r0 = 0;
+    for (; r0 + kBatch <= it.count; r0 += kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b, src += in_row) x[b] = load8(src, in_vec);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) put(r0 + b, x[b]);
     }
+    for (; r0 < it.count; ++r0, src += in_row) put(r0, load8(src, in_vec));
   }
   if (!waited) {
     pdl_wait();
@@ -247,44 +383,59 @@ __global__ void __launch_bounds__(kMaxThreads, 2) append_rows_kernel(KernelParam
 }
 
 // Tokens [begin, end) of a request's 4-bit rows as values: fmaf(code, s, z) in fp32, rounded to bf16
-// where T is 16 bits.  Sixteen lanes a row of a head, the heads of a token side by side (K, then V).
+// where T is 16 bits.  Sixteen lanes a row, a head (K heads, then V heads) a half-warp, which walks
+// down kItemRows tokens, kBatch of them in flight.  HBM-bound.
+constexpr int kReadThreads = 256;
 template <typename T>
-__global__ void __launch_bounds__(256) int4_read_kernel(KernelParams kp, int layer, int slot, int begin, int end,
-                                                        T* __restrict__ k_out, T* __restrict__ v_out) {
+__global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp, int layer, int slot, int begin, int end,
+                                                                T* __restrict__ k_out, T* __restrict__ v_out) {
   pdl_wait();
   pdl_trigger();
   const int l16 = threadIdx.x & 15, ng = kHeadDim / kp.group, Hkv = kp.n_kv_heads;
+  const int head = int(blockIdx.y) * (kReadThreads / 16) + int(threadIdx.x >> 4);
+  if (head >= 2 * Hkv) return;
+  const int kv = head >= Hkv, h = kv ? head - Hkv : head;
   const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(slot) * kp.max_pages_per_request;
-  const long long rows = (long long)(end - begin) * 2 * Hkv;
-  for (long long e = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); e < rows; e += (long long)gridDim.x * 16) {
-    const int hh = int(e % (2 * Hkv)), pos = begin + int(e / (2 * Hkv));
-    const int kv = hh >= Hkv, h = kv ? hh - Hkv : hh, t = pos % kPage;
-    const int lp = pos / kPage;
-    const int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
-    T* out = (kv ? v_out : k_out) + ((long long)(pos - begin) * Hkv + h) * kHeadDim + 8 * l16;
-    float x[8];
-    if (phys < 0 || phys >= kp.max_pages) {
-      if (l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+  const uint8_t* pool = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride +
+                        size_t(kv) * (kPage * kInt4Row);
+  const uint8_t* sz_pool = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(h) * kp.lay.sz_head_stride +
+                           size_t(kv) * (kPage * ng * 4);
+  const int group = l16 / (kp.group / 8);
+  T* out = (kv ? v_out : k_out) + size_t(h) * kHeadDim + 8 * l16;
+  for (int p0 = begin + int(blockIdx.x) * kItemRows; p0 < end; p0 += int(gridDim.x) * kItemRows) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    } else {
-      const uint8_t* row = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
-                           size_t(phys) * kp.lay.codes_page_stride + size_t(h) * kp.lay.codes_head_stride +
-                           size_t(kv) * (kPage * kInt4Row);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + int4_word(t, l16));
-      const uint32_t sz = reinterpret_cast<const uint32_t*>(
-          kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(phys) * kp.lay.sz_page_stride +
-          size_t(h) * kp.lay.sz_head_stride + size_t(kv) * (kPage * ng * 4))[t * ng + l16 / (kp.group / 8)];
-      const float s = bf16_lo(sz), z = bf16_hi(sz);
+    for (int r = 0; r < kItemRows; r += kBatch) {
+      uint32_t w[kBatch], sz[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(float((w >> (4 * i)) & 15u), s, z);
-    }
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(out) =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-    } else {
-      reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+      for (int b = 0; b < kBatch; ++b) {
+        const int pos = p0 + r + b, lp = pos / kPage, t = pos % kPage;
+        w[b] = sz[b] = 0u;
+        if (pos >= end) continue;
+        const int page = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+        if (page < 0 || page >= kp.max_pages) {  // zeros, and the flag
+          if (l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+          continue;
+        }
+        w[b] = *reinterpret_cast<const uint32_t*>(pool + size_t(unsigned(page)) * unsigned(kp.lay.codes_page_stride) + int4_word(t, l16));
+        sz[b] = reinterpret_cast<const uint32_t*>(sz_pool + size_t(unsigned(page)) * unsigned(kp.lay.sz_page_stride))[t * ng + group];
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int pos = p0 + r + b;
+        if (pos >= end) continue;
+        const float s = bf16_lo(sz[b]), z = bf16_hi(sz[b]);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(float((w[b] >> (4 * i)) & 15u), s, z);
+        T* to = out + size_t(pos - begin) * (size_t(Hkv) * kHeadDim);
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(to) =
+              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        } else {
+          reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+          reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+      }
     }
   }
 }
@@ -298,22 +449,24 @@ int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bo
   const int chunks = (H + most - 1) / most;
   p.chunk_heads = ((H + chunks - 1) / chunks + 1) / 2 * 2;
   const dim3 grid(n_items, chunks), block(16 * p.chunk_heads);
-  const size_t smem = rope ? size_t(kItemRows) * (p.rotary_dim / 2) * sizeof(float2) : 0;
+  const size_t smem = rope ? size_t(kItemRows) * (p.rotary_dim / 2) * sizeof(float4) : 0;
+  auto go = [&](auto kernel) { return launch_ex(kernel, grid, block, smem, stream, kp, layer, p); };
   int e;
-  if (int4) e = rope ? launch_ex(append_rows_kernel<true, true>, grid, block, smem, stream, kp, layer, p)
-                     : launch_ex(append_rows_kernel<true, false>, grid, block, smem, stream, kp, layer, p);
-  else e = launch_ex(append_rows_kernel<false, true>, grid, block, smem, stream, kp, layer, p);
+  if (!rope) e = go(append_rows_kernel<true, kNoTurn>);
+  else if (p.interleaved) e = int4 ? go(append_rows_kernel<true, kAdjacent>) : go(append_rows_kernel<false, kAdjacent>);
+  else if (p.rotary_dim % 16 == 0) e = int4 ? go(append_rows_kernel<true, kLanes>) : go(append_rows_kernel<false, kLanes>);
+  else e = int4 ? go(append_rows_kernel<true, kAnywhere>) : go(append_rows_kernel<false, kAnywhere>);
   if (!e) *launches += 1;
   return e;
 }
 
 int launch_int4_read(const KernelParams& kp, int layer, int slot, int begin, int end, void* k_out, void* v_out, bool f32,
                      int n_sm, void* stream, int* launches) {
-  const long long rows = (long long)(end - begin) * 2 * kp.n_kv_heads;
-  const unsigned grid = unsigned(std::min<long long>((rows + 15) / 16, 16LL * n_sm));
-  const int e = f32 ? launch_ex(int4_read_kernel<float>, dim3(grid), dim3(256), 0, stream, kp, layer, slot, begin, end,
+  const dim3 grid(std::min((end - begin + kItemRows - 1) / kItemRows, 16 * n_sm),
+                  (2 * kp.n_kv_heads + kReadThreads / 16 - 1) / (kReadThreads / 16));
+  const int e = f32 ? launch_ex(int4_read_kernel<float>, grid, dim3(kReadThreads), 0, stream, kp, layer, slot, begin, end,
                                 static_cast<float*>(k_out), static_cast<float*>(v_out))
-                    : launch_ex(int4_read_kernel<uint16_t>, dim3(grid), dim3(256), 0, stream, kp, layer, slot, begin, end,
+                    : launch_ex(int4_read_kernel<uint16_t>, grid, dim3(kReadThreads), 0, stream, kp, layer, slot, begin, end,
                                 static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out));
   if (!e) *launches += 1;
   return e;
