@@ -159,25 +159,31 @@ __device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask) {
   const uint64_t neg_lo2 = pair(neg_lo, neg_lo), inv2 = pair(inv, inv), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic),
                  minus_one = pair(-1.f, -1.f);
   uint32_t c[8];
+  float2 off[4];
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint64_t t = mul2(add2(pair(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2), inv2);
     const uint64_t m = add2(t, magic);
-    const float2 off = unpair(fma2(add2(m, unmagic), minus_one, t));
-    far = fmaxf(far, fmaxf(fabsf(off.x), fabsf(off.y)));
+    off[i] = unpair(fma2(add2(m, unmagic), minus_one, t));
+    far = fmaxf(far, fmaxf(fabsf(off[i].x), fabsf(off[i].y)));
     const float2 bits = unpair(m);
     c[2 * i] = __float_as_uint(bits.x);
     c[2 * i + 1] = __float_as_uint(bits.y);
   }
-  if (far > 0.5f - 1.52587890625e-5f) {  // 2^-16: more than 16 * 4 units of 2^-24
-    uint32_t codes = 0;
+  constexpr float kNear = 0.5f - 1.52587890625e-5f;  // 2^-16: more than 16 * 4 units of 2^-24
+  if (far > kNear) {
+    // a quotient that is a half is one between multiples of s, exactly (13 bits): it goes to the even code
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float x = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-      codes |= uint32_t(fminf(fmaxf(rintf(__fdiv_rn(x + neg_lo, s)), 0.f), 15.f)) << (4 * i);
+      const float o = i & 1 ? off[i / 2].y : off[i / 2].x, d = (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) + neg_lo;
+      if (fabsf(o) > kNear) {
+        const float at = __uint_as_float(c[i]) - kMagic, middle = at + copysignf(0.5f, o);
+        float code = 2.f * rintf(0.5f * middle);  // the even one beside a half
+        if (d != middle * s) code = rintf(__fdiv_rn(d, s));
+        c[i] = __float_as_uint(code + kMagic);
+      }
     }
-    return make_uint2(codes, sz);
   }
   // the low bytes of the even and of the odd channels
   const uint32_t even = permute(permute(c[0], c[2], 0x0040), permute(c[4], c[6], 0x0040), 0x5410);
@@ -402,38 +408,54 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
                            size_t(kv) * (kPage * ng * 4);
   const int group = l16 / (kp.group / 8);
   T* out = (kv ? v_out : k_out) + size_t(h) * kHeadDim + 8 * l16;
+  const size_t row = size_t(Hkv) * kHeadDim;
   for (int p0 = begin + int(blockIdx.x) * kItemRows; p0 < end; p0 += int(gridDim.x) * kItemRows) {
+    const int n = min(kItemRows, end - p0), lp = p0 / kPage, t0 = p0 % kPage;
+    int page[2];  // the rows lie in one page or two
+    page[0] = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+    page[1] = t0 + n <= kPage ? page[0] : lp + 1 < kp.max_pages_per_request ? ptab[lp + 1] : -1;
+    const uint8_t* rows[2];
+    const uint32_t* szs[2];
+    bool ok[2];
 #pragma unroll
-    for (int r = 0; r < kItemRows; r += kBatch) {
+    for (int i = 0; i < 2; ++i) {
+      ok[i] = page[i] >= 0 && page[i] < kp.max_pages;
+      if (!ok[i] && l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+      const unsigned at = unsigned(ok[i] ? page[i] : 0);
+      rows[i] = pool + size_t(at) * unsigned(kp.lay.codes_page_stride);
+      szs[i] = reinterpret_cast<const uint32_t*>(sz_pool + size_t(at) * unsigned(kp.lay.sz_page_stride)) + group;
+    }
+    T* to = out + size_t(p0 - begin) * row;
+#pragma unroll 2
+    for (int r = 0; r < n; r += kBatch) {
       uint32_t w[kBatch], sz[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int pos = p0 + r + b, lp = pos / kPage, t = pos % kPage;
-        w[b] = sz[b] = 0u;
-        if (pos >= end) continue;
-        const int page = lp < kp.max_pages_per_request ? ptab[lp] : -1;
-        if (page < 0 || page >= kp.max_pages) {  // zeros, and the flag
-          if (l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
-          continue;
-        }
-        w[b] = *reinterpret_cast<const uint32_t*>(pool + size_t(unsigned(page)) * unsigned(kp.lay.codes_page_stride) + int4_word(t, l16));
-        sz[b] = reinterpret_cast<const uint32_t*>(sz_pool + size_t(unsigned(page)) * unsigned(kp.lay.sz_page_stride))[t * ng + group];
+        const int t = t0 + r + b;
+        const bool behind = t >= kPage, there = r + b < n && (behind ? ok[1] : ok[0]);  // (else zeros)
+        w[b] = there ? *reinterpret_cast<const uint32_t*>((behind ? rows[1] : rows[0]) + int4_word(t % kPage, l16)) : 0u;
+        sz[b] = there ? (behind ? szs[1] : szs[0])[(t % kPage) * ng] : 0u;
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pos = p0 + r + b;
-        if (pos >= end) continue;
+      for (int b = 0; b < kBatch; ++b, to += row) {
+        if (r + b >= n) break;
         const float s = bf16_lo(sz[b]), z = bf16_hi(sz[b]);
-        float x[8];
+        // a code as the low byte of 2^23: its value by a subtraction
+        const uint32_t even = w[b] & 0x0f0f0f0fu, odd = (w[b] >> 4) & 0x0f0f0f0fu;
+        const uint64_t ss = pair(s, s), zz = pair(z, z), base = pair(-8388608.f, -8388608.f);
+        float2 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(float((w[b] >> (4 * i)) & 15u), s, z);
-        T* to = out + size_t(pos - begin) * (size_t(Hkv) * kHeadDim);
+        for (int i = 0; i < 4; ++i)
+          x[i] = unpair(fma2(add2(pair(__uint_as_float(permute(even, 0x4b000000u, 0x7650 + i)),
+                                       __uint_as_float(permute(odd, 0x4b000000u, 0x7650 + i))),
+                                  base),
+                             ss, zz));
         if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(to) =
-              make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+          *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y),
+                                                     pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
         } else {
-          reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
-          reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+          reinterpret_cast<float4*>(to)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+          reinterpret_cast<float4*>(to)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
         }
       }
     }
