@@ -14,15 +14,16 @@
 //
 // 4 bits, per token and group of 32 or 128 channels: s = bf16((max - min) / 15), z = bf16(min)
 // (exact), code = clamp(rint((x - z) / s), 0, 15), every operation in fp32, 0 where s = 0.  The
-// quotient is taken as a product with an approximate 1 / s, off by 4 units in the last place at most;
-// where it falls so near to a half that this could matter, the division itself decides.  The extremes
-// are found on packed bf16, the rest in pairs of fp32 (plain fp32 operations took 42 us for the 8192 tokens of
-// 8 kv-heads that take @A@ now).
+// extremes are found on packed bf16, the rest in pairs of fp32 by products with approximate
+// reciprocals; the few rows for which that is not known to give the definition's bits are taken
+// again, as it stands, after the item's others.  (With divisions and single operations 8192 tokens of 8
+// kv-heads took 42 us; 21 now, 2.1 TB/s.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "int4.cuh"
@@ -123,8 +124,17 @@ __device__ __forceinline__ uint2 quantize8_plain(uint4 v, int lanes, unsigned ma
   return make_uint2(codes, uint32_t(s16) | (__float_as_uint(lo) & 0xffff0000u));  // (lo is one of the values, or 2^126)
 }
 
-// The same, for groups without NaN or values past the limit and with a scale that is normal or 0.
-__device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask) {
+// The same for most groups; `plain` says that this lane's is not known to be one of them: NaN or
+// values past the limit, a scale below the normal numbers, or near a midpoint of bf16.
+//
+// The codes' quotients: t = d inv, d = fl(x - z), is off by 2^-22 of it at most (inv, which is within a unit in
+// the last place, and the product); a step of residual correction, t + (d - t s) inv, leaves 2^-44 of
+// error before its one rounding.  Only a quotient at or next to a half matters for rint.  Halves (up
+// to 14.5) times s (8 bits) are exact, so d is one, and the step exact; or d differs from it by a unit in its
+// last place or more, and then d / s is at least 2^-8 of a unit away from where its rounding would
+// turn to or from the half (s / 2 times 2^k has 8 bits, so its units are over 2^-24 (1 + 2^-8) of it):
+// the rounded sum falls on the side that the rounded quotient does.
+__device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask, bool& plain) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t up = w[0], down = w[0] ^ 0x80008000u;
 #pragma unroll
@@ -140,55 +150,31 @@ __device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask) {
     ends = max_bf16x2(ends, __shfl_xor_sync(mask, ends, 8));
   }
   const float hi = bf16_lo(ends), neg_lo = bf16_hi(ends);
-  // (a product with 1 / 15 is off by 2 units in the last place at most: where that could cross a
-  // midpoint of bf16, the division decides)
-  const float span = hi + neg_lo;
-  float fifteenth = span * (1.f / 15.f);
-  if (((__float_as_uint(fifteenth) + 4u) & 0xffffu) - 0x8000u <= 8u) fifteenth = __fdiv_rn(span, 15.f);
-  const uint16_t s16 = uint16_t(pack_bf16(fifteenth, 0.f));
-  constexpr uint32_t kLimit16 = 0x7e80u;  // 2^126
-  const bool odd = (ends & 0x7fffu) > kLimit16 || ((ends >> 16) & 0x7fffu) > kLimit16 || (s16 != 0 && s16 < 0x0080u);
-  if (__any_sync(mask, odd)) return quantize8_plain(v, lanes, mask);
-  const uint32_t sz = uint32_t(s16) | ((ends & 0xffff0000u) ^ 0x80000000u);
-  if (s16 == 0) return make_uint2(0u, sz);
-  const float s = bf16_f32(s16);
+  const float fifteenth = (hi + neg_lo) * (1.f / 15.f);  // within 2 units in the last place
+  const uint32_t s16 = pack_bf16(fifteenth, 0.f);
+  const float s = bf16_lo(s16);
+  // (4: units of the fp32 number around a midpoint; ends: 2^126 is 0x7e80; a scale of 0 by a span of 0 is none of them)
+  plain = ((__float_as_uint(fifteenth) + 4u) & 0xffffu) - 0x8000u <= 8u || (ends & 0x7fffu) > 0x7e80u ||
+          (ends & 0x7fff0000u) > 0x7e800000u || (s16 < 0x0080u && fifteenth != 0.f);
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));  // at most 1 unit in the last place off
-  // t in [0, 15 (1 + 2^-8)]: its nearest whole number is in the low bits of t + 1.5 * 2^23
-  constexpr float kMagic = 12582912.f;
-  const uint64_t neg_lo2 = pair(neg_lo, neg_lo), inv2 = pair(inv, inv), magic = pair(kMagic, kMagic), unmagic = pair(-kMagic, -kMagic),
-                 minus_one = pair(-1.f, -1.f);
+  inv = s16 == 0u ? 0.f : inv;                           // the codes of a scale of 0
+  // quotients in [0, 15 (1 + 2^-8)]: the nearest whole number is in the low bits of t + 1.5 * 2^23
+  const uint64_t neg_lo2 = pair(neg_lo, neg_lo), inv2 = pair(inv, inv), neg_s2 = pair(-s, -s), magic = pair(12582912.f, 12582912.f);
   uint32_t c[8];
-  float2 off[4];
-  float far = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t t = mul2(add2(pair(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2), inv2);
-    const uint64_t m = add2(t, magic);
-    off[i] = unpair(fma2(add2(m, unmagic), minus_one, t));
-    far = fmaxf(far, fmaxf(fabsf(off[i].x), fabsf(off[i].y)));
-    const float2 bits = unpair(m);
+    const uint64_t d = add2(pair(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2);
+    uint64_t t = mul2(d, inv2);
+    t = fma2(fma2(t, neg_s2, d), inv2, t);
+    const float2 bits = unpair(add2(t, magic));
     c[2 * i] = __float_as_uint(bits.x);
     c[2 * i + 1] = __float_as_uint(bits.y);
-  }
-  constexpr float kNear = 0.5f - 1.52587890625e-5f;  // 2^-16: more than 16 * 4 units of 2^-24
-  if (far > kNear) {
-    // a quotient that is a half is one between multiples of s, exactly (13 bits): it goes to the even code
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = i & 1 ? off[i / 2].y : off[i / 2].x, d = (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) + neg_lo;
-      if (fabsf(o) > kNear) {
-        const float at = __uint_as_float(c[i]) - kMagic, middle = at + copysignf(0.5f, o);
-        float code = 2.f * rintf(0.5f * middle);  // the even one beside a half
-        if (d != middle * s) code = rintf(__fdiv_rn(d, s));
-        c[i] = __float_as_uint(code + kMagic);
-      }
-    }
   }
   // the low bytes of the even and of the odd channels
   const uint32_t even = permute(permute(c[0], c[2], 0x0040), permute(c[4], c[6], 0x0040), 0x5410);
   const uint32_t odds = permute(permute(c[1], c[3], 0x0040), permute(c[5], c[7], 0x0040), 0x5410);
-  return make_uint2(even + 16u * odds, sz);
+  return make_uint2(even + 16u * odds, s16 | ((ends & 0xffff0000u) ^ 0x80000000u));
 }
 
 // How a lane finds the partners of its 8 channels: no turning; another lane's 8 (half layout,
@@ -307,7 +293,8 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
         to_next -= crossing * (kHeadDim * 2);
       }
     }
-    auto put = [&](int r, uint4 v) {
+    uint32_t again = 0;  // bit r: this lane's group of row r is to be quantised as the definition stands
+    auto put = [&](int r, uint4 v, auto plain) {
       if (TURN != kNoTurn && kind != 2) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if constexpr (TURN == kAdjacent) {
@@ -364,7 +351,14 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
       uint8_t* row = behind ? to_next : to;
       if (INT4 && kind != 0) {
         const int t = (t0 + r) % kPage, lanes = kp.group / 8;
-        const uint2 c = quantize8(v, lanes, mask);
+        uint2 c;
+        if constexpr (decltype(plain)::value) {
+          c = quantize8_plain(v, lanes, mask);
+        } else {
+          bool leave;
+          c = quantize8(v, lanes, mask, leave);
+          again |= leave ? 1u << r : 0u;
+        }
         *reinterpret_cast<uint32_t*>(row + int4_word(t, l16)) = c.x;
         if (l16 % lanes == 0) (behind ? sz_next : sz_to)[t * (16 / lanes) + l16 / lanes] = c.y;
       } else {
@@ -378,9 +372,17 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
 #pragma unroll
       for (int b = 0; b < kBatch; ++b, src += in_row) x[b] = load8(src, in_vec);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) put(r0 + b, x[b]);
+      for (int b = 0; b < kBatch; ++b) put(r0 + b, x[b], std::false_type());
     }
-    for (; r0 < it.count; ++r0, src += in_row) put(r0, load8(src, in_vec));
+    for (; r0 < it.count; ++r0, src += in_row) put(r0, load8(src, in_vec), std::false_type());
+    if constexpr (INT4) {
+      again = __reduce_or_sync(mask, again);
+#pragma unroll 1
+      for (; again; again &= again - 1) {
+        const int r = __ffs(again) - 1;
+        put(r, load8(in + (row0 + r) * in_row, in_vec), std::true_type());
+      }
+    }
   }
   if (!waited) {
     pdl_wait();
