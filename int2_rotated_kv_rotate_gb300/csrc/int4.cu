@@ -15,6 +15,11 @@
 // four for the values, whose pairs are two tokens' codes of a channel).  The 16 is folded into q'
 // or into the output row's factor.
 //
+// Eight query heads fill the 8 columns of an MMA.  Four stand in them twice: of the scores, the lanes of
+// the first columns take the block's first 8 tokens and those of the second its others, so that
+// no lane's scaling and softmax is idle; of the values, the second columns sum the products of the second
+// tokens (B is 0 elsewhere), and both are added at the end.
+//
 // Bound by HBM at 136 bytes (group 128) or 160 (group 32) a token and kv-head.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,6 +70,14 @@ __device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 template <int G, int GROUP>
@@ -73,6 +86,8 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
                                                                  float* __restrict__ out_f32) {
   using C = Shape4<G, GROUP>;
   constexpr int NG = C::NG, ST = C::kStages;
+  constexpr int NI = G == 8 ? 2 : 1;      // tokens of a block of 16 whose scores a lane has
+  constexpr int kLane0 = G == 8 ? 4 : 2;  // lanes with the same heads: from lane bit kLane0 on
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + C::kQs);
   uint64_t* all_bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
@@ -81,6 +96,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
   int* s_next = s_last + 1;
   int* s_poison = s_last + 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  const int col = G == 8 ? gid : gid & 3;               // the head of column gid
+  const int head_lane = G == 8 ? 2 * tig : 2 * (tig & 1);  // the heads of this lane's scores: that and the next
+  const int i_lane = G == 8 ? 0 : tig >> 1;              // G = 4: its tokens are gid + 8 i_lane of a block
   if (threadIdx.x == 0) {
     for (int i = 0; i <= NW * ST; ++i) mbar_init(smem_u32(&all_bars[i]), 1);
     *s_poison = 0;
@@ -158,8 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int n = 0; n < 8; n += 4) {
-          const float4 v = G == 8 || gid < G ? *reinterpret_cast<const float4*>(qs + gid * kQRow + 32 * g + 8 * tig + n)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 v = *reinterpret_cast<const float4*>(qs + col * kQRow + 32 * g + 8 * tig + n);
           x[g][n] = v.x;
           x[g][n + 1] = v.y;
           x[g][n + 2] = v.z;
@@ -181,10 +198,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           bq[2 * g + (n >> 1)][n & 1] = half2_bits(x[g][n] * f, x[g][n + 4] * f);
         }
     }
-    // the heads of this thread's scores: 2 tig, 2 tig + 1 (idle past G)
     float bk[2], qz[2][NG];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) bk[j] = __shfl_sync(0xffffffffu, back, 4 * (2 * tig + j));
+    for (int j = 0; j < 2; ++j) bk[j] = __shfl_sync(0xffffffffu, back, 4 * (head_lane + j));
     {
       // sums of q over the groups: lanes of column gid have theirs, then as above
       float sum[4];
@@ -192,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       for (int g = 0; g < 4; ++g) {
         sum[g] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) sum[g] += G == 8 || gid < G ? qs[gid * kQRow + 32 * g + 8 * tig + n] : 0.f;
+        for (int n = 0; n < 8; ++n) sum[g] += qs[col * kQRow + 32 * g + 8 * tig + n];
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
       }
@@ -200,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-          qz[j][g] = scale * __shfl_sync(0xffffffffu, NG == 4 ? sum[g] : (sum[0] + sum[1]) + (sum[2] + sum[3]), 4 * (2 * tig + j));
+          qz[j][g] = scale * __shfl_sync(0xffffffffu, NG == 4 ? sum[g] : (sum[0] + sum[1]) + (sum[2] + sum[3]), 4 * (head_lane + j));
     }
     // ---- the warp's half pages
     float m_run[2] = {-INFINITY, -INFINITY}, muse[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f}, zv[2][NG], oacc[8][4];
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       const uint8_t* vc = stage + C::kCodeBytes + 16 * ((gid >> 1) ^ tig);
       const uint32_t* ksz = reinterpret_cast<const uint32_t*>(stage + 2 * C::kCodeBytes);
       const uint32_t* vsz = ksz + kUnit * NG;
-      float lg[2][2][2];  // block, token gid or gid + 8, head
+      float lg[2][NI][2];  // block, token, head
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int ta = 16 * b + gid;
@@ -246,55 +262,54 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
         constexpr int NA = NG == 4 ? 4 : 2;  // at group 128 two chains of products
         float acc[NA][4];
 #pragma unroll
-        for (int g = 0; g < NA; ++g)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[g][e] = 0.f;
-#pragma unroll
         for (int g = 0; g < 4; ++g) {
           float(&a)[4] = acc[NG == 4 ? g : g & 1];
-          mma_f16_16816(a, wa[g] & kLow, wb[g] & kLow, wa[g] & kHigh, wb[g] & kHigh, bq[2 * g][0], bq[2 * g][1]);
+          if (g < NA) mma_f16_16816_first(a, wa[g] & kLow, wb[g] & kLow, wa[g] & kHigh, wb[g] & kHigh, bq[2 * g][0], bq[2 * g][1]);
+          else mma_f16_16816(a, wa[g] & kLow, wb[g] & kLow, wa[g] & kHigh, wb[g] & kHigh, bq[2 * g][0], bq[2 * g][1]);
           const uint32_t sa = wa[g] >> 8, sb = wb[g] >> 8;
           mma_f16_16816(a, sa & kLow, sb & kLow, sa & kHigh, sb & kHigh, bq[2 * g + 1][0], bq[2 * g + 1][1]);
         }
-        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, off[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NI; ++i) {
           uint32_t sz[NG];
+          const uint32_t* at = ksz + (ta + 8 * (G == 8 ? i : i_lane)) * NG;
           if constexpr (NG == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(ksz + (ta + 8 * i) * NG);
+            const uint4 v = *reinterpret_cast<const uint4*>(at);
             sz[0] = v.x, sz[1] = v.y, sz[2] = v.z, sz[3] = v.w;
           } else {
-            sz[0] = ksz[ta + 8 * i];
+            sz[0] = *at;
           }
+          float sum[2] = {0.f, 0.f}, off[2] = {0.f, 0.f};
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float s = bf16_lo(sz[g]), z = bf16_hi(sz[g]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float T = NG == 4 ? acc[g][2 * i + j] : acc[0][2 * i + j] + acc[1][2 * i + j];
-              sum[i][j] = fmaf(T, s, sum[i][j]);
-              off[i][j] = fmaf(z, qz[j][g], off[i][j]);
+              auto product = [&](int k) { return G == 8 ? acc[k][2 * i + j] : i_lane ? acc[k][2 + j] : acc[k][j]; };
+              const float T = NG == 4 ? product(g) : product(0) + product(1);
+              sum[j] = fmaf(T, s, sum[j]);
+              off[j] = fmaf(z, qz[j][g], off[j]);
             }
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) lg[b][i][j] = fmaf(sum[i][j], bk[j], off[i][j]);
+          for (int j = 0; j < 2; ++j) lg[b][i][j] = fmaf(sum[j], bk[j], off[j]);
         }
       }
       if (valid < kUnit) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (16 * b + 8 * i + gid >= valid) lg[b][i][0] = lg[b][i][1] = -INFINITY;
+          for (int i = 0; i < NI; ++i)
+            if (16 * b + 8 * (G == 8 ? i : i_lane) + gid >= valid) lg[b][i][0] = lg[b][i][1] = -INFINITY;
       }
       // ---- scales of the values, and the references of the maximum and of the scales
-      uint32_t szv[2][2][NG];
+      uint32_t szv[2][NI][NG];
       float top = 0.f;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t* at = vsz + (16 * b + 8 * i + gid) * NG;
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t* at = vsz + (16 * b + 8 * (G == 8 ? i : i_lane) + gid) * NG;
           if constexpr (NG == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(at);
             szv[b][i][0] = v.x, szv[b][i][1] = v.y, szv[b][i][2] = v.z, szv[b][i][3] = v.w;
@@ -308,13 +323,13 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       bool over = top > r;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        mloc[j] = fmaxf(fmaxf(lg[0][0][j], lg[0][1][j]), fmaxf(lg[1][0][j], lg[1][1][j]));
+        mloc[j] = fmaxf(fmaxf(lg[0][0][j], lg[0][NI - 1][j]), fmaxf(lg[1][0][j], lg[1][NI - 1][j]));
         over |= mloc[j] > m_run[j];
       }
       if (__any_sync(0xffffffffu, over)) {
         float alpha[2];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
+        for (int o = kLane0; o < 32; o <<= 1) {
           mloc[0] = fmaxf(mloc[0], __shfl_xor_sync(0xffffffffu, mloc[0], o));
           mloc[1] = fmaxf(mloc[1], __shfl_xor_sync(0xffffffffu, mloc[1], o));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -348,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       // ---- values
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        float p[2][2];
+        float p[NI][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             p[i][j] = ex2(lg[b][i][j] - muse[j]);  // masked: exactly 0, and scale and zero are finite
@@ -358,14 +373,22 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           }
         uint32_t bp[NG][2];
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+        for (int i = 0; i < NI; ++i) {
+          const float p0 = p[i][0] * r_inv, p1 = p[i][1] * r_inv;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float s = bf16_lo(szv[b][i][g]) * r_inv, z = bf16_hi(szv[b][i][g]);
-            bp[g][i] = movmatrix_trans(half2_bits(p[i][0] * s, p[i][1] * s));
+          for (int g = 0; g < NG; ++g) {
+            const float s = bf16_lo(szv[b][i][g]), z = bf16_hi(szv[b][i][g]);
+            const uint32_t x = movmatrix_trans(half2_bits(p0 * s, p1 * s));
+            if constexpr (G == 8) {
+              bp[g][i] = x;
+            } else {  // lanes of the first columns have the first tokens
+              bp[g][0] = gid < 4 ? x : 0u;
+              bp[g][1] = gid < 4 ? 0u : x;
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) zv[j][g] = fmaf(p[i][j], z, zv[j][g]);
           }
+        }
         // tokens 2 tig, + 1, + 8, + 9 of the block; chunk gid / 2 of each, its half gid % 2
         const uint8_t* at = vc + (16 * b + 2 * tig) * kInt4Row;
         const uint4 a = *reinterpret_cast<const uint4*>(at), a1 = *reinterpret_cast<const uint4*>(at + kInt4Row);
@@ -399,11 +422,17 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
+      for (int o = kLane0; o < 32; o <<= 1) {
         l_part[j] += __shfl_xor_sync(0xffffffffu, l_part[j], o);
 #pragma unroll
         for (int g = 0; g < NG; ++g) zv[j][g] += __shfl_xor_sync(0xffffffffu, zv[j][g], o);
       }
+    if constexpr (G == 4) {  // the two halves of the tokens
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[f][e] += __shfl_xor_sync(0xffffffffu, oacc[f][e], 2);
+    }
     __syncthreads();  // every warp is done with its stages
     float* wm = reinterpret_cast<float*>(smem);  // [NW][G] maxima
     float* wl = wm + NW * G;                     // [NW][G] denominators
@@ -411,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     constexpr int kRow = kHeadDim + 2;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int head = 2 * tig + j;
-      if (G == 8 || head < G) {
+      const int head = head_lane + j;
+      if (G == 8 || tig < 2) {
         if (gid == 0) {
           wm[warp * G + head] = broken ? -INFINITY : m_run[j];
           wl[warp * G + head] = broken ? 0.f : l_part[j];
