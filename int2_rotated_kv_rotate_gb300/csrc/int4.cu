@@ -125,19 +125,22 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     const int t0 = it.begin * kPage, t1 = slot_ok && it.kind == 0 ? min(it.end * kPage, dr.L) : t0;
     const int n_units = t1 > t0 ? (t1 - t0 + kUnit - 1) / kUnit : 0;
     const int n_my = n_units > warp ? (n_units - warp + NW - 1) / NW : 0;
-    const int* ptab =
-        reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(slot_ok ? dr.slot : 0) * kp.max_pages_per_request;
+    // The warp's half pages: half warp % 2 of pages begin + warp / 2, + 4, ..
+    static_assert(NW % 2 == 0, "a warp's half pages are the same half of their pages");
+    const int page0 = it.begin + warp / 2, half = warp & 1;
+    const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
+                      size_t(slot_ok ? dr.slot : 0) * kp.max_pages_per_request + page0;
+    const uint8_t* codes = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
+                           size_t(it.kvh) * kp.lay.codes_head_stride + half * C::kCodeBytes;
+    const uint8_t* szs = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(it.kvh) * kp.lay.sz_head_stride +
+                         half * C::kSzBytes;
     // copies of the warp's k-th half page into stage k % ST; false (none) if the page id is out of range
     auto issue = [&](int k) -> bool {
-      const int u = warp + NW * k, lp = it.begin + u / 2, half = u & 1;
-      const int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+      const int phys = page0 + NW / 2 * k < kp.max_pages_per_request ? ptab[NW / 2 * k] : -1;
       if (phys < 0 || phys >= kp.max_pages) return false;
       if (lane == 0) {
-        const uint8_t* code = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
-                              size_t(phys) * kp.lay.codes_page_stride + size_t(it.kvh) * kp.lay.codes_head_stride +
-                              half * C::kCodeBytes;
-        const uint8_t* sz = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(phys) * kp.lay.sz_page_stride +
-                            size_t(it.kvh) * kp.lay.sz_head_stride + half * C::kSzBytes;
+        const uint8_t* code = codes + size_t(unsigned(phys)) * unsigned(kp.lay.codes_page_stride);
+        const uint8_t* sz = szs + size_t(unsigned(phys)) * unsigned(kp.lay.sz_page_stride);
         const uint32_t bar = smem_u32(&bars[k % ST]), dst = smem_u32(pipe + (k % ST) * C::kStageBytes);
         fence_proxy_async();
         mbar_expect_tx(bar, C::kStageBytes);
@@ -151,8 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     uint32_t ok_mask = 0;  // bit st: a copy into stage st is in flight
     int issued = 0;
     for (; issued < min(ST, n_my); ++issued) {
-      const int lp = it.begin + (warp + NW * issued) / 2;
-      if (!waited && (lp + 1) * kPage > dr.H_pre) break;
+      if (!waited && (page0 + NW / 2 * issued + 1) * kPage > dr.H_pre) break;
       if (issue(issued)) ok_mask |= 1u << issued;
     }
     const size_t head0 = size_t(it.req) * kp.n_q_heads + size_t(it.kvh) * G;
