@@ -281,9 +281,10 @@ oscar_status oscar_append_rotated(oscar_cache* cache, int layer, const uint64_t*
  * Per token, K or V, and group of `group` consecutive channels, all in fp32: s = bf16((max x -
  * min x) / 15), z = bf16(min x); code = 0 if s == 0 else fminf(fmaxf(rintf((x - z) / s), 0), 15);
  * value fmaf(code, s, z).  Values past +-2^126 and infinities count as +-2^126, NaN as 2^126.
- * Pools: codes [layer][phys_page][kv_head][K|V][64 tokens][64 B], sz [layer][phys_page][kv_head]
- * [K|V][64 tokens][d/group][scale, zero] bf16.  Channel c of a page's token t is bits 4 (c % 8)
- * .. + 3 of the little-endian word at byte 64 t + 16 ((c / 8 % 4) ^ (t / 2 % 4)) + 4 (c / 32).
+ * Pool (at oscar_layout.codes; codes_page_bytes a kv-head): [layer][phys_page][kv_head][2 halves of
+ * 32 tokens], a half page being K codes [32][64 B], V codes [32][64 B], K [32][d/group][scale,
+ * zero] bf16, V the same.  Channel c of a half page's token t is bits 4 (c % 8) .. + 3 of the
+ * little-endian word at byte 64 t + 16 ((c / 8 % 4) ^ (t / 2 % 4)) + 4 (c / 32) of its codes.
  * Requests, reservations, plans and prefix sharing are as for the BF16 format.
  * oscar_int4_append: step 2 of an append, arguments as oscar_quantize_append.
  * oscar_int4_read: the values of tokens [begin, end) of a request (a pending reservation's among

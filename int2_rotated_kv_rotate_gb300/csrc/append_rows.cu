@@ -210,17 +210,13 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
   const float* factors = table + (TURN == kLanes ? 4 * (first ? l16 : l16 - eighth + pairs / 2) : TURN == kAdjacent ? 2 * c0 : 0);
   // the head's keys or values in page 0 of the layer
   uint8_t* pool = kp.base;
-  uint32_t* sz_pool = nullptr;
+  const int kv = kind == 2, ng = kHeadDim / (INT4 ? kp.group : kHeadDim);
   if (kind != 0) {
     if constexpr (!INT4) {
       pool += kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride + size_t(h) * kp.lay.bf16_head_stride +
-              size_t(kind - 1) * (kPage * kHeadDim * 2) + 16 * l16;
+              size_t(kv) * (kPage * kHeadDim * 2) + 16 * l16;
     } else {
-      pool += kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride +
-              size_t(kind - 1) * (kPage * kInt4Row);
-      sz_pool = reinterpret_cast<uint32_t*>(kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride +
-                                            size_t(h) * kp.lay.sz_head_stride +
-                                            size_t(kind - 1) * (kPage * (kHeadDim / kp.group) * 4));
+      pool += kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride;
     }
   }
   const unsigned page_stride = unsigned(INT4 ? kp.lay.codes_page_stride : kp.lay.bf16_page_stride);
@@ -268,7 +264,6 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
     // Where the rows go: the item's lie in one page or two.
     const int t0 = it.begin % kPage, crossing = kPage - t0;
     uint8_t *to = pool, *to_next = pool;
-    uint32_t *sz_to = sz_pool, *sz_next = sz_pool;
     long long to_row = kHeadDim * 2;  // bytes from row to row (4-bit rows are found by their token)
     bool ok = true, ok_next = true;
     if (kind == 0) {
@@ -284,11 +279,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
       if (l16 == 0 && !(ok && ok_next)) flag(kp, OSCAR_FLAG_BAD_PAGE);
       to += size_t(unsigned(ok ? page : 0)) * page_stride;
       to_next += size_t(unsigned(ok_next ? next : 0)) * page_stride;
-      if constexpr (INT4) {
-        const unsigned sz_stride = unsigned(kp.lay.sz_page_stride / 4);
-        sz_to += size_t(unsigned(ok ? page : 0)) * sz_stride;
-        sz_next += size_t(unsigned(ok_next ? next : 0)) * sz_stride;
-      } else {
+      if constexpr (!INT4) {
         to += t0 * (kHeadDim * 2);
         to_next -= crossing * (kHeadDim * 2);
       }
@@ -359,8 +350,8 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
           c = quantize8(v, lanes, mask, leave);
           again |= leave ? 1u << r : 0u;
         }
-        *reinterpret_cast<uint32_t*>(row + int4_word(t, l16)) = c.x;
-        if (l16 % lanes == 0) (behind ? sz_next : sz_to)[t * (16 / lanes) + l16 / lanes] = c.y;
+        *reinterpret_cast<uint32_t*>(row + int4_word(t, l16, kv, ng)) = c.x;
+        if (l16 % lanes == 0) *reinterpret_cast<uint32_t*>(row + int4_scale(t, l16 / lanes, kv, ng)) = c.y;
       } else {
         store8(reinterpret_cast<uint16_t*>(row + r * to_row), v, kind != 0 || p.q_out_vec);
       }
@@ -404,10 +395,7 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
   if (head >= 2 * Hkv) return;
   const int kv = head >= Hkv, h = kv ? head - Hkv : head;
   const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) + size_t(slot) * kp.max_pages_per_request;
-  const uint8_t* pool = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride +
-                        size_t(kv) * (kPage * kInt4Row);
-  const uint8_t* sz_pool = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(h) * kp.lay.sz_head_stride +
-                           size_t(kv) * (kPage * ng * 4);
+  const uint8_t* pool = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride;
   const int group = l16 / (kp.group / 8);
   T* out = (kv ? v_out : k_out) + size_t(h) * kHeadDim + 8 * l16;
   const size_t row = size_t(Hkv) * kHeadDim;
@@ -417,7 +405,6 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
     page[0] = lp < kp.max_pages_per_request ? ptab[lp] : -1;
     page[1] = t0 + n <= kPage ? page[0] : lp + 1 < kp.max_pages_per_request ? ptab[lp + 1] : -1;
     const uint8_t* rows[2];
-    const uint32_t* szs[2];
     bool ok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -425,7 +412,6 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
       if (!ok[i] && l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
       const unsigned at = unsigned(ok[i] ? page[i] : 0);
       rows[i] = pool + size_t(at) * unsigned(kp.lay.codes_page_stride);
-      szs[i] = reinterpret_cast<const uint32_t*>(sz_pool + size_t(at) * unsigned(kp.lay.sz_page_stride)) + group;
     }
     T* to = out + size_t(p0 - begin) * row;
 #pragma unroll 2
@@ -435,8 +421,9 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
       for (int b = 0; b < kBatch; ++b) {
         const int t = t0 + r + b;
         const bool behind = t >= kPage, there = r + b < n && (behind ? ok[1] : ok[0]);  // (else zeros)
-        w[b] = there ? *reinterpret_cast<const uint32_t*>((behind ? rows[1] : rows[0]) + int4_word(t % kPage, l16)) : 0u;
-        sz[b] = there ? (behind ? szs[1] : szs[0])[(t % kPage) * ng] : 0u;
+        const uint8_t* at = behind ? rows[1] : rows[0];
+        w[b] = there ? *reinterpret_cast<const uint32_t*>(at + int4_word(t % kPage, l16, kv, ng)) : 0u;
+        sz[b] = there ? *reinterpret_cast<const uint32_t*>(at + int4_scale(t % kPage, group, kv, ng)) : 0u;
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b, to += row) {

@@ -34,7 +34,7 @@ namespace oscar {
 namespace {
 
 constexpr int NW = 8, kThreads = 32 * NW;
-constexpr int kUnit = 32;  // tokens of a stage: half a page
+constexpr int kUnit = kInt4Half;  // tokens of a stage
 
 template <int G, int GROUP>
 struct Shape4 {
@@ -51,7 +51,7 @@ struct Shape4 {
   static constexpr int kSlabSlots = kPipe / PartialSlot<G>::kBytes;
   static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
   static_assert((NW * G * (kHeadDim + 4) + 8) * 4 <= kPipe, "per-warp results reuse the stages");
-  static_assert(kSzBytes % 16 == 0 && kStageBytes % 16 == 0, "bulk copies");
+  static_assert(kStageBytes == int4_half_bytes(NG) && kStageBytes % 16 == 0, "bulk copies");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -130,24 +130,18 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     const int page0 = it.begin + warp / 2, half = warp & 1;
     const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                       size_t(slot_ok ? dr.slot : 0) * kp.max_pages_per_request + page0;
-    const uint8_t* codes = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
-                           size_t(it.kvh) * kp.lay.codes_head_stride + half * C::kCodeBytes;
-    const uint8_t* szs = kp.base + kp.lay.sz + size_t(layer) * kp.lay.sz_layer_stride + size_t(it.kvh) * kp.lay.sz_head_stride +
-                         half * C::kSzBytes;
-    // copies of the warp's k-th half page into stage k % ST; false (none) if the page id is out of range
+    const uint8_t* halves = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride +
+                            size_t(it.kvh) * kp.lay.codes_head_stride + half * C::kStageBytes;
+    // copy of the warp's k-th half page into stage k % ST; false (none) if the page id is out of range
     auto issue = [&](int k) -> bool {
       const int phys = page0 + NW / 2 * k < kp.max_pages_per_request ? ptab[NW / 2 * k] : -1;
       if (phys < 0 || phys >= kp.max_pages) return false;
       if (lane == 0) {
-        const uint8_t* code = codes + size_t(unsigned(phys)) * unsigned(kp.lay.codes_page_stride);
-        const uint8_t* sz = szs + size_t(unsigned(phys)) * unsigned(kp.lay.sz_page_stride);
-        const uint32_t bar = smem_u32(&bars[k % ST]), dst = smem_u32(pipe + (k % ST) * C::kStageBytes);
+        const uint32_t bar = smem_u32(&bars[k % ST]);
         fence_proxy_async();
         mbar_expect_tx(bar, C::kStageBytes);
-        bulk_g2s(dst, code, C::kCodeBytes, bar);
-        bulk_g2s(dst + C::kCodeBytes, code + kPage * kInt4Row, C::kCodeBytes, bar);
-        bulk_g2s(dst + 2 * C::kCodeBytes, sz, C::kSzBytes, bar);
-        bulk_g2s(dst + 2 * C::kCodeBytes + C::kSzBytes, sz + kPage * NG * 4, C::kSzBytes, bar);
+        bulk_g2s(smem_u32(pipe + (k % ST) * C::kStageBytes), halves + size_t(unsigned(phys)) * unsigned(kp.lay.codes_page_stride),
+                 C::kStageBytes, bar);
       }
       return true;
     };

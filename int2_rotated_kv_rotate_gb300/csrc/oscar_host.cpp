@@ -143,14 +143,10 @@ DeviceLayout compute_layout(const oscar_config& c) {
     L.clip_V = take(layers * Hkv * 4);
   } else if (c.format == OSCAR_FORMAT_INT4) {
     const size_t ng = d / c.group;
-    L.codes_head_stride = 2 * kPage * kInt4Row;
+    L.codes_head_stride = 2 * int4_half_bytes(int(ng));  // scales and zeros among the codes
     L.codes_page_stride = Hkv * L.codes_head_stride;
     L.codes_layer_stride = pages * L.codes_page_stride;
     L.codes = take(layers * L.codes_layer_stride);
-    L.sz_head_stride = 2 * kPage * ng * 4;
-    L.sz_page_stride = Hkv * L.sz_head_stride;
-    L.sz_layer_stride = pages * L.sz_page_stride;
-    L.sz = take(layers * L.sz_layer_stride);
   } else {
     L.bf16_head_stride = 2 * kPage * d * 2;
     L.bf16_page_stride = Hkv * L.bf16_head_stride;
@@ -663,7 +659,8 @@ oscar_status oscar_cache_create(const oscar_config* cfg, void* device_mem, size_
   if (e == cudaSuccess) e = cudaMemset(c->base + lay.sched, 0, 16);
   // scale/zero words of rows no append has written yet (sink positions, the tail of a
   // page) are read with p = 0 by the decode: they must be finite, so the pool starts at 0
-  if (e == cudaSuccess && !is_bf16(c)) e = cudaMemset(c->base + lay.sz, 0, size_t(cfg->n_layers) * lay.sz_layer_stride);
+  if (e == cudaSuccess && is_int4(c)) e = cudaMemset(c->base + lay.codes, 0, size_t(cfg->n_layers) * lay.codes_layer_stride);
+  if (e == cudaSuccess && is_int2(c)) e = cudaMemset(c->base + lay.sz, 0, size_t(cfg->n_layers) * lay.sz_layer_stride);
   if (e == cudaSuccess)
     e = cudaMemset(c->base + lay.app_done, 0, size_t(cfg->n_layers) * cfg->max_requests * cfg->n_kv_heads * 8);
   if (e == cudaSuccess && is_int2(c)) {

@@ -86,13 +86,14 @@ def test_rows_are_the_definitions(group, n, step):
     t = n - 1
     head, ng = cache.layout.codes_page_bytes, 128 // group
     page = cache.pages(slot)[t // 64]
-    at = cache.layout.codes + (page * 3 + 2) * head + 64 * 64  # V of head 2
-    block = cache.mem[at:at + 4096].cpu().view(torch.int32).view(64, 16)
+    at = cache.layout.codes + (page * 3 + 2) * head + (t % 64 // 32) * (head // 2)  # the half page of head 2
+    assert head == 2 * 2 * 32 * (64 + 4 * ng)
+    block = cache.mem[at + 2048:at + 4096].cpu().view(torch.int32).view(32, 16)  # V
     codes, s, z = quantized(v[t, 2], group)
     for c in range(128):
-        word = int(block[t % 64, 4 * ((c // 8 % 4) ^ (t % 64 // 2 % 4)) + c // 32])
+        word = int(block[t % 32, 4 * ((c // 8 % 4) ^ (t % 64 // 2 % 4)) + c // 32])
         assert (word >> (4 * (c % 8))) & 15 == int(codes[c])
-    at = cache.layout.sz + (page * 3 + 2) * cache.layout.sz_page_bytes + 64 * ng * 4 + (t % 64) * ng * 4
+    at += 4096 + 32 * ng * 4 + (t % 32) * ng * 4
     sz = cache.mem[at:at + ng * 4].cpu().view(torch.bfloat16).view(ng, 2)
     assert torch.equal(sz[:, 0], s.flatten()) and torch.equal(sz[:, 1].float(), z.flatten())
 
