@@ -348,6 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
       const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                         size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+      // The first item's queries go before the pages: behind the copies of five stages on every SM they
+      // would take some 7 us.
+      if (ix == ix0)
+        for (int b = 0; ok && b < w.blocks; ++b) ok = all(wait(ctl->q_full[b], 0));
       for (int i = w.it.begin; ok && i < w.it.end; ++i) {
         const int two = min(2, w.pages - 2 * i);
         int y[2] = {0, 0};
@@ -477,13 +481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- Q: rows 32 wq .. 32 wq + 31 of the block, two rows of 16 chunks at a time
       {
-        const long long row = mine ? (long long)(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + w.it.kvh * G + m % G : -1;
+        // (rows past the tile's read its first row, and become zeros: with a branch around each load
+        // they came one after the other, 10000 cycles)
+        const int tok = mine ? m / G : 0, head = mine ? m % G : 0;
+        const long long row = (long long)(w.rq.row + w.it.tok0 + tok) * kp.n_q_heads + w.it.kvh * G + head;
+        const unsigned some = __ballot_sync(0xffffffffu, mine);
         uint4 v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const long long src = __shfl_sync(0xffffffffu, row, 2 * k + (lane >> 4));
-          v[k] = src >= 0 ? reinterpret_cast<const uint4*>(q + size_t(src) * kHeadDim)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+          v[k] = reinterpret_cast<const uint4*>(q + size_t(src) * kHeadDim)[lane & 15];
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (!((some >> (2 * k + (lane >> 4))) & 1u)) v[k] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int rr = 32 * wq + 2 * k + (lane >> 4), c = lane & 15;
