@@ -313,7 +313,8 @@ oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const vo
  * attends.  q, out [dev] bf16 [sum n_queries][H_q][d], requests in plan order, out_f32 nullable
  * (before the rounding); all 16-byte aligned.  workspace [dev], 256-byte aligned, of
  * oscar_window_workspace_bytes for the current plan, _max_bytes for every plan (as captured
- * launches need it, which may be replayed under any later plan).  Values of tokens that no
+ * launches need it, which may be replayed under any later plan; q and out must then hold that
+ * plan's queries).  Values of tokens that no
  * query attends are not used, and infinities and NaN reach only queries that attend them.  With
  * several queries a request, weights enter the product with the values as bf16; values below 2^78.
  * The current device must be the cache's. */

@@ -1085,6 +1085,8 @@ oscar_status oscar_int4_append(oscar_cache* c, int layer, const void* k_new, con
   p.k_row = p.v_row = (long long)c->cfg.n_kv_heads * kHeadDim;
   p.k_vec = reinterpret_cast<uintptr_t>(k_new) % 16 == 0;
   p.v_vec = reinterpret_cast<uintptr_t>(v_new) % 16 == 0;
+  oscar_status st = check_device(c);
+  if (st) return st;
   const int e = launch_append_rows(kernel_params(c), layer, p, true, false, c->app_items, stream, &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "int4 append launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;

@@ -7,12 +7,13 @@ is the analogue for this library: one loop that admits requests while the pool's
 allow, prefills their prompts (mapping a group's shared prefix from a prefix holder
 instead of recomputing it: a prefix-cache hit), decodes one token per running request per
 step through the library's calls, and frees a request's pages when it finishes.  The same
-loop runs the INT2 cache and the uncompressed BF16 cache, each sized to the same byte
-budget; the number of requests that fit at once is what differs.
+loop runs the INT2 cache, the 4-bit cache and the uncompressed BF16 cache, each sized to the
+same byte budget; the number of requests that fit at once is what differs.
 
 Around the attention the loop can run what a model's serving step runs: rotary positions on
-the queries and the new keys (`rotary`); the BF16 cache's decode with shared prefixes attended
-once (`share_decode`); and, on the BF16 cache, eviction of the tokens with the least
+the queries and the new keys (`rotary`; on the BF16 and 4-bit caches the keys are turned as they
+are appended); the BF16 cache's decode with shared prefixes attended once (`share_decode`) or
+within a sliding window and the first tokens (`window`, `window_sinks`); and, on the BF16 cache, eviction of the tokens with the least
 accumulated attention weight once a request holds more than `evict_above` of them, down to
 `evict_to`, so that a long request stays within a bounded number of pages (the weights that
 this keeps count against the budget: a row of the longest request for every slot and layer,
@@ -140,14 +141,19 @@ def cache_for_budget(w: wl.Workload, fmt: int, budget_bytes: int, max_requests: 
 
 
 class ServingLoop:
-    """Continuous batching over one cache (INT2 or BF16) of workload shape w."""
+    """Continuous batching over one cache (INT2, INT4 or BF16) of workload shape w."""
 
     def __init__(self, w: wl.Workload, fmt: int, budget_bytes: int, tokens: TokenSource, layer_params=None,
                  max_requests: int = 128, max_len: int = 1 << 16, prefix_tokens: int = 0,
                  prefill_chunk: int = 16384, device="cuda", rotary=None, share_decode: bool = False,
-                 evict_above: int = 0, evict_to: int = 0, n_sink: int = 4, n_recent: int = 64):
-        if (share_decode or evict_above) and fmt in _INT2:
-            raise ValueError("share_decode and eviction need the BF16 format")
+                 evict_above: int = 0, evict_to: int = 0, n_sink: int = 4, n_recent: int = 64, window: int = 0,
+                 window_sinks: int = 0):
+        if (share_decode or evict_above or window) and fmt != N.OSCAR_FORMAT_BF16:
+            raise ValueError("share_decode, eviction and a window need the BF16 format")
+        if window < 0 or window_sinks < 0 or (window_sinks and not window):
+            raise ValueError("window_sinks go with a window of at least one token")
+        if window and (share_decode or evict_above):
+            raise ValueError("a window excludes share_decode and eviction")
         if share_decode and evict_above:
             raise ValueError("share_decode and eviction exclude each other (the weights' decode does not share)")
         if evict_above and not (0 < evict_to <= evict_above and n_sink >= 0 and n_recent >= 0 and n_sink + n_recent <= evict_to):
@@ -163,6 +169,7 @@ class ServingLoop:
             for layer in range(w.n_layers):
                 self.cache.set_layer_params(layer, RK[layer], RV[layer], cK[layer], cV[layer])
         self.rotary, self.share_decode = rotary, share_decode
+        self.window, self.window_sinks = window, window_sinks
         self.evict_above, self.evict_to, self.protect = evict_above, evict_to, (n_sink, n_recent)
         if evict_above:
             self.weights = [self.cache.new_weights() for _ in range(w.n_layers)]
@@ -201,6 +208,9 @@ class ServingLoop:
                 if layer == 0:
                     positions = torch.cat([torch.arange(a, a + n, dtype=torch.int32, device=K.device)
                                            for a, n in zip(starts, counts)])
+                if self.fmt not in _INT2:
+                    c.append_rotated(layer, self.rotary, K, V, positions=positions)
+                    continue
                 self.rotary.apply(positions, K, q_out=K)
             c.append(layer, K, V)
         c.commit()
@@ -313,7 +323,10 @@ class ServingLoop:
         reqs = self.running
         slots = [r.slot for r in reqs]
         c.reserve(slots, [1] * len(reqs))
-        c.plan(slots, flags=N.OSCAR_PLAN_SHARED_PREFIX if self.share_decode else 0)
+        if self.window:
+            c.plan_window(slots, n_sink=self.window_sinks, window=self.window)
+        else:
+            c.plan(slots, flags=N.OSCAR_PLAN_SHARED_PREFIX if self.share_decode else 0)
         # pool rows of every request's new token and query, all layers: row = (A * stream +
         # B * layer + position) mod P, one device tensor per step
         tk = self.tokens
@@ -328,18 +341,26 @@ class ServingLoop:
             K = tk.K.index_select(0, idx)
             V = tk.V.index_select(0, idx)
             q = tk.Q.index_select(0, qi)
-            if self.rotary is not None:
+            turned = self.rotary is not None and self.fmt not in _INT2  # by the append
+            if turned:
+                c.append_rotated(layer, self.rotary, K, V, q, positions=positions, q_out=q)
+            elif self.rotary is not None:
                 self.rotary.apply(positions, q, K, q_out=q, k_out=K)
             o32 = torch.empty(q.shape, dtype=torch.float32, device=q.device) if on_output else None
             if self.fmt in _INT2:
                 out = c.append_decode(layer, K, V, q, out_f32=o32)
             else:
-                c.bf16_append(layer, K, V)
+                if not turned:
+                    c.append(layer, K, V)
                 if self.evict_above:
                     out, _ = c.decode_weights(layer, q, self.weights[layer], out_f32=o32)
+                elif self.window:
+                    out = c.attend_window(layer, q, out_f32=o32)
                 else:
                     out = c.decode(layer, q, out_f32=o32)
             if on_output:
+                if turned:  # (the rows as the cache has them)
+                    self.rotary.apply(positions, K, q_out=K)
                 on_output(self.stats["steps"], layer, list(reqs), K, V, q, out, o32)
         c.commit()
         for r in reqs:
