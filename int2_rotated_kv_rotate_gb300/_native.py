@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -135,8 +136,7 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(ctypes.c_float)]),
                 "oscar_rope": (I, [ctypes.POINTER(oscar_rope_tensor), I, P, I, I, ctypes.c_float, I, ctypes.c_uint32, P,
                                    ctypes.c_longlong, P]),
-                "oscar_append_rotated": (I, [P, I, P, I, ctypes.c_float, ctypes.c_uint32, P, ctypes.POINTER(oscar_rope_tensor),
-                                             ctypes.POINTER(oscar_rows), ctypes.POINTER(oscar_rows), P]),
+                "oscar_append_rotated": (I, [P, I, P, I, ctypes.c_float, ctypes.c_uint32, P, P, P, P, P]),
                 "oscar_int4_append": (I, [P, I, P, P, P]),
                 "oscar_int4_read": (I, [P, I, I, I, I, P, P, I, P]),
                 "oscar_int4_decode_attention": (I, [P, I, P, P, P, S, P, P]),
@@ -459,16 +459,22 @@ def oscar_rope(tensors, steps, head_dim: int, rotary_dim: int, magnitude: float,
                             positions.data_ptr(), positions.shape[0], _stream(stream)))
 
 
+_pack_rope_tensor = struct.Struct("@PPi4xqqqq").pack  # (as oscar_rope_tensor; packed bytes cost half a Structure's time)
+_pack_rows = struct.Struct("@Pqq").pack
+
+
 def oscar_append_rotated(handle: int, layer: int, steps, rotary_dim: int, magnitude: float, flags: int, positions, q, q_out,
-                         k, v, stream=None) -> None:
-    """k, v and (nullable) q, q_out: [rows, heads, 128] device tensors of any row and head strides."""
-    sk, sv = k.stride(), v.stride()
+                         k, v, stream=None, q_strides=None, k_strides=None, v_strides=None) -> None:
+    """k, v and (nullable) q, q_out: [rows, heads, 128] device tensors of any row and head strides
+    (theirs where the caller has them)."""
+    sk, sv = k_strides or k.stride(), v_strides or v.stride()
     qd = None
     if q is not None:
-        a, b = q.stride(), q_out.stride()
-        qd = oscar_rope_tensor(q.data_ptr(), q_out.data_ptr(), q.shape[1], a[0], a[1], b[0], b[1])
-    _check(lib().oscar_append_rotated(handle, layer, steps.data_ptr(), rotary_dim, magnitude, flags, _ptr(positions),
-                                      qd, oscar_rows(k.data_ptr(), sk[0], sk[1]), oscar_rows(v.data_ptr(), sv[0], sv[1]),
+        a, b = q_strides or (q.stride(), q_out.stride())
+        qd = _pack_rope_tensor(q.data_ptr(), q_out.data_ptr(), q.shape[1], a[0], a[1], b[0], b[1])
+    _check(lib().oscar_append_rotated(handle, layer, steps.data_ptr(), rotary_dim, magnitude, flags,
+                                      None if positions is None else positions.data_ptr(), qd,
+                                      _pack_rows(k.data_ptr(), sk[0], sk[1]), _pack_rows(v.data_ptr(), sv[0], sv[1]),
                                       _stream(stream)))
 
 

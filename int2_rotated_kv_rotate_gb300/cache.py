@@ -117,35 +117,37 @@ class KVCache:
         rows, dev = self._rows, self.mem.device
         if rotary.head_dim != 128 or rotary.device != dev:
             raise ValueError(f"rotary must have 128 channels a head, on {dev}")
-        for name, t, heads in (("k_new", k_new, self.cfg.n_kv_heads), ("v_new", v_new, self.cfg.n_kv_heads)):
-            if (tuple(t.shape) != (rows, heads, 128) or t.dtype != torch.bfloat16 or t.device != dev
-                    or t.stride()[2] != 1):
-                raise ValueError(f"{name} must be bf16 [{rows}, {heads}, 128] on {dev} with contiguous channels")
+        shape = (rows, self.cfg.n_kv_heads, 128)
+        sk, sv = k_new.stride(), v_new.stride()
+        if (k_new.shape != shape or v_new.shape != shape or k_new.dtype is not torch.bfloat16
+                or v_new.dtype is not torch.bfloat16 or k_new.device != dev or v_new.device != dev or sk[2] != 1 or sv[2] != 1):
+            raise ValueError(f"k_new and v_new must be bf16 {shape} on {dev} with contiguous channels")
         flags = N.OSCAR_ROPE_INTERLEAVED if rotary.interleaved else 0
         if positions is not None:
-            if (tuple(positions.shape) != (rows,) or positions.dtype not in (torch.int32, torch.int64)
+            if (positions.shape != (rows,) or positions.dtype not in (torch.int32, torch.int64)
                     or positions.device != dev or (rows > 1 and positions.stride(0) != 1)):
                 raise ValueError(f"positions must be contiguous int32 or int64 [{rows}] on {dev}")
-            if positions.dtype == torch.int64:
+            if positions.dtype is torch.int64:
                 flags |= N.OSCAR_ROPE_POSITIONS64
-        given = q_out is not None
+        given, strides = q_out is not None, None
         if q is not None:
-            shape = tuple(q.shape)
-            if (len(shape) != 3 or shape[0] != rows or shape[1] < 1 or shape[2] != 128 or q.dtype != torch.bfloat16
-                    or q.device != dev or q.stride()[2] != 1):
+            shape, a = q.shape, q.stride()
+            if (len(shape) != 3 or shape[0] != rows or shape[1] < 1 or shape[2] != 128 or q.dtype is not torch.bfloat16
+                    or q.device != dev or a[2] != 1):
                 raise ValueError(f"q must be bf16 [{rows}, heads, 128] on {dev} with contiguous channels")
-            if torch.is_grad_enabled() and (q.requires_grad or (given and q_out.requires_grad)):
+            if (q.requires_grad or (given and q_out.requires_grad)) and torch.is_grad_enabled():
                 raise ValueError("queries that require grad are turned by RotaryEmbedding.apply")
             if not given:
                 with N.on_stream(stream):  # in the launch's order
                     q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            elif (tuple(q_out.shape) != shape or q_out.dtype != torch.bfloat16 or q_out.device != dev
-                    or q_out.stride()[2] != 1):
+            b = q_out.stride()
+            if given and (q_out.shape != shape or q_out.dtype is not torch.bfloat16 or q_out.device != dev or b[2] != 1):
                 raise ValueError("q_out must be like q, with contiguous channels")
+            strides = a, b
         elif given:
             raise ValueError("q_out without q")
         N.oscar_append_rotated(self.handle, layer, rotary.steps, rotary.rotary_dim, rotary.magnitude, flags, positions, q, q_out,
-                               k_new, v_new, stream)
+                               k_new, v_new, stream, strides, sk, sv)
         if given:
             torch.autograd.graph.increment_version(q_out)
         return q_out

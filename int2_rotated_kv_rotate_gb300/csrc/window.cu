@@ -635,18 +635,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = reinterpret_cast<float*>(slot + kBlockRows * 8) + size_t(r) * kHeadDim;
       if (mine && !whole_tile) reinterpret_cast<float2*>(slot)[r] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
       if (!idle) {
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 16) {
-          uint32_t o[16];
-          tmem::ld_x16(tl + kColO + c, o);
-          tmem::wait_ld();
-          float x[16];
+        uint32_t o[2][32];  // 32 columns on their way while the last 32 are stored
+        tmem::ld_x32(tl + kColO, o[0]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * inv;
-          if (odd && mine) {  // infinities and NaN that this row sees of the steps that were looked over
+        for (int c = 0; c < kHeadDim; c += 32) {
+          uint32_t(&cur)[32] = o[(c / 32) & 1];
+          tmem::wait_ld();
+          if (c + 32 < kHeadDim) tmem::ld_x32(tl + kColO + c + 32, o[(c / 32 + 1) & 1]);
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(cur[e]) * inv;
+          if (odd && mine) {  // infinities and NaN that this row sees of the pages that were looked over
             const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
             const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                               size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+#pragma unroll 1
             for (int j = w.page0(b); j < end; j += w.stride()) {
               if (whole_in_tile.has(j)) continue;
               const uint64_t see = w.visible(j, pos);
@@ -657,15 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       kp.base + kp.lay.bf16_pages + size_t(layer) * kp.lay.bf16_layer_stride +
                                       size_t(phys) * kp.lay.bf16_page_stride + size_t(w.it.kvh) * kp.lay.bf16_head_stride) +
                                   kPage * kHeadDim + c;
+#pragma unroll 1
               for (int t = 0; t < kPage; ++t)
                 if ((see >> t) & 1ull)
-                  for (int e = 0; e < 16; ++e) {
-                    const float y = bf16_f32(v[t * kHeadDim + e]);
-                    if (!(fabsf(y) < INFINITY)) {
 #pragma unroll
-                      for (int g = 0; g < 16; ++g)
-                        if (g == e) x[g] += y;
-                    }
+                  for (int e = 0; e < 32; ++e) {
+                    const float y = bf16_f32(v[t * kHeadDim + e]);
+                    if (!(fabsf(y) < INFINITY)) x[e] += y;
                   }
             }
           }
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (whole_tile) {
               uint4* dst = reinterpret_cast<uint4*>(out + row * kHeadDim + c);
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
+              for (int e = 0; e < 4; ++e)
                 dst[e] = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]), pack_bf16(x[8 * e + 2], x[8 * e + 3]),
                                     pack_bf16(x[8 * e + 4], x[8 * e + 5]), pack_bf16(x[8 * e + 6], x[8 * e + 7]));
             }
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    : reinterpret_cast<float4*>(part + c);
             if (f)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) f[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+              for (int e = 0; e < 8; ++e) f[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         }
       }

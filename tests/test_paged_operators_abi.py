@@ -16,7 +16,9 @@ def lib():
 
 def test_null_handles_are_rejected(lib):
     one = (ctypes.c_int * 1)(0)
-    rows = N.oscar_rows(16, 128, 128)
+    rows = ctypes.addressof(keep := N.oscar_rows(16, 128, 128))
+    assert ctypes.sizeof(N.oscar_rows) == 24 and ctypes.sizeof(N.oscar_rope_tensor) == 56 and keep.row == 128
+    assert len(N._pack_rows(1, 2, 3)) == 24 and bytes(N.oscar_rope_tensor(1, 2, 3, 4, 5, 6, 7)) == N._pack_rope_tensor(1, 2, 3, 4, 5, 6, 7)
     assert lib.oscar_append_rotated(None, 0, 16, 128, 1.0, 0, None, None, rows, rows, None) == 1
     assert lib.oscar_int4_append(None, 0, 16, 16, None) == 1
     assert lib.oscar_int4_read(None, 0, 0, 0, 1, 16, 16, N.OSCAR_DTYPE_BF16, None) == 1
