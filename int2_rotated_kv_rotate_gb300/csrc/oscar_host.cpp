@@ -518,7 +518,8 @@ void place_tiles(const oscar_cache* c, const std::vector<WindowTile>& whole, int
   // equal shares: P borders at most, an item's fixed time each, and the merge's
   const long long share = (shared_total + 2LL * kWindowItemSteps * (n + P) + P - 1) / P;
   const long long cuts = std::min<long long>(P, n * 64LL);
-  const long long shared_cost = std::max<long long>(share, 2 * kWindowMinSteps + 2 * kWindowItemSteps) + kWindowMergeCost + cuts / 32;
+  const long long shared_cost = std::max<long long>(share, 2 * kWindowMinSteps + 2 * kWindowItemSteps) +
+                                (split && n_split ? 0 : kWindowMergeCost) + cuts / 32;
   const bool cut = shared_cost < longest && 4LL * P + 2 * (split ? n_split : 0) <= kWindowSlots;
   std::vector<std::vector<WindowTile>> of(P);
   auto add = [&](int cta, const WindowTile& t) { of[cta].push_back(t); };

@@ -596,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (again) break;
           const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-          const bool raise = top > m_ref + kRaise;  // also from -inf
-          if (!__any_sync(0xffffffffu, raise)) break;
-          const float f = raise ? ex2(m_ref - top) : 1.f;
-          if (raise) m_ref = top;
+          if (!__any_sync(0xffffffffu, top > m_ref + kRaise)) break;  // (also from -inf)
+          // all rows of the warp to their maxima, so that the others' turns come less often
+          const float f = top > m_ref ? ex2(m_ref - top) : 1.f;
+          m_ref = fmaxf(m_ref, top);
           l *= f;
           if (j == w.page0(b)) continue;  // (O is not there yet)
           done &= wait(ctl->o_done[b][buf ^ 1u], (n - 1) >> 1);
