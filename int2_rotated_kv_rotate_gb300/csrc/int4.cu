@@ -312,6 +312,10 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           } else {
             szv[b][i][0] = *at;
           }
+          // (what lies behind the last token may be anything, and is multiplied by a weight of 0)
+          if (valid < kUnit && 16 * b + 8 * (G == 8 ? i : i_lane) + gid >= valid)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) szv[b][i][g] = 0u;
 #pragma unroll
           for (int g = 0; g < NG; ++g) top = fmaxf(top, bf16_lo(szv[b][i][g]));
         }
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            p[i][j] = ex2(lg[b][i][j] - muse[j]);  // masked: exactly 0, and scale and zero are finite
+            p[i][j] = ex2(lg[b][i][j] - muse[j]);  // masked: exactly 0
             l_part[j] += p[i][j];
           }
         uint32_t bp[NG][2];

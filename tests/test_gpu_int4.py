@@ -21,10 +21,12 @@ LIMIT = 2.0 ** 126
 
 
 def make(lengths, hkv=2, gqa=4, group=32, layers=1, spare=0):
-    pages = sum((n + 63) // 64 for n in lengths) + spare
-    return KVCache(fmt=OSCAR_FORMAT_INT4, n_q_heads=hkv * gqa, n_kv_heads=hkv, group=group, n_layers=layers,
-                   max_requests=max(1, len(lengths)), max_pages=max(1, pages),
-                   max_pages_per_request=max(1, pages))
+    pages = max(1, sum((n + 63) // 64 for n in lengths) + spare)
+    cache = KVCache(fmt=OSCAR_FORMAT_INT4, n_q_heads=hkv * gqa, n_kv_heads=hkv, group=group, n_layers=layers,
+                    max_requests=max(1, len(lengths)), max_pages=pages, max_pages_per_request=pages)
+    at = cache.layout.codes  # what no token was written to: NaN scales and zeros
+    cache.mem[at:at + layers * pages * hkv * cache.layout.codes_page_bytes].fill_(255)
+    return cache
 
 
 def tokens(n, hkv, seed, scale_k=1.0, scale_v=1.0):
@@ -132,7 +134,6 @@ def check(out, out32, q, k, v, sv, group, label):
                                                 ((70, 500), 2, 2.0 ** -60, 2.0 ** 90), ((70, 500), 2, 1e-3, 2.0 ** -100)])
 def test_decode(gqa, group, lengths, hkv, sk, svs):
     cache = make(lengths, hkv=hkv, gqa=gqa, group=group)
-    cache.mem[cache.layout.codes:cache.layout.codes + 64].fill_(255)
     slots = [cache.alloc() for _ in lengths]
     kv = [tokens(n, hkv, 10 + i, sk, svs) for i, n in enumerate(lengths)]
     fill(cache, slots, kv)
