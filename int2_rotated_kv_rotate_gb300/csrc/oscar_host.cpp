@@ -485,17 +485,14 @@ oscar_status make_page_map(oscar_cache* c, const char* what) {
 // The tiles of a window plan as work items by CTA.  Either whole tiles, the longest first, each to
 // the CTA that is done soonest; or, where that leaves CTAs idle, an equal share of all steps to
 // each, so that a tile at a border of shares is cut.  Tiles of one block of rows are split over the
-// two blocks of accumulators where they are long enough and there is room for their parts.
+// two blocks of accumulators where they are long enough.
 void place_tiles(const oscar_cache* c, const std::vector<WindowTile>& whole, int G, std::vector<WindowTile>* tiles,
                  std::vector<WindowMerge>* merges, std::vector<int>* first_item, int* n_slots) {
   const int P = c->n_sm, n = int(whole.size());
   if (!n) return;
   auto one_block = [&](const WindowTile& t) { return t.n_tok * G <= kWindowRows / 2; };
   // An item's time in half steps (pages of two blocks, or two of one): its pages, and a fixed part.
-  long long n_split = 0;
-  for (const WindowTile& t : whole) n_split += one_block(t) && t.end >= kWindowSplitSteps;
-  const bool split = 2 * n_split <= kWindowSlots;
-  auto splits = [&](const WindowTile& t) { return split && one_block(t) && t.end >= kWindowSplitSteps; };
+  auto splits = [&](const WindowTile& t) { return one_block(t) && t.end >= kWindowSplitSteps; };
   auto cost = [&](const WindowTile& t, long long steps) { return (splits(t) ? 1 : 2) * steps + 2 * kWindowItemSteps; };
   // whole tiles
   std::vector<int> order(n), cta_of(n);
@@ -519,15 +516,17 @@ void place_tiles(const oscar_cache* c, const std::vector<WindowTile>& whole, int
   const long long share = (shared_total + 2LL * kWindowItemSteps * (n + P) + P - 1) / P;
   const long long cuts = std::min<long long>(P, n * 64LL);
   const long long shared_cost = std::max<long long>(share, 2 * kWindowMinSteps + 2 * kWindowItemSteps) +
-                                (split && n_split ? 0 : kWindowMergeCost) + cuts / 32;
-  const bool cut = shared_cost < longest && 4LL * P + 2 * (split ? n_split : 0) <= kWindowSlots;
+                                kWindowMergeCost + cuts / 32;
+  const bool cut = shared_cost < longest && 4LL * P <= kWindowSlots;  // (at most 2 P parts of cut tiles)
   std::vector<std::vector<WindowTile>> of(P);
   auto add = [&](int cta, const WindowTile& t) { of[cta].push_back(t); };
   auto finish = [&](const WindowTile& t, const std::vector<std::pair<int, WindowTile>>& parts) {
     // a tile's parts by CTA: their slots, and its merge
     const bool s = splits(t);
-    if (parts.size() == 1 && !s) {
-      add(parts[0].first, parts[0].second);
+    if (parts.size() == 1) {
+      WindowTile w = parts[0].second;
+      w.split = s;  // (its blocks are joined in the CTA)
+      add(parts[0].first, w);
       return;
     }
     const int per = s || !one_block(t) ? 2 : 1;

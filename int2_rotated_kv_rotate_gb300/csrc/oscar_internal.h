@@ -116,16 +116,16 @@ struct WindowReq {
 };
 // One work item of the tile kernel: queries tok0 .. tok0 + n_tok - 1 of request req, the heads of
 // kvh, steps [begin, end) of the tile's list of pages (two a step).  split (at most 128 rows): the
-// even pages of the list go to one block of accumulators, the odd ones to another, a part each.
-// slot: where the blocks' results go, one after the other; -1 where the item is the whole tile and
-// not split.  Items are stored by CTA.
+// even pages of the list go to one block of accumulators, the odd ones to another.  slot: where the
+// blocks' results go, one after the other, for the merge; -1 where the item is the whole tile (the
+// blocks of a split one are joined in the CTA).  Items are stored by CTA.
 constexpr int kWindowRows = 256;  // query rows (queries x G) of a tile at most, two blocks of 128
 constexpr size_t kWindowSlotBytes = kWindowRows / 2 * (8 + 4 * kHeadDim);  // (maximum, denominator), then rows
 constexpr int kWindowSlots = 1216;  // of a plan at most
 struct WindowTile {
   int req, kvh, tok0, n_tok, begin, end, slot, split;
 };
-// A tile of several parts: part k of block b is slot first_slot + stride k + b.
+// A tile that was cut: part k of block b is slot first_slot + stride k + b.
 struct WindowMerge {
   int req, kvh, tok0, n_tok, first_slot, n_parts, stride;
 };

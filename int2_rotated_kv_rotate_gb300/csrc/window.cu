@@ -29,7 +29,7 @@
 // 8-11 and 12-15 are the blocks' softmax, one thread a row.   S of a page is in
 // one of two buffers of 64 columns, P over it, so that S of the next page and O of the last one are
 // computed beside a page's softmax.  An item of at most 128 rows has its even pages in one block
-// and its odd ones in the other, each with results of its own.
+// and its odd ones in the other, which are joined through shared memory, or by the merge.
 // Where few tiles would leave SMs idle, the plan cuts their pages into parts, whose partial results
 // window_merge_kernel joins, in a fixed order.
 #include <cuda.h>
@@ -167,6 +167,10 @@ struct Control {
   // Page n of the block has buffer n % 2, whose completion is n / 2: S is written, P is written, O
   // holds the pages up to n (and P is read).
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
+  // A split item that is a whole tile: block 0's rows have O, block 1's are in shared memory, block 0
+  // has read them.  Completion n is the n-th such item.
+  uint64_t join_ready, join_full, join_done;
+  float2 join[kBlockRows];  // maximum and denominator of block 1's rows
   uint64_t drain[4];
   uint32_t tmem;
   int abort;
@@ -288,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->drain[b]), 1);
       mbar_init(smem_u32(&ctl->drain[2 + b]), 1);
     }
+    mbar_init(smem_u32(&ctl->join_ready), kBlockRows);
+    mbar_init(smem_u32(&ctl->join_full), kBlockRows);
+    mbar_init(smem_u32(&ctl->join_done), kBlockRows);
     ctl->abort = ctl->odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -296,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem::fence_after();
   const uint32_t tm = ctl->tmem;
-  pdl_wait();
-  pdl_trigger();
+  // The plan is older than the preceding kernel: only those who read rows or queries, or write
+  // results, wait for it, with their first item at hand.
   const int* counts = plan_counts(kp);
   const int G = kp.gqa;
   const int* first_item = reinterpret_cast<const int*>(kp.base + kp.lay.window_plan + counts[7]);  // of each CTA
@@ -335,6 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return done;
   };
   auto all = [](int done) -> bool { return __all_sync(0xffffffffu, done); };
+  if (ix0 == ix1) {  // no item: the launch still orders itself after the preceding kernel
+    pdl_wait();
+    pdl_trigger();
+  }
 
   if (warp < 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
@@ -348,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
       const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                         size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+      if (ix == ix0) {
+        pdl_wait();
+        pdl_trigger();
+      }
       // The first item's queries go before the pages: they would come behind the copies of five stages on
       // every SM (8192 queries, window 4096: 306 against 298 us).
       if (ix == ix0)
@@ -466,16 +481,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = (warp - 8) >> 2, wq = warp & 3, r = (wq << 5) | lane;
     const float scale = kLog2e * rsqrtf(float(kHeadDim));
     const uint32_t tl = tm + b * kBlockCols + (uint32_t(32 * wq) << 16);
-    uint32_t n = 0, nv = 1;  // pages of this block; fillings up to the item's first values
+    uint32_t n = 0, nv = 1, joins = 0;  // pages of this block; fillings up to the item's first values; joined items
     bool ok = true;
     for (int ix = ix0; ok && ix < ix1; ++ix) {
       const Work w = load_work(ix);
+      if (ix == ix0) pdl_wait();
       const int first = w.first_page(), end = w.end_page(), fillings = 2 * (w.it.end - w.it.begin);
       const int m = w.row(b, r);
       const bool mine = m < w.rows;
       uint8_t* slot = parts + size_t(w.it.slot < 0 ? 0 : w.it.slot + b) * kWindowSlotBytes;  // of a part, the block's
       if (b >= w.blocks) {
-        if (w.it.split && mine) reinterpret_cast<float2*>(slot)[r] = make_float2(-INFINITY, 0.f);  // no page for this block
+        if (w.it.split && w.it.slot >= 0 && mine) reinterpret_cast<float2*>(slot)[r] = make_float2(-INFINITY, 0.f);  // no page for this block
         nv += fillings;
         continue;
       }
@@ -629,8 +645,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = all(wait(ctl->o_done[b][(n - 1) & 1u], (n - 1) >> 1)))) break;
       tmem::fence_after();
       const bool odd = *reinterpret_cast<volatile int*>(&ctl->odd) != 0;
+      const bool whole_tile = w.it.slot < 0, join = w.it.split && whole_tile && w.blocks == 2;
+      // Joined blocks: the second's rows go through the queries' memory, which no product reads any
+      // more, 16-byte chunk c of row r at c ^ (r & 7) of its 512 bytes.
+      float4* joined = reinterpret_cast<float4*>(smem) + r * (kHeadDim / 4);
+      float f0 = 1.f, f1 = 0.f;  // what this row's O and the joined row's count
+      if (join && b == 1) {
+        if (!(ok = all(wait(ctl->join_ready, joins)))) break;
+        ctl->join[r] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
+        if (!idle) {
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            uint32_t o[32];
+            tmem::ld_x32(tl + kColO + c, o);
+            tmem::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              joined[(c / 4 + e) ^ (r & 7)] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                          __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          }
+        }
+        tmem::fence_before();
+        mbar_arrive(smem_u32(&ctl->join_full));
+        if (!(ok = all(wait(ctl->join_done, joins++)))) break;
+        continue;
+      }
+      if (join) {
+        mbar_arrive(smem_u32(&ctl->join_ready));
+        if (!(ok = all(wait(ctl->join_full, joins)))) break;
+        const float2 ml = ctl->join[r];
+        const float m0 = l == 0.f ? -INFINITY : m_ref, top = fmaxf(m0, ml.x);
+        if (top != -INFINITY) {
+          f0 = ex2(m0 - top);
+          f1 = ex2(ml.x - top);
+        }
+        l = fmaf(l, f0, ml.y * f1);
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool whole_tile = w.it.slot < 0;
+      f0 *= inv;
+      f1 *= inv;
       const size_t row = size_t(w.rq.row + w.it.tok0 + m / G) * kp.n_q_heads + size_t(w.it.kvh) * G + m % G;
       float* part = reinterpret_cast<float*>(slot + kBlockRows * 8) + size_t(r) * kHeadDim;
       if (mine && !whole_tile) reinterpret_cast<float2*>(slot)[r] = make_float2(l == 0.f ? -INFINITY : m_ref, l);
@@ -644,13 +697,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c + 32 < kHeadDim) tmem::ld_x32(tl + kColO + c + 32, o[(c / 32 + 1) & 1]);
           float x[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(cur[e]) * inv;
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(cur[e]) * f0;
+          if (join)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 y = joined[(c / 4 + e) ^ (r & 7)];
+              x[4 * e] = fmaf(y.x, f1, x[4 * e]);
+              x[4 * e + 1] = fmaf(y.y, f1, x[4 * e + 1]);
+              x[4 * e + 2] = fmaf(y.z, f1, x[4 * e + 2]);
+              x[4 * e + 3] = fmaf(y.w, f1, x[4 * e + 3]);
+            }
           if (odd && mine) {  // infinities and NaN that this row sees of the pages that were looked over
             const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
             const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
                               size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
 #pragma unroll 1
-            for (int j = w.page0(b); j < end; j += w.stride()) {
+            for (int j = join ? first : w.page0(b); j < end; j += join ? 1 : w.stride()) {
               if (whole_in_tile.has(j)) continue;
               const uint64_t see = w.visible(j, pos);
               const int lp = w.page(j);
@@ -687,6 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tmem::fence_before();  // O is read before the next item's first MMA writes it
+      if (join) {  // and the joined rows before the next queries come there
+        mbar_arrive(smem_u32(&ctl->join_done));
+        if (!(ok = all(wait(ctl->join_done, joins++)))) break;
+      }
     }
   }
   __syncwarp();
@@ -702,14 +768,18 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeSplit = 4;  // CTAs to a tile
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParams kp, const uint8_t* __restrict__ parts,
                                                                      uint16_t* __restrict__ out, float* __restrict__ out_f32) {
-  pdl_wait();
-  pdl_trigger();
-  const int* counts = plan_counts(kp);
+  const int* counts = plan_counts(kp);  // (the plan is older than the preceding kernel)
   const WindowMerge* merges = reinterpret_cast<const WindowMerge*>(kp.base + kp.lay.window_plan + counts[6]);
+  bool waited = false;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = kp.gqa;
   for (int e = blockIdx.x; e < counts[2] * kMergeSplit; e += gridDim.x) {
     const WindowMerge mg = merges[e / kMergeSplit];
     const WindowReq rq = plan_reqs(kp)[mg.req];
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
     for (int m = (e % kMergeSplit) * (kMergeThreads / 32) + warp; m < mg.n_tok * G; m += kMergeSplit * (kMergeThreads / 32)) {
       // part k of block m / 128: slot first_slot + stride k + m / 128
       const size_t step = size_t(mg.stride) * kWindowSlotBytes;
@@ -763,6 +833,10 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParam
       reinterpret_cast<uint2*>(out + row * kHeadDim)[lane] = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
       if (out_f32) reinterpret_cast<float4*>(out_f32 + row * kHeadDim)[lane] = y;
     }
+  }
+  if (!waited) {
+    pdl_wait();
+    pdl_trigger();
   }
 }
 
