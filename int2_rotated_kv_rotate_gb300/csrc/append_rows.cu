@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
 
 // Tokens [begin, end) of a request's 4-bit rows as values: fmaf(code, s, z) in fp32, rounded to bf16
 // where T is 16 bits.  Sixteen lanes a row, a head (K heads, then V heads) a half-warp, which walks
-// down kItemRows tokens, kBatch of them in flight.  HBM-bound.
+// down kItemRows tokens, eight of them in flight.  HBM-bound.
 constexpr int kReadThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp, int layer, int slot, int begin, int end,
@@ -398,55 +398,56 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
   const uint8_t* pool = kp.base + kp.lay.codes + size_t(layer) * kp.lay.codes_layer_stride + size_t(h) * kp.lay.codes_head_stride;
   const int group = l16 / (kp.group / 8);
   T* out = (kv ? v_out : k_out) + size_t(h) * kHeadDim + 8 * l16;
-  const size_t row = size_t(Hkv) * kHeadDim;
-  for (int p0 = begin + int(blockIdx.x) * kItemRows; p0 < end; p0 += int(gridDim.x) * kItemRows) {
-    const int n = min(kItemRows, end - p0), lp = p0 / kPage, t0 = p0 % kPage;
-    int page[2];  // the rows lie in one page or two
-    page[0] = lp < kp.max_pages_per_request ? ptab[lp] : -1;
-    page[1] = t0 + n <= kPage ? page[0] : lp + 1 < kp.max_pages_per_request ? ptab[lp + 1] : -1;
-    const uint8_t* rows[2];
-    bool ok[2];
+  const long long row = (long long)Hkv * kHeadDim;
+  const int shift = 4 * (l16 >> 2) + kv * (kInt4Half * kInt4Row), chunk = l16 & 3;
+  // The tokens by sixteens of their places, each of which lies in one half page.
+  for (int p0 = (begin / kItemRows + int(blockIdx.x)) * kItemRows; p0 < end; p0 += int(gridDim.x) * kItemRows) {
+    const int lp = p0 / kPage, t0 = p0 % kPage;
+    const int page = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+    const bool ok = page >= 0 && page < kp.max_pages;  // (else zeros, and the flag)
+    if (!ok && l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+    const uint8_t* at = pool + size_t(unsigned(ok ? page : 0)) * unsigned(kp.lay.codes_page_stride);
+    const uint8_t* rows = at + int4_word(t0, 0, 0, ng) + shift;
+    const uint32_t* szs = reinterpret_cast<const uint32_t*>(at + int4_scale(t0, group, kv, ng));
+    T* to = out + (long long)(p0 - begin) * row;  // (rows before begin are not touched)
+    auto word = [&](int r) { return ok ? *reinterpret_cast<const uint32_t*>(rows + r * kInt4Row + 16 * (chunk ^ ((r >> 1) & 3))) : 0u; };
+    auto scale = [&](int r) { return ok ? szs[r * ng] : 0u; };
+    auto put = [&](int r, uint32_t w, uint32_t sz) {
+      const float s = bf16_lo(sz), z = bf16_hi(sz);
+      // a code as the low byte of 2^23: its value by a subtraction
+      const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+      const uint64_t ss = pair(s, s), zz = pair(z, z), base = pair(-8388608.f, -8388608.f);
+      float2 x[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ok[i] = page[i] >= 0 && page[i] < kp.max_pages;
-      if (!ok[i] && l16 == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
-      const unsigned at = unsigned(ok[i] ? page[i] : 0);
-      rows[i] = pool + size_t(at) * unsigned(kp.lay.codes_page_stride);
-    }
-    T* to = out + size_t(p0 - begin) * row;
-#pragma unroll 2
-    for (int r = 0; r < n; r += kBatch) {
-      uint32_t w[kBatch], sz[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int t = t0 + r + b;
-        const bool behind = t >= kPage, there = r + b < n && (behind ? ok[1] : ok[0]);  // (else zeros)
-        const uint8_t* at = behind ? rows[1] : rows[0];
-        w[b] = there ? *reinterpret_cast<const uint32_t*>(at + int4_word(t % kPage, l16, kv, ng)) : 0u;
-        sz[b] = there ? *reinterpret_cast<const uint32_t*>(at + int4_scale(t % kPage, group, kv, ng)) : 0u;
+      for (int i = 0; i < 4; ++i)
+        x[i] = unpair(fma2(add2(pair(__uint_as_float(permute(even, 0x4b000000u, 0x7650 + i)),
+                                     __uint_as_float(permute(odd, 0x4b000000u, 0x7650 + i))),
+                                base),
+                           ss, zz));
+      T* p = to + r * row;
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y),
+                                                  pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
+      } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
       }
+    };
+    if (begin <= p0 && p0 + kItemRows <= end) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b, to += row) {
-        if (r + b >= n) break;
-        const float s = bf16_lo(sz[b]), z = bf16_hi(sz[b]);
-        // a code as the low byte of 2^23: its value by a subtraction
-        const uint32_t even = w[b] & 0x0f0f0f0fu, odd = (w[b] >> 4) & 0x0f0f0f0fu;
-        const uint64_t ss = pair(s, s), zz = pair(z, z), base = pair(-8388608.f, -8388608.f);
-        float2 x[4];
+      for (int r = 0; r < kItemRows; r += 2 * kBatch) {
+        uint32_t w[2 * kBatch], sz[2 * kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = unpair(fma2(add2(pair(__uint_as_float(permute(even, 0x4b000000u, 0x7650 + i)),
-                                       __uint_as_float(permute(odd, 0x4b000000u, 0x7650 + i))),
-                                  base),
-                             ss, zz));
-        if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y),
-                                                     pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
-        } else {
-          reinterpret_cast<float4*>(to)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-          reinterpret_cast<float4*>(to)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+        for (int b = 0; b < 2 * kBatch; ++b) {
+          w[b] = word(r + b);
+          sz[b] = scale(r + b);
         }
+#pragma unroll
+        for (int b = 0; b < 2 * kBatch; ++b) put(r + b, w[b], sz[b]);
       }
+    } else {
+#pragma unroll 1
+      for (int r = max(0, begin - p0); r < min(kItemRows, end - p0); ++r) put(r, word(r), scale(r));
     }
   }
 }
@@ -473,7 +474,7 @@ int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bo
 
 int launch_int4_read(const KernelParams& kp, int layer, int slot, int begin, int end, void* k_out, void* v_out, bool f32,
                      int n_sm, void* stream, int* launches) {
-  const dim3 grid(std::min((end - begin + kItemRows - 1) / kItemRows, 16 * n_sm),
+  const dim3 grid(std::min((end + kItemRows - 1) / kItemRows - begin / kItemRows, 16 * n_sm),
                   (2 * kp.n_kv_heads + kReadThreads / 16 - 1) / (kReadThreads / 16));
   const int e = f32 ? launch_ex(int4_read_kernel<float>, grid, dim3(kReadThreads), 0, stream, kp, layer, slot, begin, end,
                                 static_cast<float*>(k_out), static_cast<float*>(v_out))

@@ -81,9 +81,10 @@ def test_rows_are_the_definitions(group, n, step):
     got = cache.read(0, slot, 0, n, dtype=torch.float32)
     for x, y in zip((k, v), got):
         assert torch.equal(y.cpu(), values(x, group))
-    half = cache.read(0, slot, n // 3, n)
-    for x, y in zip(got, half):
-        assert torch.equal(y, x[n // 3:].bfloat16())
+    for a, b in ((n // 3, n), (n // 2, n - n // 7), (0, 1)):
+        for dtype in (torch.bfloat16, torch.float32):
+            for x, y in zip(got, cache.read(0, slot, a, b, dtype=dtype)):
+                assert torch.equal(y, x[a:b].to(dtype))
     # the stored layout: bits and words as documented
     t = n - 1
     head, ng = cache.layout.codes_page_bytes, 128 // group

@@ -136,6 +136,22 @@ def test_tiles_are_cut_and_joined():
     check(out[7:], o32[7:], q[7:], *kv[1], 40, 0, 0, "short")
 
 
+def test_many_small_tiles():
+    """More small tiles than SMs: a CTA joins the blocks of several, beside larger and single ones."""
+    lengths = [200 + 37 * i for i in range(40)]
+    new = [(5, 2, 9, 1, 40)[i % 5] for i in range(40)]
+    c, slots, kv = filled(lengths, 8, 4)
+    q = torch.randn(sum(new), 32, 128, device="cuda").bfloat16()
+    c.plan_window(slots, new, n_sink=4, window=700)
+    out, o32 = run(c, q)
+    at = 0
+    for i, n in enumerate(new):
+        if i % 3 == 0:
+            check(out[at:at + n], o32[at:at + n], q[at:at + n], *kv[i], n, 4, 700, f"request {i} {c.window_info()}")
+        at += n
+    assert torch.equal(run(c, q)[1], o32) and c.status() == (0, 0)
+
+
 @pytest.mark.parametrize("gqa", [4, 8])
 @pytest.mark.parametrize("new", [(1, 1), (300, 2)])
 def test_infinities_and_nan_reach_only_those_who_see_them(gqa, new):
