@@ -17,7 +17,7 @@
 // extremes are found on packed bf16, the rest in pairs of fp32 by products with approximate
 // reciprocals; the few rows for which that is not known to give the definition's bits are taken
 // again, as it stands, after the item's others.  (With divisions and single operations 8192 tokens of 8
-// kv-heads took 42 us; 21 now, 2.1 TB/s.)
+// kv-heads took 42 us; 20 now, 2.3 TB/s.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -221,8 +221,14 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
   }
   const unsigned page_stride = unsigned(INT4 ? kp.lay.codes_page_stride : kp.lay.bf16_page_stride);
   bool waited = false;
-  for (int ix = blockIdx.x; ix < n_items; ix += gridDim.x) {
-    const AppendItem it = reinterpret_cast<const AppendItem*>(kp.base + kp.lay.append_items)[ix];
+  for (int ix = blockIdx.x; ix < n_items * p.item_parts; ix += gridDim.x) {
+    AppendItem it = reinterpret_cast<const AppendItem*>(kp.base + kp.lay.append_items)[ix / p.item_parts];
+    if (p.item_parts > 1) {  // a part of the item's rows
+      const int rows = kItemRows / p.item_parts, at = ix % p.item_parts * rows;
+      it.begin += at;
+      it.count = min(rows, it.count - at);
+      if (it.count <= 0) continue;
+    }
     const AppendReq a = reinterpret_cast<const AppendReq*>(kp.base + kp.lay.append_reqs)[it.req];
     const bool slot_ok = a.slot >= 0 && a.slot < kp.max_requests;
     if (!slot_ok && threadIdx.x == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
@@ -454,13 +460,16 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
 
 }  // namespace
 
-int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bool int4, bool rope, int n_items, void* stream,
-                       int* launches) {
+int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bool int4, bool rope, int n_items, long long n_rows,
+                       int n_sm, void* stream, int* launches) {
   // whole heads, evenly over the CTAs of an item, an even number of them in each (full warps)
   const int H = p.q.n_heads + 2 * kp.n_kv_heads, most = kMaxThreads / 16;
   const int chunks = (H + most - 1) / most;
   p.chunk_heads = ((H + chunks - 1) / chunks + 1) / 2 * 2;
-  const dim3 grid(n_items, chunks), block(16 * p.chunk_heads);
+  // Where whole items would leave every SM less than four CTAs, halves of them, if most have so many
+  // rows (8192 rows of 16 heads into 4-bit pages: 21.3 against 19.7 us).
+  p.item_parts = !rope && (long long)n_items * chunks < 4LL * n_sm && n_rows > 8LL * n_items ? 2 : 1;
+  const dim3 grid(n_items * p.item_parts, chunks), block(16 * p.chunk_heads);
   const size_t smem = rope ? size_t(kItemRows) * (p.rotary_dim / 2) * sizeof(float4) : 0;
   auto go = [&](auto kernel) { return launch_ex(kernel, grid, block, smem, stream, kp, layer, p); };
   int e;

@@ -1062,7 +1062,8 @@ oscar_status oscar_append_rotated(oscar_cache* c, int layer, const uint64_t* ste
   p.magnitude = magnitude;
   p.interleaved = (flags & OSCAR_ROPE_INTERLEAVED) != 0;
   p.positions64 = (flags & OSCAR_ROPE_POSITIONS64) != 0;
-  const int e = launch_append_rows(kernel_params(c), layer, p, is_int4(c), true, c->app_items, stream, &g_launches);
+  const int e = launch_append_rows(kernel_params(c), layer, p, is_int4(c), true, c->app_items, c->app_rows, c->n_sm, stream,
+                                   &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "rotated append launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }
@@ -1086,7 +1087,8 @@ oscar_status oscar_int4_append(oscar_cache* c, int layer, const void* k_new, con
   p.v_vec = reinterpret_cast<uintptr_t>(v_new) % 16 == 0;
   oscar_status st = check_device(c);
   if (st) return st;
-  const int e = launch_append_rows(kernel_params(c), layer, p, true, false, c->app_items, stream, &g_launches);
+  const int e = launch_append_rows(kernel_params(c), layer, p, true, false, c->app_items, c->app_rows, c->n_sm, stream,
+                                   &g_launches);
   if (e) return fail(OSCAR_ERR_CUDA, "int4 append launch: %s", cudaGetErrorString(cudaError_t(e)));
   return OSCAR_OK;
 }

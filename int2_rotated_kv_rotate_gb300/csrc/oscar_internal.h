@@ -308,7 +308,7 @@ int launch_rope(const RopeParams& p, int dtype, bool aligned, int n_sm, void* st
 
 // Appends with rotary positions and of 4-bit rows (append_rows.cu): bf16 rows of the pending
 // reservation, strides in elements; *_vec: rows and heads start on 16-byte boundaries.  The last
-// field is the launcher's.
+// fields are the launcher's.
 struct AppendRowsParams {
   RopeTensor q;  // n_heads 0: none
   const void *k, *v;
@@ -319,10 +319,10 @@ struct AppendRowsParams {
   float magnitude;
   bool interleaved, positions64;
   bool q_in_vec, q_out_vec, k_vec, v_vec;
-  int chunk_heads;
+  int chunk_heads, item_parts;
 };
-int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bool int4, bool rope, int n_items, void* stream,
-                       int* launches);
+int launch_append_rows(const KernelParams& kp, int layer, AppendRowsParams p, bool int4, bool rope, int n_items, long long n_rows,
+                       int n_sm, void* stream, int* launches);
 int launch_int4_read(const KernelParams& kp, int layer, int slot, int begin, int end, void* k_out, void* v_out, bool f32,
                      int n_sm, void* stream, int* launches);
 // Decode over 4-bit pages (int4.cu).
