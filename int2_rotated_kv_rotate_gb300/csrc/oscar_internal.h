@@ -265,8 +265,8 @@ struct WindowWorkspace {
   size_t total;
 };
 int launch_window(const KernelParams& kp, int layer, const void* map, const void* q, void* out, float* out_f32, uint8_t* ws,
-                  const WindowWorkspace& wl, bool rows, bool deep, bool tiles, bool merges, int n_sm, void* stream, int* launches);
-int window_rows_resident_ctas(int gqa, bool deep, int n_sm);
+                  const WindowWorkspace& wl, bool rows, bool tiles, bool merges, int n_sm, void* stream, int* launches);
+int window_rows_resident_ctas(int gqa, int n_sm);
 
 // CTAs of the decode kernel of this shape that fit on the GPU at once (occupancy x SMs);
 // the planner sizes work items so that one wave holds them all.
