@@ -11,7 +11,7 @@
 //
 // Rotary: the row that is stored is the turned one rounded to bf16, as by RotaryEmbedding and an
 // append after it, bit for bit.
-// HBM-bound when there are many rows, 61 us (5.5 TB/s) for 13656 rows of 32 + 8 + 8 heads; 64 registers a thread,
+// HBM-bound when there are many rows, 61 us (5.5 TB/s) for 13635 rows of 32 + 8 + 8 heads; 64 registers a thread,
 // four CTAs an SM (384 threads at 56 registers spill: 93 us).
 //
 // 4 bits, per token and group of 32 or 128 channels: s = bf16((max - min) / 15), z = bf16(min)
@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "int4.cuh"
 #include "oscar_internal.h"
+#include "packed.cuh"
 #include "rope_dev.cuh"
 
 namespace oscar {
@@ -63,37 +64,6 @@ __device__ __forceinline__ void store8(uint16_t* p, uint4 v, bool vec) {
   }
 }
 
-// Two floats in one register pair, and operations on both.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
 // Larger of each half, NaN where either is.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -162,14 +132,14 @@ __device__ __forceinline__ uint2 quantize8(uint4 v, int lanes, unsigned mask, bo
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));  // at most 1 unit in the last place off
   inv = s16 == 0u ? 0.f : inv;                           // the codes of a scale of 0
   // quotients in [0, 15 (1 + 2^-8)]: the nearest whole number is in the low bits of t + 1.5 * 2^23
-  const uint64_t neg_lo2 = pair(neg_lo, neg_lo), inv2 = pair(inv, inv), neg_s2 = pair(-s, -s), magic = pair(12582912.f, 12582912.f);
+  const uint64_t neg_lo2 = pack2(neg_lo, neg_lo), inv2 = pack2(inv, inv), neg_s2 = pack2(-s, -s), magic = pack2(12582912.f, 12582912.f);
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t d = add2(pair(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2);
+    const uint64_t d = add2(pack2(bf16_lo(w[i]), bf16_hi(w[i])), neg_lo2);
     uint64_t t = mul2(d, inv2);
     t = fma2(fma2(t, neg_s2, d), inv2, t);
-    const float2 bits = unpair(add2(t, magic));
+    const float2 bits = unpack2(add2(t, magic));
     c[2 * i] = __float_as_uint(bits.x);
     c[2 * i + 1] = __float_as_uint(bits.y);
   }
@@ -304,7 +274,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
               if (c0 + 2 * i < R) {
                 const float4 f = at[i];
                 const float u = bf16_lo(w[i]), t = bf16_hi(w[i]);
-                const float2 o = unpair(fma2(pair(u, u), pair(f.x, f.y), mul2(pair(t, t), pair(f.z, f.w))));
+                const float2 o = unpack2(fma2(pack2(u, u), pack2(f.x, f.y), mul2(pack2(t, t), pack2(f.z, f.w))));
                 w[i] = pack_bf16(o.x, o.y);
               }
           }
@@ -318,8 +288,8 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSM) append_rows_kernel(Kernel
             for (int i = 0; i < 4; ++i) {
               const float4 f = at[i * eighth];
               const uint32_t X = first ? w[i] : y[i], Y = first ? y[i] : w[i];
-              const float2 o = unpair(fma2(pair(bf16_lo(X), bf16_hi(X)), pair(f.x, f.y),
-                                           mul2(pair(bf16_lo(Y), bf16_hi(Y)), pair(f.z, f.w))));
+              const float2 o = unpack2(fma2(pack2(bf16_lo(X), bf16_hi(X)), pack2(f.x, f.y),
+                                           mul2(pack2(bf16_lo(Y), bf16_hi(Y)), pack2(f.z, f.w))));
               w[i] = pack_bf16(o.x, o.y);
             }
           }
@@ -424,11 +394,11 @@ __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(KernelParams kp
       const float s = bf16_lo(sz), z = bf16_hi(sz);
       // a code as the low byte of 2^23: its value by a subtraction
       const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-      const uint64_t ss = pair(s, s), zz = pair(z, z), base = pair(-8388608.f, -8388608.f);
+      const uint64_t ss = pack2(s, s), zz = pack2(z, z), base = pack2(-8388608.f, -8388608.f);
       float2 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[i] = unpair(fma2(add2(pair(__uint_as_float(permute(even, 0x4b000000u, 0x7650 + i)),
+        x[i] = unpack2(fma2(add2(pack2(__uint_as_float(permute(even, 0x4b000000u, 0x7650 + i)),
                                      __uint_as_float(permute(odd, 0x4b000000u, 0x7650 + i))),
                                 base),
                            ss, zz));

@@ -45,6 +45,7 @@
 
 #include "common.cuh"
 #include "oscar_internal.h"
+#include "packed.cuh"
 #include "tmem.cuh"
 
 namespace oscar {
@@ -200,24 +201,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -606,13 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) {
             const uint32_t* x = e < 16 ? s[0] + 2 * e : s[1] + 2 * (e - 16);
             mx[e & 3] = max3(mx[e & 3], __uint_as_float(x[0]), __uint_as_float(x[1]));
-            float pa, pb;
-            unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, minus_ref), pa, pb);
-            pa = ex2(pa);
-            pb = ex2(pb);
-            if (e & 1) l2 = add2(l2, pack2(pa, pb));
-            else l3 = add2(l3, pack2(pa, pb));
-            pw[e] = pack_bf16(pa, pb);
+            float2 p = unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, minus_ref));
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            if (e & 1) l2 = add2(l2, pack2(p.x, p.y));
+            else l3 = add2(l3, pack2(p.x, p.y));
+            pw[e] = pack_bf16(p.x, p.y);
           }
           if (again) break;
           const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
@@ -635,9 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem::st_x32(ts, pw);
-        float la, lb;
-        unpack2(add2(l2, l3), la, lb);
-        l += la + lb;
+        const float2 sums = unpack2(add2(l2, l3));
+        l += sums.x + sums.y;
         tmem::wait_st();
         tmem::fence_before();
         mbar_arrive(smem_u32(&ctl->p_full[b][buf]));
