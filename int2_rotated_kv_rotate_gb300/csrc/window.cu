@@ -335,133 +335,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp < 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-  if (warp == 0) {
-    // ---------------------------------------------------------------- pages
-    uint32_t n = 0, issued = 0;  // fillings of stages: keys and values of each step in turn
-    bool ok = true;
-    for (int ix = ix0; ok && ix < ix1; ++ix) {
-      const Work w = load_work(ix);
-      const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
-      if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
-      const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
-                        size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
-      if (ix == ix0) {
-        pdl_wait();
-        pdl_trigger();
-      }
-      // The first item's queries go before the pages: they would come behind the copies of five stages on
-      // every SM (8192 queries, window 4096: 306 against 298 us).
-      if (ix == ix0)
-        for (int b = 0; ok && b < w.blocks; ++b) ok = all(wait(ctl->q_full[b], 0));
-      for (int i = w.it.begin; ok && i < w.it.end; ++i) {
-        const int two = min(2, w.pages - 2 * i);
-        int y[2] = {0, 0};
-        for (int j = 0; j < two; ++j) {
-          const int lp = w.page(2 * i + j);
-          int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
-          if (phys < 0 || phys >= kp.max_pages) {  // page 0 instead, and the flag
-            if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
-            phys = 0;
-          }
-          y[j] = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- pages
+      uint32_t n = 0, issued = 0;  // fillings of stages: keys and values of each step in turn
+      bool ok = true;
+      for (int ix = ix0; ok && ix < ix1; ++ix) {
+        const Work w = load_work(ix);
+        const bool slot_ok = w.rq.slot >= 0 && w.rq.slot < kp.max_requests;
+        if (!slot_ok && lane == 0) flag(kp, OSCAR_FLAG_BAD_SLOT);
+        const int* ptab = reinterpret_cast<const int*>(kp.base + kp.lay.page_table) +
+                          size_t(slot_ok ? w.rq.slot : 0) * kp.max_pages_per_request;
+        if (ix == ix0) {
+          pdl_wait();
+          pdl_trigger();
         }
-        for (int kv = 0; ok && kv < 2; ++kv, ++n) {
-          const uint32_t st = n % kStages;
-          const int done = n >= kStages ? wait(ctl->empty[st], n / kStages - 1) : 1;
-          if (lane == 0 && done) {  // (lane 0 polled: no copy into a stage that was not left)
-            const uint32_t bar = smem_u32(&ctl->full[st]), dst = sst + st * kStageBytes;
-            mbar_expect_tx(bar, two * (kStageBytes / 2));
-            for (int j = 0; j < two; ++j) {
-              tma_load(dst + j * (kHalf / 2), &map, 0, y[j] + kv * kPage, bar);
-              tma_load(dst + kHalf + j * (kHalf / 2), &map, 64, y[j] + kv * kPage, bar);
+        // The first item's queries go before the pages: they would come behind the copies of five stages on
+        // every SM (8192 queries, window 4096: 306 against 298 us).
+        if (ix == ix0)
+          for (int b = 0; ok && b < w.blocks; ++b) ok = all(wait(ctl->q_full[b], 0));
+        for (int i = w.it.begin; ok && i < w.it.end; ++i) {
+          const int two = min(2, w.pages - 2 * i);
+          int y[2] = {0, 0};
+          for (int j = 0; j < two; ++j) {
+            const int lp = w.page(2 * i + j);
+            int phys = lp < kp.max_pages_per_request ? ptab[lp] : -1;
+            if (phys < 0 || phys >= kp.max_pages) {  // page 0 instead, and the flag
+              if (lane == 0) flag(kp, OSCAR_FLAG_BAD_PAGE);
+              phys = 0;
             }
+            y[j] = ((layer * kp.max_pages + phys) * kp.n_kv_heads + w.it.kvh) * (2 * kPage);
           }
-          if ((ok = all(done))) issued = n + 1;
+          for (int kv = 0; ok && kv < 2; ++kv, ++n) {
+            const uint32_t st = n % kStages;
+            const int done = n >= kStages ? wait(ctl->empty[st], n / kStages - 1) : 1;
+            if (lane == 0 && done) {  // (lane 0 polled: no copy into a stage that was not left)
+              const uint32_t bar = smem_u32(&ctl->full[st]), dst = sst + st * kStageBytes;
+              mbar_expect_tx(bar, two * (kStageBytes / 2));
+              for (int j = 0; j < two; ++j) {
+                tma_load(dst + j * (kHalf / 2), &map, 0, y[j] + kv * kPage, bar);
+                tma_load(dst + kHalf + j * (kHalf / 2), &map, 64, y[j] + kv * kPage, bar);
+              }
+            }
+            if ((ok = all(done))) issued = n + 1;
+          }
         }
       }
-    }
-    // the last arrivals on the stages' barriers come before the CTA leaves
-    for (uint32_t k = n > kStages ? n - kStages : 0; ok && k < n; ++k) ok = all(wait(ctl->empty[k % kStages], k / kStages));
-    if (!ok)  // copies still in flight land first, too
-      for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
-        mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
-  } else if (warp == 1 || warp == 2) {
-    // ---------------------------------------------------------------- S = Q K^T of block b
-    const int b = warp - 1;
-    constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
-    const uint64_t qb = tmem::sdesc_sw128(sq + b * kQBlock, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
-    uint32_t f = 0, items_done = 0, n = 0;  // fillings; items and pages of the block
-    bool ok = true;
-    for (int ix = ix0; ok && ix < ix1; ++ix) {
-      const Work w = load_work(ix);
-      const bool here = b < w.blocks;
-      if (here) ok = all(wait(ctl->q_full[b], items_done++));
-      for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
-        const uint32_t st = f % kStages;
-        const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
-        ok = all(wait(ctl->full[st], f / kStages));
-        if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
-        for (int j = j0; ok && j < j1; ++j, ++n) {
-          const uint32_t buf = n & 1u;
-          const int done = n >= 2 ? wait(ctl->o_done[b][buf], (n >> 1) - 1) : 1;
-          tmem::fence_after();
-          if (elect_one()) {
-            const uint32_t d = tm + b * kBlockCols + buf * kPage;
-            const uint64_t kb = kd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
+      // the last arrivals on the stages' barriers come before the CTA leaves
+      for (uint32_t k = n > kStages ? n - kStages : 0; ok && k < n; ++k) ok = all(wait(ctl->empty[k % kStages], k / kStages));
+      if (!ok)  // copies still in flight land first, too
+        for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+          mbar_wait(smem_u32(&ctl->full[k % kStages]), (k / kStages) & 1u);
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------------- S = Q K^T of block b
+      const int b = warp - 1;
+      constexpr uint32_t kIdS = tmem::idesc_bf16(kBlockRows, kPage, false);
+      const uint64_t qb = tmem::sdesc_sw128(sq + b * kQBlock, 16, 1024), kd = tmem::sdesc_sw128(sst, 16, 1024);
+      uint32_t f = 0, items_done = 0, n = 0;  // fillings; items and pages of the block
+      bool ok = true;
+      for (int ix = ix0; ok && ix < ix1; ++ix) {
+        const Work w = load_work(ix);
+        const bool here = b < w.blocks;
+        if (here) ok = all(wait(ctl->q_full[b], items_done++));
+        for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
+          const uint32_t st = f % kStages;
+          const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
+          ok = all(wait(ctl->full[st], f / kStages));
+          if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
+          for (int j = j0; ok && j < j1; ++j, ++n) {
+            const uint32_t buf = n & 1u;
+            const int done = n >= 2 ? wait(ctl->o_done[b][buf], (n >> 1) - 1) : 1;
+            tmem::fence_after();
+            if (elect_one()) {
+              const uint32_t d = tm + b * kBlockCols + buf * kPage;
+              const uint64_t kb = kd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              tmem::mma_ss(d, qb + ((c >> 2) * (kQBlock / 2) + (c & 3) * 32) / 16, kb + ((c >> 2) * kHalf + (c & 3) * 32) / 16,
-                           kIdS, c > 0);
-            tmem::commit(smem_u32(&ctl->s_full[b][buf]));
-            if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+              for (int c = 0; c < 8; ++c)
+                tmem::mma_ss(d, qb + ((c >> 2) * (kQBlock / 2) + (c & 3) * 32) / 16, kb + ((c >> 2) * kHalf + (c & 3) * 32) / 16,
+                             kIdS, c > 0);
+              tmem::commit(smem_u32(&ctl->s_full[b][buf]));
+              if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            }
+            ok = all(done);
           }
-          ok = all(done);
         }
       }
-    }
-    if (!ok) {  // MMAs in flight end before the tensor memory is freed
-      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[b]));
-      __syncwarp();
-      mbar_wait(smem_u32(&ctl->drain[b]), 0);
-    }
-  } else if (warp == 4 || warp == 5) {
-    // ---------------------------------------------------------------- O += P V of block b
-    const int b = warp - 4;
-    constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
-    const uint64_t vd = tmem::sdesc_sw128(sst, kHalf, 1024);
-    uint32_t f = 1, n = 0;
-    bool ok = true;
-    for (int ix = ix0; ok && ix < ix1; ++ix) {
-      const Work w = load_work(ix);
-      const bool here = b < w.blocks;
-      for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
-        const uint32_t st = f % kStages;
-        const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
-        ok = all(wait(ctl->full[st], f / kStages));
-        if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
-        for (int j = j0; ok && j < j1; ++j, ++n) {
-          const uint32_t buf = n & 1u;
-          const int done = wait(ctl->p_full[b][buf], n >> 1);
-          tmem::fence_after();
-          if (elect_one()) {
-            const uint32_t a = tm + b * kBlockCols + buf * kPage, d = tm + b * kBlockCols + kColO;
-            const uint64_t vb = vd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
+      if (!ok) {  // MMAs in flight end before the tensor memory is freed
+        if (elect_one()) tmem::commit(smem_u32(&ctl->drain[b]));
+        __syncwarp();
+        mbar_wait(smem_u32(&ctl->drain[b]), 0);
+      }
+    } else if (warp == 4 || warp == 5) {
+      // ---------------------------------------------------------------- O += P V of block b
+      const int b = warp - 4;
+      constexpr uint32_t kIdO = tmem::idesc_bf16(kBlockRows, kHeadDim, true);
+      const uint64_t vd = tmem::sdesc_sw128(sst, kHalf, 1024);
+      uint32_t f = 1, n = 0;
+      bool ok = true;
+      for (int ix = ix0; ok && ix < ix1; ++ix) {
+        const Work w = load_work(ix);
+        const bool here = b < w.blocks;
+        for (int i = w.it.begin; ok && i < w.it.end; ++i, f += 2) {
+          const uint32_t st = f % kStages;
+          const int j0 = 2 * i + (w.it.split ? b : 0), j1 = here ? min(w.it.split ? j0 + 1 : j0 + 2, w.pages) : 0;
+          ok = all(wait(ctl->full[st], f / kStages));
+          if (j0 >= j1 && lane == 0) mbar_arrive(smem_u32(&ctl->empty[st]));
+          for (int j = j0; ok && j < j1; ++j, ++n) {
+            const uint32_t buf = n & 1u;
+            const int done = wait(ctl->p_full[b][buf], n >> 1);
+            tmem::fence_after();
+            if (elect_one()) {
+              const uint32_t a = tm + b * kBlockCols + buf * kPage, d = tm + b * kBlockCols + kColO;
+              const uint64_t vb = vd + st * (kStageBytes >> 4) + (j & 1) * (kHalf / 2 / 16);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, j > w.page0(b) || c > 0);
-            tmem::commit(smem_u32(&ctl->o_done[b][buf]));
-            if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+              for (int c = 0; c < 4; ++c) tmem::mma_ts(d, a + 8 * c, vb + c * (2048 / 16), kIdO, j > w.page0(b) || c > 0);
+              tmem::commit(smem_u32(&ctl->o_done[b][buf]));
+              if (j == j1 - 1) tmem::commit(smem_u32(&ctl->empty[st]));
+            }
+            ok = all(done);
           }
-          ok = all(done);
         }
       }
+      if (!ok) {
+        if (elect_one()) tmem::commit(smem_u32(&ctl->drain[2 + b]));
+        __syncwarp();
+        mbar_wait(smem_u32(&ctl->drain[2 + b]), 0);
+      }
     }
-    if (!ok) {
-      if (elect_one()) tmem::commit(smem_u32(&ctl->drain[2 + b]));
-      __syncwarp();
-      mbar_wait(smem_u32(&ctl->drain[2 + b]), 0);
-    }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---------------------------------------------------------------- softmax of block b
