@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Bounded wait of a whole warp for a barrier's completion `index`.  Every lane polls: one lane's
   // polls, with the warp brought together behind them, cost some 300 cycles of each of a page's three
-  // hand-overs (2432 queries on 8192 tokens: 292 against 188 us).  After a wait that ran out MMAs
+  // hand-overs (2432 queries on 8192 tokens: 292 against 204 us, and 188 with try_wait from the first
+  // poll on, as here).  After a wait that ran out MMAs
   // and stores of that page still go out, on memory of this CTA; the roles vote once a page, and
   // every role then leaves its loop.
   auto wait = [&](uint64_t& bar, uint32_t index) -> int {
