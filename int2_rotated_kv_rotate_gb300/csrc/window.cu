@@ -630,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the rows' results
       if (!(ok = all(wait(ctl->o_done[b][(n - 1) & 1u], (n - 1) >> 1)))) break;
       tmem::fence_after();
-      const bool odd = *reinterpret_cast<volatile int*>(&ctl->odd) != 0;
       const bool whole_tile = w.it.slot < 0, join = w.it.split && whole_tile && w.blocks == 2;
       // Joined blocks: the second's rows go through the queries' memory, which no product reads any
       // more, 16-byte chunk c of row r at c ^ (r & 7) of its 512 bytes.
@@ -667,6 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l = fmaf(l, f0, ml.y * f1);
       }
+      // Read behind every look at the row's values: its own block's (o_done), and a joined block's, at
+      // other pages (join_full).
+      const bool odd = *reinterpret_cast<volatile int*>(&ctl->odd) != 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
       f1 *= inv;
