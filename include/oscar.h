@@ -291,8 +291,9 @@ oscar_status oscar_append_rotated(oscar_cache* cache, int layer, const uint64_t*
  * them once they are appended) into k_out, v_out [dev] [end - begin][H_kv][d], contiguous, in
  * dtype OSCAR_DTYPE_BF16 (one more rounding) or OSCAR_DTYPE_F32, 16-byte aligned, not overlapping.
  * oscar_int4_decode_attention: softmax(q K^T / sqrt(d)) V over the values of all L tokens, as
- * oscar_bf16_decode_attention takes it (values below 2^100).  The current device must be the
- * cache's. */
+ * oscar_bf16_decode_attention takes it (values below 2^100).  Weights enter the product with the
+ * codes times their scale, each rounded to 11 bits, or by 2^-31 of a head's largest such product
+ * in the item where it is far below it.  The current device must be the cache's. */
 oscar_status oscar_int4_append(oscar_cache* cache, int layer, const void* k_new, const void* v_new, void* stream);
 oscar_status oscar_int4_read(oscar_cache* cache, int layer, int slot, int begin, int end, void* k_out, void* v_out,
                              int dtype, void* stream);

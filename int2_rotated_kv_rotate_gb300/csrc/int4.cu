@@ -6,10 +6,14 @@
 // loop).  Per 16 tokens, with mma.sync m16n8k16 (fp16 in, fp32 accumulate):
 //   scores  S[t, h] = sum_c code_K[t, c] q'[c, h]; q.k = s (q . code) + z sum(q) per group, in
 //           fp32.  q' is q (bf16, 8 bits) times a power of two of its head, exact in fp16;
-//   values  O[c, h] += sum_t code_V[c, t] P'[t, h], P' = p s_V / r (fp16), and sum_t p z_V in
-//           fp32.  r is a power of two no smaller than any scale so far (raised with O rescaled),
-//           so P' <= 1 at any magnitude of the values.  Its rounding to 11 bits is the one that
-//           the sums carry: 2^-12 of each token's share, where the output's own is up to 2^-8 of all.
+//   values  O[c, h] += sum_t code_V[c, t] P'[t, h], P' = p s_V u_h (fp16), and sum_t p z_V in
+//           fp32.  u_h makes the head's largest p s_V so far 64 or more: a token counts by what it adds, not
+//           by its scale, and one that is hardly attended costs the others nothing.  P' is rounded to 11
+//           bits, 2^-11 of each token's share (the output's own rounding: 2^-8 of all), or, where it is
+//           subnormal, by up to 2^-25, 2^-31 of the largest share.
+//           When the head's maximum rises, p s_V of what came before falls and u_h rises by as much, so O
+//           stands as it is; a half page with a scale above 65000 / u_h is looked through for its
+//           largest p s_V, and O rescaled if that needs another u_h.
 // A nibble masked in place (w & 0x000f000f, or << 4) is an fp16 subnormal, code * 2^-24 or 16 code *
 // 2^-24: one AND turns two codes into an MMA operand (one shift in four ANDs, and a byte permute in
 // four for the values, whose pairs are two tokens' codes of a channel).  The 16 is folded into q'
@@ -76,6 +80,14 @@ __device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, 
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Of u: the P' of the head's largest p s so far is kLeastPeak or more, no P' above kMostP (fp16 ends at
+// 65504), and u at most 2^113 (values below 2^-107 in all), so that its inverse is normal.
+constexpr float kLeastPeak = 64.f, kMostP = 65000.f, kMostUp = 1.0384593717069655e34f;
+__device__ __forceinline__ float rcp(float x) {  // at most 1 unit in the last place off
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     }
     // ---- the warp's half pages
     float m_run[2] = {-INFINITY, -INFINITY}, muse[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f}, zv[2][NG], oacc[8][4];
-    float r_inv = 8.507059173023462e37f, r = 1.1754943508222875e-38f;  // 2^126 and its inverse
+    float u[2] = {kMostUp, kMostUp};  // of this lane's two heads
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -319,44 +331,64 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           for (int g = 0; g < NG; ++g) top = fmaxf(top, bf16_lo(szv[b][i][g]));
         }
       float mloc[2];
-      bool over = top > r;
+      bool rise = false, over = top * fmaxf(u[0], u[1]) > kMostP;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         mloc[j] = fmaxf(fmaxf(lg[0][0][j], lg[0][NI - 1][j]), fmaxf(lg[1][0][j], lg[1][NI - 1][j]));
-        over |= mloc[j] > m_run[j];
+        rise |= mloc[j] > m_run[j];
       }
-      if (__any_sync(0xffffffffu, over)) {
-        float alpha[2];
+      if (__any_sync(0xffffffffu, rise || over)) {
+        if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-        for (int o = kLane0; o < 32; o <<= 1) {
-          mloc[0] = fmaxf(mloc[0], __shfl_xor_sync(0xffffffffu, mloc[0], o));
-          mloc[1] = fmaxf(mloc[1], __shfl_xor_sync(0xffffffffu, mloc[1], o));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          for (int o = kLane0; o < 32; o <<= 1) {
+            mloc[0] = fmaxf(mloc[0], __shfl_xor_sync(0xffffffffu, mloc[0], o));
+            mloc[1] = fmaxf(mloc[1], __shfl_xor_sync(0xffffffffu, mloc[1], o));
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mnew = fmaxf(m_run[j], mloc[j]);
+            muse[j] = mnew == -INFINITY ? 0.f : mnew;
+            const float alpha = ex2(m_run[j] - muse[j]);  // 0 while the reference was -inf
+            m_run[j] = mnew;
+            l_part[j] *= alpha;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) zv[j][g] *= alpha;
+            u[j] *= rcp(alpha);  // O stands as it is
+          }
+          over = top * fmaxf(u[0], u[1]) > kMostP || !(u[0] <= kMostUp) || !(u[1] <= kMostUp);
         }
-        float down = 1.f;
-        if (top > r) {  // (the lanes of a token have the same scales: uniform)
-          const float next = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x00800000u);  // < 2^126: finite
-          down = r * (1.f / next);
-          r = next;
-          r_inv = 1.f / next;
-        }
+        if (__any_sync(0xffffffffu, over)) {
+          float most[2] = {0.f, 0.f};  // of p s
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float mnew = fmaxf(m_run[j], mloc[j]);
-          muse[j] = mnew == -INFINITY ? 0.f : mnew;
-          alpha[j] = ex2(m_run[j] - muse[j]);  // 0 while the reference was -inf
-          m_run[j] = mnew;
-          l_part[j] *= alpha[j];
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) zv[j][g] *= alpha[j];
-          alpha[j] *= down;
-        }
+            for (int i = 0; i < NI; ++i) {
+              float s = bf16_lo(szv[b][i][0]);
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          oacc[f][0] *= alpha[0];
-          oacc[f][1] *= alpha[1];
-          oacc[f][2] *= alpha[0];
-          oacc[f][3] *= alpha[1];
+              for (int g = 1; g < NG; ++g) s = fmaxf(s, bf16_lo(szv[b][i][g]));
+#pragma unroll
+              for (int j = 0; j < 2; ++j) most[j] = fmaxf(most[j], ex2(lg[b][i][j] - muse[j]) * s);
+            }
+#pragma unroll
+          for (int o = kLane0; o < 32; o <<= 1) {
+            most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], o));
+            most[1] = fmaxf(most[1], __shfl_xor_sync(0xffffffffu, most[1], o));
+          }
+          float down[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // (a scale is below 2^124, so u above 2^-119)
+            const float next = fminf(fminf(u[j], kMostUp), kLeastPeak * rcp(fmaxf(most[j], kLeastPeak / kMostUp)));
+            down[j] = next * rcp(u[j]);  // 0 after inf
+            u[j] = next;
+          }
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            oacc[f][0] *= down[0];
+            oacc[f][1] *= down[1];
+            oacc[f][2] *= down[0];
+            oacc[f][3] *= down[1];
+          }
         }
       }
       // ---- values
@@ -373,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
         uint32_t bp[NG][2];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const float p0 = p[i][0] * r_inv, p1 = p[i][1] * r_inv;
+          const float p0 = p[i][0] * u[0], p1 = p[i][1] * u[1];
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float s = bf16_lo(szv[b][i][g]), z = bf16_hi(szv[b][i][g]);
@@ -446,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           wl[warp * G + head] = broken ? 0.f : l_part[j];
         }
         float* mine = wo + (warp * G + head) * kRow + 4 * gid;
+        const float r = rcp(u[j]);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
           // rows gid: 2^-24 a code; rows gid + 8: 2^-20
