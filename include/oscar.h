@@ -317,7 +317,9 @@ oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const vo
  * oscar_window_workspace_bytes for the current plan, _max_bytes for every plan (as captured
  * launches need it, which may be replayed under any later plan; q and out must then hold that
  * plan's queries).  Values of tokens that no
- * query attends are not used, and infinities and NaN reach only queries that attend them.  With
+ * query attends are not used, and infinities and NaN reach only queries that attend them: a query
+ * or key of NaN, or a score of +inf, makes the whole output NaN, a value its channel NaN or
+ * infinite (as in every decode of this library).  With
  * several queries a request, weights enter the product with the values as bf16; values below 2^78.
  * The current device must be the cache's. */
 oscar_status oscar_plan_window(oscar_cache* cache, const int* slots, const int* n_queries, int n_req, int n_sink,

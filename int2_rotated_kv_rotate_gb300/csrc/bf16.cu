@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(128, kBf16PerSM<NBUF>) bf16_split_kernel(Kerne
       const int c = threadIdx.x;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float r = acc.L[h] > 0.f ? acc.O[h] / acc.L[h] : 0.f;
+        const float r = merged(acc.L[h], acc.O[h]);
         out[(head0 + h) * kHeadDim + c] = bf16_rne(r);
         if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = r;
         if constexpr (WEIGHTS)
-          if (c == h) ml[head0 + h] = acc.L[h] > 0.f ? make_float2(acc.M[h], 1.f / acc.L[h]) : make_float2(0.f, 0.f);
+          if (c == h)  // (a denominator of NaN: nothing is added to the weights)
+            ml[head0 + h] = acc.L[h] > 0.f ? make_float2(acc.M[h], 1.f / acc.L[h]) : make_float2(0.f, 0.f);
       }
     }
     fence_proxy_async();  // generic use of the buffers is over before later bulk copies

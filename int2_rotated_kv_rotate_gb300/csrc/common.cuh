@@ -144,7 +144,8 @@ __device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(pa
 // ---------------------------------------------------------------- partial slots
 // The partial of one work item for the G heads of its kv group: float2 (m, l) per head
 // (m in log2 units, l the softmax denominator), then the normalised output o~ / l per head
-// and channel in fp32 (0 where l = 0).  fp16 here was measured to exceed the output
+// and channel in fp32 (0 where l = 0, which is how an item without weights is known: the
+// denominator of one that attends a NaN is NaN, whatever its m).  fp16 here was measured to exceed the output
 // tolerance on large values (its error is relative to the value).
 template <int G>
 struct PartialSlot {
@@ -157,7 +158,7 @@ struct PartialSlot {
 template <int G>
 __device__ __forceinline__ void store_slot(uint8_t* slot, int h, int c, float m, float l, float o) {
   if (c == 0) reinterpret_cast<float2*>(slot)[h] = make_float2(m, l);
-  reinterpret_cast<float*>(slot + PartialSlot<G>::kMlBytes)[h * kHeadDim + c] = l > 0.f ? o / l : 0.f;
+  reinterpret_cast<float*>(slot + PartialSlot<G>::kMlBytes)[h * kHeadDim + c] = l == 0.f ? 0.f : o / l;
 }
 
 // ---------------------------------------------------------------- BF16 rows on tensor cores
@@ -394,10 +395,10 @@ __device__ void bf16_rows_mma(RowK rowK, RowV rowV, int begin, int end, const fl
     float l = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float mw = wres[(w * G + h) * (kHeadDim + 2)];
-      if (mw == -INFINITY) continue;
-      const float a = ex2(mw - ms);
-      l = fmaf(a, wres[(w * G + h) * (kHeadDim + 2) + 1], l);
+      const float lw = wres[(w * G + h) * (kHeadDim + 2) + 1];
+      if (lw == 0.f) continue;
+      const float a = ex2(wres[(w * G + h) * (kHeadDim + 2)] - ms);
+      l = fmaf(a, lw, l);
       o = fmaf(a, wres[(w * G + h) * (kHeadDim + 2) + 2 + c], o);
     }
     store_slot<G>(part, h, c, ms, l, o);
@@ -425,6 +426,9 @@ struct MergeAcc {
   float M[HPT], L[HPT], O[HPT];  // running max (log2), sum of weights, weighted sum of o~ / l
 };
 
+// The output of a channel: the sums' quotient, NaN where the denominator is, 0 where nothing was attended.
+__device__ __forceinline__ float merged(float L, float O) { return L == 0.f ? 0.f : O / L; }
+
 // Online merge of n partial slots staged in shared memory into acc.
 template <int G, int NTH>
 __device__ void merge_slab(const uint8_t* slab, int n, MergeAcc<G, NTH>& acc) {
@@ -436,14 +440,14 @@ __device__ void merge_slab(const uint8_t* slab, int n, MergeAcc<G, NTH>& acc) {
     const int h = hb + A::kStride * q;
     float mx = acc.M[q];
     for (int i = 0; i < n; ++i) mx = fmaxf(mx, reinterpret_cast<const float2*>(slab + i * S)[h].x);
-    if (mx == -INFINITY) continue;  // nothing but empty partials so far
-    const float a = ex2(acc.M[q] - mx);  // acc.M = -inf gives 0
+    const float ref = mx == -INFINITY ? 0.f : mx;  // (-inf: partials that are empty or NaN)
+    const float a = ex2(acc.M[q] - ref);  // acc.M = -inf gives 0
     float L = acc.L[q] * a, O = acc.O[q] * a;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float2 ml = reinterpret_cast<const float2*>(slab + i * S)[h];
-      if (ml.x == -INFINITY) continue;
-      const float w = ex2(ml.x - mx) * ml.y;
+      if (ml.y == 0.f) continue;
+      const float w = ex2(ml.x - ref) * ml.y;
       L += w;
       O = fmaf(w, reinterpret_cast<const float*>(slab + i * S + PartialSlot<G>::kMlBytes)[h * kHeadDim + c], O);
     }

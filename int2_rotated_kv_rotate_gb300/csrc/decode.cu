@@ -250,7 +250,7 @@ __device__ void finish_output(const KernelParams& kp, const DecodeItem& it, cons
   float* os = reinterpret_cast<float*>(smem) + kHeadDim * kHeadDim;  // o~ [G][128]
   float* red = os + G * kHeadDim;                                      // [KS][G][128] partial sums
 #pragma unroll
-  for (int q = 0; q < HPT; ++q) os[(hb + KS * q) * kHeadDim + c] = acc.L[q] > 0.f ? acc.O[q] / acc.L[q] : 0.f;
+  for (int q = 0; q < HPT; ++q) os[(hb + KS * q) * kHeadDim + c] = merged(acc.L[q], acc.O[q]);
   const bool ok = mbar_wait(mbar, mphase);
   if (!ok) {
     if (t == 0) flag(kp, OSCAR_FLAG_TIMEOUT);
@@ -300,7 +300,7 @@ __device__ void finish_output_folded(const KernelParams& kp, const DecodeItem& i
 #pragma unroll
   for (int q = 0; q < HPT; ++q) {
     const int h = hb + KS * q;
-    const float v = acc.L[q] > 0.f ? acc.O[q] / acc.L[q] : 0.f;
+    const float v = merged(acc.L[q], acc.O[q]);
     out[(head0 + h) * kHeadDim + c] = bf16_rne(v);
     if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = v;
   }

@@ -498,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
       float l = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float mw = wm[w * G + h];
-        if (mw == -INFINITY) continue;
-        const float a = ex2(mw - ms);
-        l = fmaf(a, wl[w * G + h], l);
+        const float lw = wl[w * G + h];
+        if (lw == 0.f) continue;
+        const float a = ex2(wm[w * G + h] - ms);
+        l = fmaf(a, lw, l);
         o = fmaf(a, wo[(w * G + h) * kRow + c], o);
       }
       store_slot<G>(part, h, c, ms, l, o);
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
 #pragma unroll
       for (int i = 0; i < MergeAcc<G, kThreads>::HPT; ++i) {
         const int h = hb + MergeAcc<G, kThreads>::kStride * i;
-        const float o = acc.L[i] > 0.f ? acc.O[i] / acc.L[i] : 0.f;
+        const float o = merged(acc.L[i], acc.O[i]);
         out[(head0 + h) * kHeadDim + c] = bf16_rne(o);
         if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = o;
       }

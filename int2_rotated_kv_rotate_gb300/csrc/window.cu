@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(128, kRowsPerSM)
       const int c = threadIdx.x;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float r = acc.L[h] > 0.f ? acc.O[h] / acc.L[h] : 0.f;
+        const float r = merged(acc.L[h], acc.O[h]);
         out[(head0 + h) * kHeadDim + c] = bf16_rne(r);
         if (out_f32) out_f32[(head0 + h) * kHeadDim + c] = r;
       }
@@ -782,11 +782,12 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParam
         float mx = ml.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        if (mx == -INFINITY) continue;
         mx = fmaxf(mx, top);
-        const float old = ex2(top - mx);  // 0 at first
+        const float ref = mx == -INFINITY ? 0.f : mx;  // (-inf: parts that are empty or NaN)
+        const float old = ex2(top - ref);               // 0 at first
         top = mx;
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx) * ml.y;
+        const float f = ml.y == 0.f ? 0.f : ex2(ml.x - ref) * ml.y;
+        const unsigned some = __ballot_sync(0xffffffffu, ml.y != 0.f);
         float sum = f;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(KernelParam
           for (int i = 0; i < 8; ++i) {
             g[i] = __shfl_sync(0xffffffffu, f, (k + i) & 31);
             x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k + i < n && g[i] != 0.f)  // (a part without a visible token has no row)
+            if (k + i < n && ((some >> (k + i)) & 1u))  // (a part without a visible token has no row)
               x[i] = reinterpret_cast<const float4*>(slot + (k0 + k + i) * step + kBlockRows * 8)[r * (kHeadDim / 4) + lane];
             else g[i] = 0.f;
           }
