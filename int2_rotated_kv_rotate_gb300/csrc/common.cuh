@@ -82,6 +82,9 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
                : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Generic-proxy writes made visible to this thread (e.g. by an acquire) are ordered before
+// its later async-proxy (bulk copy) reads of global memory.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 
 // Ampere-style 16-byte asynchronous copy global -> shared; src_bytes = 0 zero-fills.
@@ -490,6 +493,7 @@ __device__ bool merge_partial(const KernelParams& kp, const DecodeItem& it, int 
     const int n = min(slab_slots, it.head_count - base);
     if (threadIdx.x == 0) {
       fence_proxy_async();
+      fence_proxy_async_global();  // the other CTAs' partials, seen through the acquire, before the copies
       mbar_expect_tx(slab_bar, uint32_t(n * S));
       bulk_g2s(smem_u32(slab), partials + size_t(it.head_first + base) * S, uint32_t(n * S), slab_bar);
     }
@@ -560,10 +564,6 @@ __device__ __forceinline__ bool wait_counter(const unsigned* ctr, unsigned expec
   }
   return false;
 }
-
-// Generic-proxy writes made visible to this thread (e.g. by an acquire) are ordered before
-// its later async-proxy (bulk copy) reads of global memory.
-__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // What `make` gives (positive, or a negative error) for the current device, made at its first
 // call there: a kernel's attributes and occupancy belong to a device.
