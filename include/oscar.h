@@ -263,8 +263,8 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const vo
  * those of oscar_rope (keys rounded to bf16) and the append after it, bit for bit.
  * k, v: the rows of the reservation [sum n_new][H_kv][d] bf16, any row and head strides >= 0 in
  * elements, channels contiguous (a fused projection's slices go in as they are).  q NULL, or
- * the queries of the same rows in bf16, as a tensor of oscar_rope (q->out may be q->in; no other
- * overlap of q->out with an input is allowed).  steps, rotary_dim (<= 128), magnitude: as for
+ * the queries of the same rows in bf16, as a tensor of oscar_rope (q->out may be q->in; any other
+ * overlap of q->out with q->in, k, v or positions is refused).  steps, rotary_dim (<= 128), magnitude: as for
  * oscar_rope; flags: OSCAR_ROPE_INTERLEAVED, OSCAR_ROPE_POSITIONS64.  positions [dev]: int32
  * (int64 with the flag), one a row, or NULL: a token's place in its request.  The current device
  * must be the cache's. */

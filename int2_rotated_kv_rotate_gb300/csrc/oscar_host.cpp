@@ -17,6 +17,7 @@
 
 #include "int4.cuh"
 #include "oscar_internal.h"
+#include "overlap.h"
 
 using namespace oscar;
 
@@ -980,9 +981,10 @@ oscar_status oscar_bf16_append(oscar_cache* c, int layer, const void* k_new, con
 
 // Bytes that a call's rows reach past its pointer, or -1: a stride or their sum is out of range.
 static long long rows_reach(long long n_rows, int n_heads, long long row, long long head, size_t size) {
+  if (row < 0 || head < 0) return -1;
   if (n_rows <= 0) return 0;
   const long long limit = 1LL << 46;
-  if (row < 0 || head < 0 || row > limit / n_rows || head > limit / n_heads) return -1;
+  if (row > limit / n_rows || head > limit / n_heads) return -1;
   return ((n_rows - 1) * row + (n_heads - 1) * head + kHeadDim) * (long long)size;
 }
 
@@ -1004,30 +1006,28 @@ oscar_status oscar_append_rotated(oscar_cache* c, int layer, const uint64_t* ste
   struct In {
     const char* name;
     uintptr_t at;
-    long long row, head, reach;
+    long long row, head;
     int heads;
   };
-  In in[3] = {{"k", reinterpret_cast<uintptr_t>(k->in), k->row, k->head, 0, c->cfg.n_kv_heads},
-              {"v", reinterpret_cast<uintptr_t>(v->in), v->row, v->head, 0, c->cfg.n_kv_heads},
-              {"q", 0, 0, 0, 0, 0}};
+  In in[3] = {{"k", reinterpret_cast<uintptr_t>(k->in), k->row, k->head, c->cfg.n_kv_heads},
+              {"v", reinterpret_cast<uintptr_t>(v->in), v->row, v->head, c->cfg.n_kv_heads},
+              {"q", 0, 0, 0, 0}};
   if (q) {
     if (q->n_heads < 1 || q->n_heads > 65536) return fail(OSCAR_ERR_INVALID_ARG, "q: %d heads", q->n_heads);
-    in[2] = {"q", reinterpret_cast<uintptr_t>(q->in), q->in_row, q->in_head, 0, q->n_heads};
+    in[2] = {"q", reinterpret_cast<uintptr_t>(q->in), q->in_row, q->in_head, q->n_heads};
   }
   for (In& x : in) {
     if (!x.heads) continue;
     if (n > 0 && !x.at) return fail(OSCAR_ERR_INVALID_ARG, "%s: NULL", x.name);
     if (x.at % 2) return fail(OSCAR_ERR_INVALID_ARG, "%s: not aligned to bf16", x.name);
-    x.reach = rows_reach(n, x.heads, x.row, x.head, 2);
-    if (x.row < 0 || x.head < 0 || x.reach < 0) return fail(OSCAR_ERR_INVALID_ARG, "%s: strides out of range", x.name);
+    if (rows_reach(n, x.heads, x.row, x.head, 2) < 0) return fail(OSCAR_ERR_INVALID_ARG, "%s: strides out of range", x.name);
   }
   auto vec = [](uintptr_t at, long long row, long long head) { return (at | uintptr_t(2 * row) | uintptr_t(2 * head)) % 16 == 0; };
   if (q) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(q->out);
     if (n > 0 && !at) return fail(OSCAR_ERR_INVALID_ARG, "q: NULL out");
     if (at % 2) return fail(OSCAR_ERR_INVALID_ARG, "q: out is not aligned to bf16");
-    const long long reach = rows_reach(n, q->n_heads, q->out_row, q->out_head, 2);
-    if (q->out_row < 0 || q->out_head < 0 || reach < 0) return fail(OSCAR_ERR_INVALID_ARG, "q: strides out of range");
+    if (rows_reach(n, q->n_heads, q->out_row, q->out_head, 2) < 0) return fail(OSCAR_ERR_INVALID_ARG, "q: strides out of range");
     // heads inside their row, or rows inside their head
     const bool rows_out = (q->n_heads == 1 || q->out_head >= kHeadDim) &&
                           (n <= 1 || q->out_row >= (q->n_heads - 1) * q->out_head + kHeadDim);
@@ -1045,6 +1045,16 @@ oscar_status oscar_append_rotated(oscar_cache* c, int layer, const uint64_t* ste
   const size_t pos_size = flags & OSCAR_ROPE_POSITIONS64 ? 8 : 4;
   if (reinterpret_cast<uintptr_t>(steps) % 8 || reinterpret_cast<uintptr_t>(positions) % pos_size)
     return fail(OSCAR_ERR_INVALID_ARG, "steps or positions are not aligned to their type");
+  if (q) {
+    // (rows that are still to be read must not be written)
+    const Pieces out = {reinterpret_cast<uintptr_t>(q->out), n, q->n_heads, 2 * q->out_row, 2 * q->out_head, 2 * kHeadDim};
+    for (const In& x : in)
+      if (!(&x == &in[2] && x.at == out.at) &&  // (in place)
+          share_bytes(out, {x.at, n, x.heads, 2 * x.row, 2 * x.head, 2 * kHeadDim}))
+        return fail(OSCAR_ERR_INVALID_ARG, "q: out overlaps %s", x.name);
+    if (positions && share_bytes(out, {reinterpret_cast<uintptr_t>(positions), n, 1, (long long)pos_size, 0, (long long)pos_size}))
+      return fail(OSCAR_ERR_INVALID_ARG, "q: out overlaps positions");
+  }
   oscar_status st = check_device(c);
   if (st) return st;
   p.k = k->in;
