@@ -7,13 +7,13 @@
 //   scores  S[t, h] = sum_c code_K[t, c] q'[c, h]; q.k = s (q . code) + z sum(q) per group, in
 //           fp32.  q' is q (bf16, 8 bits) times a power of two of its head, exact in fp16;
 //   values  O[c, h] += sum_t code_V[c, t] P'[t, h], P' = p s_V u_h (fp16), and sum_t p z_V in
-//           fp32.  u_h makes the head's largest p s_V so far 64 or more: a token counts by what it adds, not
-//           by its scale, and one that is hardly attended costs the others nothing.  P' is rounded to 11
-//           bits, 2^-11 of each token's share (the output's own rounding: 2^-8 of all), or, where it is
-//           subnormal, by up to 2^-25, 2^-31 of the largest share.
-//           When the head's maximum rises, p s_V of what came before falls and u_h rises by as much, so O
-//           stands as it is; a half page with a scale above 65000 / u_h is looked through for its
-//           largest p s_V, and O rescaled if that needs another u_h.
+//           fp32.  u_h, a power of two (weights of 1 stay exact), makes the head's largest p s_V so far 64
+//           or more: a token counts by what it adds, not by its scale, and one that is hardly attended
+//           costs the others nothing.  P' is rounded to 11 bits, 2^-11 of each token's share (the output's
+//           own rounding: 2^-8 of all), or, where it is subnormal, by up to 2^-25, 2^-31 of the
+//           largest share.
+//           u_h rises as the p s_V of what came before fall, when the head's maximum rises; a half page
+//           with a scale above 65000 / u_h is looked through for its largest p s_V.
 // A nibble masked in place (w & 0x000f000f, or << 4) is an fp16 subnormal, code * 2^-24 or 16 code *
 // 2^-24: one AND turns two codes into an MMA operand (one shift in four ANDs, and a byte permute in
 // four for the values, whose pairs are two tokens' codes of a channel).  The 16 is folded into q'
@@ -81,14 +81,17 @@ __device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, 
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// Of u: the P' of the head's largest p s so far is kLeastPeak or more, no P' above kMostP (fp16 ends at
-// 65504), and u at most 2^113 (values below 2^-107 in all), so that its inverse is normal.
-constexpr float kLeastPeak = 64.f, kMostP = 65000.f, kMostUp = 1.0384593717069655e34f;
+// The P' of the head's largest p s so far is kLeastPeak / 2 or more, none is above kMostP (fp16 ends at
+// 65504), and u at most 2^113 (values below 2^-106 in all), so that its inverse is normal.
+constexpr float kLeastPeak = 128.f, kMostP = 65000.f, kMostUp = 1.0384593717069655e34f;
 __device__ __forceinline__ float rcp(float x) {  // at most 1 unit in the last place off
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Of a normal x > 0: the power of two in [x / 2, x], and a power of two's inverse.
+__device__ __forceinline__ float pow2_floor(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 template <int G, int GROUP>
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
     }
     // ---- the warp's half pages
     float m_run[2] = {-INFINITY, -INFINITY}, muse[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f}, zv[2][NG], oacc[8][4];
-    float u[2] = {kMostUp, kMostUp};  // of this lane's two heads
+    float u[2] = {kMostUp, kMostUp};  // of this lane's two heads, before it is rounded down to a power of two
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -338,6 +341,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
         rise |= mloc[j] > m_run[j];
       }
       if (__any_sync(0xffffffffu, rise || over)) {
+        float down[2];  // of O
+#pragma unroll
+        for (int j = 0; j < 2; ++j) down[j] = pow2_inverse(pow2_floor(u[j]));
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
           for (int o = kLane0; o < 32; o <<= 1) {
@@ -353,9 +359,10 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
             l_part[j] *= alpha;
 #pragma unroll
             for (int g = 0; g < NG; ++g) zv[j][g] *= alpha;
-            u[j] *= rcp(alpha);  // O stands as it is
+            down[j] *= alpha;
+            u[j] = fminf(u[j] * rcp(alpha), kMostUp);
           }
-          over = top * fmaxf(u[0], u[1]) > kMostP || !(u[0] <= kMostUp) || !(u[1] <= kMostUp);
+          over = top * fmaxf(u[0], u[1]) > kMostP;
         }
         if (__any_sync(0xffffffffu, over)) {
           float most[2] = {0.f, 0.f};  // of p s
@@ -374,21 +381,18 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
             most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], o));
             most[1] = fmaxf(most[1], __shfl_xor_sync(0xffffffffu, most[1], o));
           }
-          float down[2];
+          // (a scale is below 2^124, so u above 2^-118)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            // (a scale is below 2^124, so u above 2^-119)
-            const float next = fminf(fminf(u[j], kMostUp), kLeastPeak * rcp(fmaxf(most[j], kLeastPeak / kMostUp)));
-            down[j] = next * rcp(u[j]);  // 0 after inf
-            u[j] = next;
-          }
+          for (int j = 0; j < 2; ++j) u[j] = fminf(u[j], kLeastPeak * rcp(fmaxf(most[j], kLeastPeak / kMostUp)));
+        }
 #pragma unroll
-          for (int f = 0; f < 8; ++f) {
-            oacc[f][0] *= down[0];
-            oacc[f][1] *= down[1];
-            oacc[f][2] *= down[0];
-            oacc[f][3] *= down[1];
-          }
+        for (int j = 0; j < 2; ++j) down[j] *= pow2_floor(u[j]);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          oacc[f][0] *= down[0];
+          oacc[f][1] *= down[1];
+          oacc[f][2] *= down[0];
+          oacc[f][3] *= down[1];
         }
       }
       // ---- values
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
         uint32_t bp[NG][2];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const float p0 = p[i][0] * u[0], p1 = p[i][1] * u[1];
+          const float p0 = p[i][0] * pow2_floor(u[0]), p1 = p[i][1] * pow2_floor(u[1]);
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float s = bf16_lo(szv[b][i][g]), z = bf16_hi(szv[b][i][g]);
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_split_kernel(KernelParams kp
           wl[warp * G + head] = broken ? 0.f : l_part[j];
         }
         float* mine = wo + (warp * G + head) * kRow + 4 * gid;
-        const float r = rcp(u[j]);
+        const float r = pow2_inverse(pow2_floor(u[j]));
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
           // rows gid: 2^-24 a code; rows gid + 8: 2^-20
