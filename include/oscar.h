@@ -265,7 +265,7 @@ oscar_status oscar_bf16_decode_attention(oscar_cache* cache, int layer, const vo
  * elements, channels contiguous (a fused projection's slices go in as they are).  q NULL, or
  * the queries of the same rows in bf16, as a tensor of oscar_rope (q->out may be q->in; any other
  * overlap of q->out with q->in, k, v or positions is refused).  steps, rotary_dim (<= 128), magnitude: as for
- * oscar_rope; flags: OSCAR_ROPE_INTERLEAVED, OSCAR_ROPE_POSITIONS64.  positions [dev]: int32
+ * oscar_rope (steps may be read before the kernel in front of this one has ended); flags: OSCAR_ROPE_INTERLEAVED, OSCAR_ROPE_POSITIONS64.  positions [dev]: int32
  * (int64 with the flag), one a row, or NULL: a token's place in its request.  The current device
  * must be the cache's. */
 typedef struct {
@@ -316,7 +316,8 @@ oscar_status oscar_int4_decode_attention(oscar_cache* cache, int layer, const vo
  * (before the rounding); all 16-byte aligned.  workspace [dev], 256-byte aligned, of
  * oscar_window_workspace_bytes for the current plan, _max_bytes for every plan (as captured
  * launches need it, which may be replayed under any later plan; q and out must then hold that
- * plan's queries).  Values of tokens that no
+ * plan's queries; a captured call holds the kernels of single and of several queries, whatever its
+ * own plan).  Values of tokens that no
  * query attends are not used, and infinities and NaN reach only queries that attend them: a query
  * or key of NaN, or a score of +inf, makes the whole output NaN, a value its channel NaN or
  * infinite (as in every decode of this library).  With

@@ -5,7 +5,8 @@
 // tokens) of an item, which bulk copies bring into stages of its own (no block barriers in the
 // loop).  Per 16 tokens, with mma.sync m16n8k16 (fp16 in, fp32 accumulate):
 //   scores  S[t, h] = sum_c code_K[t, c] q'[c, h]; q.k = s (q . code) + z sum(q) per group, in
-//           fp32.  q' is q (bf16, 8 bits) times a power of two of its head, exact in fp16;
+//           fp32.  q' is q (bf16, 8 bits) times a power of two of its head, exact in fp16 down to 2^-26 of
+//           the head's largest channel;
 //   values  O[c, h] += sum_t code_V[c, t] P'[t, h], P' = p s_V u_h (fp16), and sum_t p z_V in
 //           fp32.  u_h, a power of two (weights of 1 stay exact), makes the head's largest p s_V so far 64
 //           or more: a token counts by what it adds, not by its scale, and one that is hardly attended
@@ -25,8 +26,9 @@
 // tokens (B is 0 elsewhere), and both are added at the end.
 //
 // Bound by HBM at 136 bytes (group 128) or 160 (group 32) a token and kv-head, and near it by a warp's
-// latency over its half pages: 8 x 100000 tokens of 8 kv-heads, G = 4, 161 us (5.4 TB/s) and 195 us (5.3); G = 8
-// 177 and 225; one request of 32768 tokens 14 and 15.5 us.  A CTA alone on an SM runs at 0.6 of the rate of
+// latency over its half pages: 8 x 100000 tokens of 8 kv-heads, G = 4, 163 us (5.3 TB/s) and 195 to 198 us (5.2);
+// G = 8 177 and 227; one request of 32768 tokens 14.0 to 15.1 and 15.7 us.  Where every half page holds a scale far
+// above what is attended, 8 to 9 % more.  A CTA alone on an SM runs at 0.6 of the rate of
 // two; 128 registers leave no room for a third.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

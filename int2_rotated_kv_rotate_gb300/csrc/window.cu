@@ -33,8 +33,8 @@
 // Where few tiles would leave SMs idle, the plan cuts their pages into parts, whose partial results
 // window_merge_kernel joins, in a fixed order.
 //
-// Measured, G = 4, 8 kv-heads: 2048 queries behind 32768 tokens 783 to 789 us (1.36 PFLOP/s), 2 x 8192 queries
-// with windows of 4096 748 us (1.27; the tensor pipe is active 57 % of the time), 16 requests of 3 to 7 drafted tokens at
+// Measured, G = 4, 8 kv-heads: 2048 queries behind 32768 tokens 772 to 789 us (1.36 PFLOP/s), 2 x 8192 queries
+// with windows of 4096 744 to 749 us (1.27; the tensor pipe is active 57 % of the time), 16 requests of 3 to 7 drafted tokens at
 // G = 8 with windows of 2048 26 us.  A page and block takes some 650 cycles, its products 512.
 #include <cuda.h>
 #include <cuda_bf16.h>
