@@ -20,9 +20,9 @@ inline Pieces joined(Pieces p) {
   return p;
 }
 
-// a's pieces do not overlap: its heads lie inside their row, or its rows inside their head.  Constant time for
-// disjoint ranges and for slices of the same rows (a fused projection's), else a few steps for each of b's
-// pieces.
+// a's pieces do not overlap: its heads lie inside their row, or its rows inside their head.  For disjoint ranges
+// and for slices of the same rows (a fused projection's) no more than a few steps for each of b's heads, else
+// for each of its pieces.
 inline bool share_bytes(Pieces a, Pieces b) {
   a = joined(a);
   b = joined(b);
@@ -30,30 +30,40 @@ inline bool share_bytes(Pieces a, Pieces b) {
   if (a.at + uintptr_t(reach(a)) <= b.at || b.at + uintptr_t(reach(b)) <= a.at) return false;
   const long long d = (long long)(b.at - a.at);
   auto below = [](long long x, long long y) { return x / y - (x % y != 0 && x < 0); };  // floor(x / y), y > 0
-  if (a.heads == 1 && b.heads == 1 && (a.n == 1 || b.n == 1 || a.row == b.row)) {
-    // piece j of b is d + (j - i) stride bytes behind piece i of a: the first of these that ends behind its start
-    const long long stride = a.n > 1 ? a.row : b.row;
-    if (stride == 0) return true;  // one piece each, of overlapping ranges
-    long long k = below(-b.bytes - d, stride) + 1;
-    if (k < -(a.n - 1)) k = -(a.n - 1);
-    return k <= b.n - 1 && d + k * stride < a.bytes;
-  }
-  // a as groups of pieces, the wider stride outside
-  const bool rows_out = a.heads == 1 || a.row >= a.head * (a.heads - 1) + a.bytes;
-  const long long outer = rows_out ? a.row : a.head, inner = rows_out ? a.head : a.row;
-  const long long n_outer = rows_out ? a.n : a.heads, n_inner = rows_out ? a.heads : a.n;
-  const long long group = (n_inner - 1) * inner + a.bytes;
-  // the members i of [0, count), `size` bytes each every `stride`, that [x, x + bytes) meets: first .. last
+  // the members i of [0, count), `size` bytes each every `stride`, that [x, x + b.bytes) meets: first .. last
   auto range = [&](long long x, long long size, long long stride, long long count, long long* first, long long* last) {
     *first = stride ? below(x - size, stride) + 1 : x >= size;  // (i stride + size > x)
     *last = stride ? below(x + b.bytes - 1, stride) : (x + b.bytes > 0) - 1;
     if (*first < 0) *first = 0;
     if (*last > count - 1) *last = count - 1;
   };
+  long long i0, i1;
+  if (a.n == 1 || b.n == 1 || a.row == b.row) {
+    // Rows of one stride: row j of b begins d + (j - i) stride bytes behind row i of a.  The differences for
+    // which the rows' ranges meet:
+    const long long stride = a.n > 1 ? a.row : b.row;
+    const long long span_a = (a.heads - 1) * a.head + a.bytes, span_b = (b.heads - 1) * b.head + b.bytes;
+    long long k0 = stride ? below(-span_b - d, stride) + 1 : 0, k1 = stride ? below(span_a - 1 - d, stride) : 0;
+    if (k0 < -(a.n - 1)) k0 = -(a.n - 1);
+    if (k1 > b.n - 1) k1 = b.n - 1;
+    if (k1 - k0 < 8) {  // (rows whose heads lie far apart meet more of the others: below)
+      for (long long k = k0; k <= k1; ++k)
+        for (long long h = 0; h < b.heads; ++h) {
+          range(d + k * stride + h * b.head, a.bytes, a.head, a.heads, &i0, &i1);
+          if (i0 <= i1) return true;
+        }
+      return false;
+    }
+  }
+  // a as groups of pieces, the wider stride outside
+  const bool rows_out = a.heads == 1 || a.row >= a.head * (a.heads - 1) + a.bytes;
+  const long long outer = rows_out ? a.row : a.head, inner = rows_out ? a.head : a.row;
+  const long long n_outer = rows_out ? a.n : a.heads, n_inner = rows_out ? a.heads : a.n;
+  const long long group = (n_inner - 1) * inner + a.bytes;
   for (long long r = 0; r < b.n; ++r)
     for (long long h = 0; h < b.heads; ++h) {
       const long long x = d + r * b.row + h * b.head;
-      long long o0, o1, i0, i1;
+      long long o0, o1;
       range(x, group, outer, n_outer, &o0, &o1);
       for (long long o = o0; o <= o1; ++o) {
         range(x - o * outer, a.bytes, inner, n_inner, &i0, &i1);

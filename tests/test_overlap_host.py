@@ -84,3 +84,19 @@ def test_slices_of_a_projection(answers):
     # (a row from base - 2 k + x on begins at base + q + x)
     assert answers(cases) == [False, False, True, True, False, False, True, False, False]
     assert time.perf_counter() - t < 5
+
+
+def test_heads_apart_in_the_rows_of_a_projection(answers):
+    """Heads of 192 channels of which 128 are turned, their values behind: no slower for any number of rows."""
+    n, base = 1 << 30, 1 << 40
+    row = 64 * 384 + 16 * 384
+    out = (base, n, 64, row, 384, 256)
+    rest = (base + 256, n, 64, row, 384, 128)  # the channels between
+    k = (base + 64 * 384, n, 8, row, 384, 256)
+    cases = [(out, rest), (out, k), (out, (base + 255, n, 64, row, 384, 128)), (out, (base + 256, n, 64, row, 384, 129)),
+             (out, (base + 64 * 384 - 129, n, 8, row, 384, 256)), (out, (base - 16 * 384 - 128, n, 16, row, 384, 128)),
+             (out, (base - 16 * 384 + 1, n, 16, row, 384, 384))]
+    t = time.perf_counter()
+    # (a row from base - 16 x 384 + x on begins at base + 64 x 384 + x; the last ends 383 bytes past the next row's first)
+    assert answers(cases) == [False, False, True, True, True, False, True]
+    assert time.perf_counter() - t < 5
